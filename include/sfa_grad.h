@@ -70,7 +70,10 @@ typedef enum { SFA_LAYOUT_BSND = 0, SFA_LAYOUT_TND = 1 } sfa_layout;
 /* Device error word values (sfa_read_device_error). */
 #define SFA_DEVERR_NONE 0
 #define SFA_DEVERR_TIMEOUT 1  /* a kernel abandoned a pipeline wait after the wall-clock limit (no hang) */
-#define SFA_DEVERR_SEQLENS 2  /* TND lengths negative or not summing to T1/T2: every key was masked */
+#define SFA_DEVERR_SEQLENS 2  /* TND lengths negative or not summing to T1/T2: every key was masked; the
+                                 paged calls: lengths that do not fit the tokens or the block table */
+#define SFA_DEVERR_PAGE 3     /* the paged calls: a block table entry outside the cache */
+#define SFA_DEVERR_POSITION 4 /* sfa_cache_append: a token's position outside the rotation table */
 
 /*
  * Problem description (replaces the page's aclTensor shape metadata and the
@@ -300,6 +303,136 @@ sfa_status sfa_grad_host(const sfa_params* p, const void* q, const void* k, cons
                          const int32_t* act_seq_q, const int32_t* act_seq_kv, const void* q_rope, const void* k_rope,
                          void* dq, void* dk, void* dv, void* dq_rope, void* dk_rope, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ latent rows
+ *
+ * The rows around the attention.  norm_rope makes the attention's inputs from
+ * a layer's projections, and its gradient takes sfa_grad's outputs back to
+ * them; cache_append puts the same key rows into a paged cache, and paged_fwd
+ * is the attention of new tokens over that cache.
+ *
+ * A row of 512 is normalised to  y = x * rstd * w,  rstd = 1 / sqrt(mean x^2 +
+ * eps), and a row of 64 rotated by its token's position: with
+ * c = cos_sin[position][i] and s = cos_sin[position][32 + i], pair i (a, b)
+ * becomes (a c - b s, b c + a s).  Pair i is elements (2i, 2i + 1) when
+ * interleaved = 1 and (i, i + 32) when interleaved = 0.  Sums and products are
+ * in fp32, each output is rounded once.
+ *
+ * Shapes: q (T1,N1,512), q_rope (T1,N1,64), k (T1,512), k_rope (T1,64),
+ * positions int32 (T1,), cos_sin fp32 (table_len, 64), weights (512,) in
+ * dtype, rstd fp32 (T1,N1) and (T1,).
+ */
+typedef struct sfa_rows_params {
+  int32_t dtype;        /* element type of rows, weights and outputs */
+  int32_t interleaved;  /* 0 or 1: which elements form a rotated pair */
+  int64_t T1, N1;       /* tokens; query heads, 1..128 */
+  int64_t table_len;    /* rows of cos_sin */
+  double eps;           /* finite, >= 0 */
+} sfa_rows_params;
+
+/*
+ * Normalises k (and q) and rotates k_rope and q_rope in one launch.  Each of
+ * q, q_rope, k, k_rope may be null, and then its output and weight are ignored;
+ * q and k need their weights, the rope tensors positions and cos_sin.
+ * q_rstd / k_rstd (optional) receive what the gradient needs.  A token whose
+ * position lies outside the table is padding: its output rows and rstd are
+ * zero (positions null: no padding).  An output may be its own input.
+ * Asynchronous on `stream`; no workspace.
+ * Errors: SFA_ERR_NULLPTR (p, or a tensor that another one needs),
+ * SFA_ERR_PARAM_INVALID (dtype or interleaved out of range, a pointer that is
+ * not 16-byte aligned), SFA_ERR_SHAPE (sizes or eps out of range, table_len <
+ * 1 with rope tensors), SFA_ERR_RUNTIME.
+ */
+sfa_status sfa_norm_rope(const sfa_rows_params* p, const int32_t* positions, const float* cos_sin, const void* q,
+                         const void* q_weight, const void* q_rope, const void* k, const void* k_weight,
+                         const void* k_rope, void* q_out, void* q_rope_out, void* k_out, void* k_rope_out,
+                         float* q_rstd, float* k_rstd, void* stream);
+
+/*
+ * Gradients of sfa_norm_rope: from d_q, d_q_rope, d_k, d_k_rope (gradients of
+ * its outputs; each may be null, and then its results are ignored) to dq,
+ * dq_rope, dk, dk_rope and the weights' gradients dq_weight, dk_weight (fp32
+ * (512,), summed over every token and head in a fixed order: two calls give
+ * the same bits).  q, q_weight, q_rstd (k, ...) are the forward's and needed
+ * with d_q (d_k).  Padding tokens get zero rows and add nothing to the
+ * weights' gradients.  `workspace`: at least the size below, 256-byte aligned,
+ * scratch; two calls that may overlap need one each.
+ */
+sfa_status sfa_norm_rope_grad_workspace_size(const sfa_rows_params* p, size_t* bytes);
+sfa_status sfa_norm_rope_grad(const sfa_rows_params* p, const int32_t* positions, const float* cos_sin, const void* q,
+                              const void* q_weight, const float* q_rstd, const void* k, const void* k_weight,
+                              const float* k_rstd, const void* d_q, const void* d_q_rope, const void* d_k,
+                              const void* d_k_rope, void* dq, void* dq_rope, void* dk, void* dk_rope,
+                              float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * A paged cache of latent rows: num_pages pages of page_size tokens of 512 +
+ * Dr elements (the latent part, then the rotated part), contiguous.  Token j
+ * of sequence b is row j % page_size of page block_table[b][j / page_size];
+ * block_table is int32 (B, max_pages), of which only the entries of a
+ * sequence's tokens are read.
+ *
+ * The new tokens of a call are the last of their sequences: with lengths
+ * qlen and kvlen, token i has position kvlen - qlen + i.
+ *   BSND: q (B,S1,N1,512); qlen = act_seq_q[b] <= S1, or S1 where act_seq_q is
+ *         null.
+ *   TND:  q (T1,N1,512), sequence after sequence; act_seq_q int32 (B,), with
+ *         a sum of at most T1.
+ *   act_seq_kv int32 (B,): tokens in the cache, the new ones among them.
+ * Rows of q and of the outputs that belong to no sequence are neither read
+ * for a result nor written.
+ */
+typedef struct sfa_paged_params {
+  int32_t layout, dtype;
+  int64_t B, S1, T1;                      /* S1: BSND; T1: TND */
+  int64_t N1, D, Dr;                      /* 1..128; 512; 64 or 0 */
+  int64_t num_pages, page_size, max_pages; /* page_size: a multiple of 16, 16..1024 */
+  double scale;
+  int64_t sparse_mode;                    /* 0 (all kvlen keys) or 3 (keys up to the token's position) */
+  int32_t interleaved;                    /* sfa_cache_append */
+  int32_t wait_limit_us;                  /* sfa_paged_fwd; as in sfa_params */
+} sfa_paged_params;
+
+/*
+ * Appends the new tokens' rows to the cache: [k * rstd * k_weight || rotated
+ * k_rope] (k itself where k_weight is null), and, where q_rope is not null,
+ * rotates q_rope into q_rope_out (which may be q_rope) in the same launch.
+ * k (tokens, 512), k_rope (tokens, 64), q_rope (tokens, N1, 64).  With Dr = 0
+ * the rope tensors and cos_sin are ignored.  No two tokens share a row unless
+ * the block table names a page twice.  A token is left out when its sequence's
+ * lengths are negative, exceed the block table or its position is negative
+ * (SFA_DEVERR_SEQLENS), when its page lies outside the cache (SFA_DEVERR_PAGE)
+ * or its position outside the table (SFA_DEVERR_POSITION); `error` (optional,
+ * device int32) then receives the code, and is not written otherwise.
+ * scale, sparse_mode and wait_limit_us are not used.
+ */
+sfa_status sfa_cache_append(const sfa_paged_params* p, void* cache, const int32_t* block_table,
+                            const int32_t* act_seq_q, const int32_t* act_seq_kv, const void* k, const void* k_rope,
+                            const void* k_weight, double eps, const float* cos_sin, int64_t table_len,
+                            const void* q_rope, void* q_rope_out, int32_t* error, void* stream);
+
+/*
+ * Attention of the new tokens over the cache, keys and values from one latent
+ * row: with row_j = [c_j || r_j],
+ *   x_j = scale * ([q || q_rope] . row_j),  out = sum_j P_j c_j
+ * over the keys that sparse_mode leaves; softmax_max, softmax_sum fp32
+ * (tokens, N1) as sfa_fwd's.  A token with no key gets out = 0, softmax_max =
+ * -inf, softmax_sum = 0.  Rows of the cache past a sequence's kvlen are not
+ * used, whatever they hold.  P is formed relative to a running max and
+ * rounded once to dtype; the same call gives the same bits.  Capturable into a
+ * CUDA graph: the lengths and the block table are read on the device, when the
+ * graph runs.  `workspace` as for sfa_grad (two graphs or streams that may run
+ * at once need one each); its error word is rewritten by every call.  Lengths
+ * that are negative, exceed S1, T1 or the block table give
+ * SFA_DEVERR_SEQLENS, and no output is written; a block table entry outside
+ * the cache reads as rows of zeros and gives SFA_DEVERR_PAGE.
+ */
+sfa_status sfa_paged_workspace_size(const sfa_paged_params* p, size_t* bytes);
+sfa_status sfa_paged_fwd(const sfa_paged_params* p, const void* q, const void* q_rope, const void* cache,
+                         const int32_t* block_table, const int32_t* act_seq_q, const int32_t* act_seq_kv, void* out,
+                         float* softmax_max, float* softmax_sum, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 /*
  * Human-readable detail of the most recent SFA_ERR_RUNTIME returned on the

@@ -411,3 +411,7 @@ def read_device_error(workspace: torch.Tensor, stream=None) -> int:
         _check(lib().sfa_read_device_error(_ptr(workspace), _stream(stream), ctypes.byref(code)),
                "sfa_read_device_error")
     return code.value
+
+
+from .latent import (cache_append, make_paged_params, norm_rope, norm_rope_grad,  # noqa: E402
+                     norm_rope_grad_workspace_size, paged_fwd, paged_workspace_size)

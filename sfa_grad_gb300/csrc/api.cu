@@ -283,6 +283,10 @@ sfa_status fail(cudaError_t e, int line) {
 }  // namespace
 
 void set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
+int device_sm_count() { return sm_count(); }
+bool encode_map2d(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
+  return encode2d(m, f16, base, cols, rows, box_rows);
+}
 
 namespace {
 

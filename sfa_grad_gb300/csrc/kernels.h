@@ -1,6 +1,7 @@
 // Internal launcher declarations shared by the C-ABI host code and the kernels.
 #pragma once
 #include "common.cuh"
+#include "paged.cuh"
 
 namespace sfa {
 
@@ -92,6 +93,11 @@ cudaError_t launch_stats_combine(const Prob& p, const float* tile_stats, int nti
 
 // Records a message for sfa_last_error_message on the calling thread (api.cu).
 void set_last_error(const char* msg);
+// SMs of the current device (api.cu).
+int device_sm_count();
+// 2-D map of rows x cols 16-bit elements, boxes of 64 columns x box_rows rows
+// with 128-byte swizzle; false when the driver refuses it (api.cu).
+bool encode_map2d(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
 
 // Deterministic key-side reduction (det.cu): counting sort of the chunk's
 // (kv row, token, slot) entries by row (count, then launch_blk_scan over the
@@ -104,5 +110,62 @@ cudaError_t launch_det_sort(const Prob& p, const int* gbeg, const int* ngroups, 
                             cudaStream_t st);
 cudaError_t launch_det_reduce(const Prob& p, const int* groups, const int* gbeg, const int* ngroups, const int* ent,
                               const uint16_t* partials, float* acc, cudaStream_t st);
+
+// Workspaces that grow with the grid are sized for this many SMs, and grids
+// are cut to it.
+constexpr int kMaxSms = 160;
+
+// Norm and rotation of input rows (rows.cu).  Forward: q, k, qr, kr -> qo, ko,
+// qro, kro.  Gradient: dq, dk with q, k -> qo, ko and the weights' gradients;
+// qr, kr are then the rotated rows' gradients.
+struct RowsArgs {
+  const int* pos;        // (T) or null
+  const float* cs;       // (table_len, 64)
+  long long table_len;
+  const void *q, *qw, *qr, *k, *kw, *kr;
+  void *qo, *qro, *ko, *kro;
+  float *q_rstd, *k_rstd;
+  const void *dq, *dk;
+  float *dqw, *dkw, *part;
+  int T, G, interleaved;
+  float eps;
+  int blocks_k, blocks_q;   // set by the launchers
+};
+template <typename T>
+cudaError_t launch_norm_rope(RowsArgs a, cudaStream_t st);
+template <typename T>
+cudaError_t launch_norm_rope_grad(RowsArgs a, int nsm, cudaStream_t st);
+// Blocks (partial sums of dw) of the gradient over `rows` rows of 512.
+int norm_grad_blocks(long long rows, int nsm);
+
+// Append to the paged cache (append.cu).
+struct AppendArgs {
+  Paged pg;
+  void* cache;
+  const void *k, *kr, *kw, *qr;
+  void* qro;
+  const float* cs;       // null without rope
+  long long table_len;
+  int* error;            // or null
+  float eps;
+  int interleaved;
+  int blocks_k;          // set by the launcher
+};
+template <typename T>
+cudaError_t launch_append(AppendArgs a, cudaStream_t st);
+
+// Attention over the paged cache (paged.cu).
+struct PagedArgs {
+  Paged pg;
+  const void *q, *qr, *cache;
+  void* out;
+  float *smax, *ssum;
+  float scale;
+  unsigned long long wait_ns;
+  uint8_t* ws;
+};
+size_t paged_workspace(const Paged& p);
+template <typename T>
+cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st);
 
 }  // namespace sfa
