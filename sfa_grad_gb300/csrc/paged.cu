@@ -2,100 +2,927 @@
 //
 //   x_j = scale [q || q_rope] . row_j,  out = sum_j exp(x_j - m) row_j[:512] / l
 //
-// One warp a (token, head): q and the output row stay in registers, 16 + 2 and
-// 16 values a lane, the keys pass one by one with a running max and sum.
+// Query rows (token, head) are packed 128 to a row tile, keys pass in tiles of
+// 128 with a running max m and sum l.  A row tile belongs to a pair of CTAs
+// (one cluster), each with 64 of its rows: O needs 512 fp32 columns a row, so
+// 128 rows would fill the tensor memory of an SM and leave nothing for S,
+// while M = 64 on one SM runs at half rate.  With cta_group::2 and M = 128
+// both SMs run at full rate (64 clk an MMA of N = 256), O takes 256 columns of
+// 128 lanes (lanes 64..127 hold columns N/2.. of the same 64 rows), and each
+// SM stages only half of every B operand: the keys of its half of the tile for
+// S = Q K^T, its half of the features for O += P V.
+//
+// Work: every row tile counts its key tiles; the pairs split the total
+// evenly and in order, so a pair takes some whole row tiles and at most one
+// piece of a tile at each end.  Pieces leave (m, l, O) in fp32 and a second
+// kernel merges them in order: few rows over a long cache spread over all
+// SMs, and the result does not depend on timing.
+//
+// Warps of a CTA: 0 TMA loads, 1 S MMAs, 2 P V MMAs (both only in the pair's
+// first CTA), 3 the walk over the work, 4..7 softmax and epilogue.
 #include "kernels.h"
 #include "rows.cuh"
 
 namespace sfa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 256;
+constexpr int kTile = 128;                  // keys of a tile, rows of a row tile
+constexpr int kSlots = 8;                   // ring slots, two 64 x 64 panels each
+constexpr uint32_t kPanel = 8192;           // 64 rows of 128 bytes
+constexpr uint32_t kSlot = 2 * kPanel;
+constexpr uint32_t kOffP = 9 * kPanel;      // P: 64 rows x 128 keys
+constexpr uint32_t kOffRing = kOffP + 2 * kPanel;
+constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
+constexpr uint32_t kColS = 256;             // tensor memory: O, then two S tiles of 64 columns
+constexpr int kSegs = 4;                    // work descriptors in flight
+constexpr int kMinUnits = 2;                // key tiles a pair takes at least
+constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
+constexpr int kMaxPairs = kMaxSms / 2;
 
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) paged_kernel(PagedArgs a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int* err = reinterpret_cast<int*>(a.ws);
-  const Paged& p = a.pg;
-  // lengths: every warp checks all of them
+// One piece of work: key tiles kt0 .. kt1 - 1 of a row tile.
+struct Seg {
+  int seq, row0, nrows;   // rows of q, row0 the first
+  int i0;                 // first row's index in its sequence (token * heads + head)
+  int kt0, kt1;           // kt1 = 0: end of the work
+  int kend;               // keys any row sees
+  int base;               // mode 3: last key of the sequence's first new token; mode 0: of every token
+  int slot;               // -1: whole row tile; else where the piece's result goes
+};
+
+// A piece's place in the workspace, for the merge.
+struct Piece {
+  int valid, row0, nrows;
+  int first, last;        // begins / ends its row tile
+  int pad[3];
+};
+
+struct Ctl {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t qfull, qempty;
+  uint64_t sfull[2], sfree[2];
+  uint64_t pready, pfree, ofree, vloc[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t xch[2];
+  uint64_t settle[2];
+  Seg seg[kSegs];
+  float xbuf[2][128];
+  int scan[16];
+  long long scan64[16];
+  long long total_units;
+  long long start_off;    // units into the first sequence
+  int start_seq, start_row;
+  int bad, npairs;
+  uint32_t tmem;
+  int abort;
+  int issued, q_issued;   // ring slots and query tiles this CTA has loaded
+  int nclean, missing;    // value tiles loaded on vloc; bytes the last of them lacks
+  int own_mask;           // bit s: slot s was last loaded on vloc
+};
+
+constexpr uint32_t kSmem = kOffCtl + sizeof(Ctl) + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+static_assert(kSmem > kOneCtaSmem, "one CTA an SM: it allocates all of tensor memory");
+
+// ------------------------------------------------------------------ cluster
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Cluster-window address of `a` in CTA `rank` of the pair.
+__device__ __forceinline__ uint32_t map_to(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ int load_from(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+// Bounded wait whose acquire covers both CTAs of the pair.
+template <bool POLL>
+__device__ __forceinline__ bool pair_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if (POLL)
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, "
+        "p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, "
+        "0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(10000u)
+        : "memory");
+  return ok != 0;
+}
+template <bool POLL = false>
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, const Waiter& w) {
+  const uint32_t a = smem_u32(bar);
+  if (pair_test<POLL>(a, parity)) return true;
+  const unsigned long long t0 = gtime_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (pair_test<POLL>(a, parity)) return true;
+    if (!POLL || (it & 31u) == 0) {
+      if (*w.abort) return false;
+      if (gtime_ns() - t0 > w.limit_ns) break;
+    }
+  }
+  *w.abort = 1;
+  atomicExch(w.gerr, kErrTimeout);
+  return false;
+}
+
+// ------------------------------------------------------------------ tensor cores, both SMs of the pair
+template <uint32_t SA, uint32_t SB>
+__device__ __forceinline__ void pair_mma_k64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc_first) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %5, %6, %3, 1;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %7, %8, %3, 1;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %9, %10, %3, 1;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc_first), "l"(a + SA), "l"(b + SB), "l"(a + 2 * SA), "l"(b + 2 * SB),
+      "l"(a + 3 * SA), "l"(b + 3 * SB)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once this thread's MMAs so far are complete.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// ... of this CTA only.
+__device__ __forceinline__ void pair_commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// One 64-column box into this CTA's shared memory; the bytes count on `bar`, a
+// barrier of either CTA (cluster address).
+__device__ __forceinline__ void pair_tma(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ the work
+// Row tile j of a sequence: keys its last row sees, and its key tiles (at
+// least one: a tile without keys still writes its rows).
+struct SeqWork {
+  int qlen, kvlen, rows, tiles;
+};
+__device__ __forceinline__ SeqWork seq_work(const Paged& p, int b) {
+  SeqWork s;
+  s.qlen = p.act_q ? __ldg(p.act_q + b) : p.S1;
+  s.kvlen = __ldg(p.act_kv + b);
+  s.rows = s.qlen * p.G;
+  s.tiles = (s.rows + kTile - 1) / kTile;
+  return s;
+}
+__device__ __forceinline__ int tile_keys(const Paged& p, const SeqWork& s, int j) {
+  if (p.mode == 0) return s.kvlen;
+  const int tok = min((j + 1) * kTile - 1, s.rows - 1) / p.G;
+  return max(0, s.kvlen - s.qlen + tok + 1);
+}
+__device__ __forceinline__ int tile_units(const Paged& p, const SeqWork& s, int j) {
+  return max(1, (tile_keys(p, s, j) + kTile - 1) / kTile);
+}
+// Key tiles of row tiles 0 .. n-1, n < tiles (mode 3).  Tile j ends at token
+// (128 j + 127) / G, so its units are max(1, (j + e) / G) rounded down with
+// e = (127 + G (base + 128)) / 128 rounded down: ones while j + e < 2 G, then
+// a sum over i / G.
+__device__ __forceinline__ long long units_before(const Paged& p, const SeqWork& s, int n) {
+  if (n <= 0) return 0;
+  if (p.mode == 0) return (long long)n * max(1, (s.kvlen + kTile - 1) / kTile);
+  const long long x = 127 + (long long)p.G * (s.kvlen - s.qlen + kTile);
+  const long long e = x >> 7;
+  const long long ones = min((long long)n, max(0LL, 2LL * p.G - e));
+  auto sum = [&](long long m) {   // sum of i / G over i < m
+    const long long q = (long long)((unsigned)m / (unsigned)p.G), r = m - q * p.G;
+    return (long long)p.G * (q * (q - 1) / 2) + q * r;
+  };
+  return ones + (ones < n ? sum(n + e) - sum(ones + e) : 0);
+}
+__device__ __forceinline__ long long seq_units(const Paged& p, const SeqWork& s) {
+  return s.tiles ? units_before(p, s, s.tiles - 1) + tile_units(p, s, s.tiles - 1) : 0;
+}
+
+// Block-wide: checks the lengths, sums the work, and finds where this pair's
+// share begins.
+__device__ void plan_work(const Paged& p, Ctl* c, int pair, int max_pairs) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  long long units = 0, toks = 0;
   bool bad = false;
-  long long total = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const int q = p.act_q ? __ldg(p.act_q + b) : p.S1, kv = __ldg(p.act_kv + b);
-    bad |= q < 0 || kv < 0 || (!p.tnd && q > p.S1) || kv > (long long)p.max_pages * p.page_size;
-    total += q;
+  for (int b = b0; b < b1; ++b) {
+    const SeqWork s = seq_work(p, b);
+    const bool no = s.qlen < 0 || s.kvlen < 0 || s.qlen > (p.tnd ? p.T : p.S1) ||
+                    s.kvlen > (long long)p.max_pages * p.page_size;
+    bad |= no;
+    if (!no) units += seq_units(p, s), toks += s.qlen;
   }
+  // inclusive scans over the block's threads
+  long long u = units, t = toks;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-  bad |= p.tnd && total > p.T;
-  if (__any_sync(~0u, bad)) {
-    *err = kErrSeqLens;
-    return;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long du = __shfl_up_sync(~0u, u, o), dt = __shfl_up_sync(~0u, t, o);
+    if (lane >= o) u += du, t += dt;
   }
-  const long long item = (long long)blockIdx.x * kWarps + warp;
-  if (item >= (long long)p.T * p.G) return;
-  const int t = (int)(item / p.G);
-  const SeqTok s = find_token(p, t);
-  if (s.seq < 0) return;
-  const int kv = __ldg(p.act_kv + s.seq);
-  const long long keys = p.mode == 3 ? min((long long)kv, (long long)kv - s.qlen + s.i + 1) : kv;
-  float q[16], qr[2] = {0.f, 0.f}, o[16], m = -INFINITY, l = 0.f;
-  load_row512((const T*)a.q + (size_t)item * 512, lane, q);
-  if (p.row == 576) {
-    const T* r = (const T*)a.qr + (size_t)item * 64 + 2 * lane;
-    qr[0] = Elt<T>::to_f(r[0]);
-    qr[1] = Elt<T>::to_f(r[1]);
+  if (lane == 31) c->scan64[w] = u, c->scan64[8 + w] = t;
+  const bool any = __syncthreads_or(bad);
+  long long total = 0, toks_all = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < w) u += c->scan64[i], t += c->scan64[8 + i];
+    total += c->scan64[i];
+    toks_all += c->scan64[8 + i];
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  const int* table = p.table + (size_t)s.seq * p.max_pages;
-  for (long long j = 0; j < keys; ++j) {
-    const int page = __ldg(table + j / p.page_size);
-    float c[16], r[2] = {0.f, 0.f};
-    if (page < 0 || page >= p.num_pages) {
-      *err = kErrPage;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) c[i] = 0.f;
-    } else {
-      const T* row = (const T*)a.cache + ((size_t)page * p.page_size + j % p.page_size) * p.row;
-      load_row512(row, lane, c);
-      if (p.row == 576) {
-        r[0] = Elt<T>::to_f(row[512 + 2 * lane]);
-        r[1] = Elt<T>::to_f(row[513 + 2 * lane]);
+  const bool wrong = any || (p.tnd && toks_all > p.T);
+  const long long n = (total + kMinUnits - 1) / kMinUnits;
+  const int np = n < 1 ? 1 : n < max_pairs ? (int)n : max_pairs;
+  if (tid == 0) {
+    c->bad = wrong;
+    c->total_units = total;
+    c->npairs = np;
+    c->start_seq = -1;
+  }
+  __syncthreads();
+  const long long u0 = total * pair / np;
+  if (!wrong && pair < np && u0 >= u - units && u0 < u) {
+    long long at = u - units, row = t - toks;
+    for (int b = b0; b < b1; ++b) {
+      const SeqWork s = seq_work(p, b);
+      const long long k = seq_units(p, s);
+      if (u0 < at + k) {
+        c->start_seq = b;
+        c->start_off = u0 - at;
+        c->start_row = (int)row;
+        break;
+      }
+      at += k;
+      row += s.qlen;
+    }
+  }
+  __syncthreads();
+}
+
+// The first piece's row tile: the last j with units_before(j) <= off; all
+// lanes of a warp search together.
+__device__ __forceinline__ int find_tile(const Paged& p, const SeqWork& s, long long off) {
+  int lo = 0, hi = s.tiles;   // units_before(lo) <= off < units_before(hi)
+  const int lane = threadIdx.x & 31;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 32) / 33;
+    const int j = lo + (lane + 1) * step;
+    const unsigned ok = __ballot_sync(~0u, j < hi && units_before(p, s, j) <= off);
+    const int n = __popc(ok);   // a prefix of the lanes
+    lo += n * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+struct Args {
+  PagedArgs a;
+  int max_pairs, box;      // box: rows of a cache box (16, 32 or 64)
+  int* status;             // one word a CTA
+  Piece* piece;
+  float2* stats;           // (slot, row) x {m, l}
+  float* part;             // (slot, row, 512)
+};
+
+struct Maps2 {
+  CUtensorMap q, qr, kv;   // boxes of 64 columns; kv: box rows = Args::box
+};
+
+template <typename T, bool ROPE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    paged_kernel(const __grid_constant__ Maps2 maps, const Args args) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  Ctl* c = reinterpret_cast<Ctl*>(sm + kOffCtl);
+  const Paged& p = args.a.pg;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cta_rank();
+  const int pair = blockIdx.x >> 1;
+  const bool leader = rank == 0;
+  constexpr int kKSlots = ROPE ? 5 : 4;       // ring slots of a tile's keys (S), 4 more for its values
+  constexpr int kPer = kKSlots + 4;
+  int* status = args.status + blockIdx.x;
+
+  if (tid == 0) {
+    *status = 0;
+    c->abort = 0;
+    c->issued = 0;
+    c->q_issued = 0;
+    c->own_mask = 0;
+    c->nclean = 0;
+    c->missing = 0;
+    for (int i = 0; i < kSlots; ++i) mbar_init(&c->full[i], 1), mbar_init(&c->empty[i], 1);
+    mbar_init(&c->qfull, 1);
+    mbar_init(&c->qempty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->sfull[i], 1);
+      mbar_init(&c->sfree[i], 8);
+      mbar_init(&c->xch[i], 2);
+      mbar_init(&c->settle[i], 1);
+      mbar_init(&c->vloc[i], 1);
+    }
+    mbar_init(&c->pready, 8);
+    mbar_init(&c->pfree, 1);
+    mbar_init(&c->ofree, 8);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], leader ? 7 : 5);
+    mbar_fence_init();
+  }
+  if (warp == 3) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  plan_work(p, c, pair, args.max_pairs);   // with block barriers
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem;
+  const Waiter w{&c->abort, status, args.a.wait_ns};
+  const bool work = c->start_seq >= 0;
+  const long long u0 = c->total_units * pair / c->npairs, u1 = c->total_units * (pair + 1) / c->npairs;
+  const int ntiles = work ? (int)(u1 - u0) : 0;
+  // ring position of tile n's first key slot and value slot: K(0) K(1) V(0)
+  // K(2) V(1) ... K(N-1) V(N-2) V(N-1)
+  auto kpos = [&](int n) { return n == 0 ? 0 : kKSlots + (n - 1) * kPer; };
+  auto vpos = [&](int n) { return kpos(n + 1) + (n + 1 < ntiles ? kKSlots : 0); };
+  const uint32_t ring = smem_u32(sm + kOffRing), lead = 0;
+
+  if (tid == 0 && leader) {
+    // a piece at the beginning, a piece at the end: none until the walk says so
+    args.piece[2 * pair].valid = 0;
+    args.piece[2 * pair + 1].valid = 0;
+  }
+  if (c->bad && tid == 0) *status = kErrSeqLens;
+  __syncthreads();
+
+  if (work && warp == 3) {
+    // ---------------------------------------------------------------- the walk
+    int b = c->start_seq;
+    long long left = u1 - u0;
+    SeqWork s = seq_work(p, b);
+    int j = find_tile(p, s, c->start_off);
+    int kt = (int)(c->start_off - units_before(p, s, j));
+    int row = p.tnd ? c->start_row * p.G : b * p.S1 * p.G;   // first row of the sequence
+    for (int n = 0;; ++n) {
+      Seg g;
+      g.kt1 = 0;
+      if (left > 0) {
+        while (j >= s.tiles) {
+          row += (p.tnd ? s.qlen : p.S1) * p.G;
+          s = seq_work(p, ++b);
+          j = 0;
+        }
+        const int units = tile_units(p, s, j);
+        g.seq = b;
+        g.row0 = row + j * kTile;
+        g.i0 = j * kTile;
+        g.nrows = min(kTile, s.rows - g.i0);
+        g.kt0 = kt;
+        g.kt1 = (int)min((long long)units, kt + left);
+        g.kend = tile_keys(p, s, j);
+        g.base = p.mode == 3 ? s.kvlen - s.qlen : s.kvlen - 1;
+        g.slot = g.kt0 == 0 && g.kt1 == units ? -1 : n == 0 ? 2 * pair : 2 * pair + 1;
+        left -= g.kt1 - g.kt0;
+        if (g.slot >= 0 && leader && lane == 0)
+          args.piece[g.slot] = Piece{1, g.row0, g.nrows, g.kt0 == 0, g.kt1 == units, {0, 0, 0}};
+        kt = 0;
+        ++j;
+      }
+      const int r = n % kSegs;
+      if (n >= kSegs && !mbar_wait(&c->seg_empty[r], (n / kSegs - 1) & 1, w)) break;
+      if (lane == 0) {
+        c->seg[r] = g;
+        mbar_arrive(&c->seg_full[r]);
+      }
+      if (g.kt1 == 0) break;
+    }
+  } else if (work && warp == 0) {
+    // ---------------------------------------------------------------- TMA loads
+    const int nb = 64 / args.box;                   // boxes of 64 rows
+    const int none = p.num_pages * p.page_size;     // a row outside the map: zeros
+    const uint32_t full0 = map_to(smem_u32(&c->full[0]), lead), qfull = map_to(smem_u32(&c->qfull), lead);
+    int use = 0, nclean = 0;
+    bool ok = true;
+    // lane l < 2 nb: cache row of the tile's box l
+    auto boxes = [&](const Seg& g, int kt) {
+      int y = none;
+      const int key = kt * kTile + lane * args.box;
+      if (lane < 2 * nb && key < g.kend) {
+        const int page = __ldg(p.table + (size_t)g.seq * p.max_pages + key / p.page_size);
+        if (page >= 0 && page < p.num_pages)
+          y = page * p.page_size + key % p.page_size;
+        else
+          *status = kErrPage;
+      }
+      return y;
+    };
+    auto take = [&]() {   // the next slot, free
+      const int s = use % kSlots;
+      if (use >= kSlots && !pair_wait(&c->empty[s], (use / kSlots - 1) & 1, w)) ok = false;
+      return s;
+    };
+    auto load_slot = [&](int y, int box0, int x, int panels, uint32_t bar) {
+      const int s = use % kSlots, pn = lane / nb, bx = lane - pn * nb;
+      const int yy = __shfl_sync(~0u, y, box0 + bx);
+      if (pn < panels)
+        pair_tma(ring + s * kSlot + pn * kPanel + bx * args.box * 128, &maps.kv, x + pn * 64, yy, bar);
+    };
+    // values of a tile; where a row of keys is masked for some query row, the
+    // softmax warps clean them first, so they land on this CTA's own barrier
+    auto load_v = [&](const Seg& g, int kt, int y) {
+      const bool clean = (kt + 1) * kTile > (p.mode == 3 ? g.base + g.i0 / p.G : g.base) + 1;
+      for (int i = 0; i < 4 && ok; ++i) {
+        const int s = take();
+        if (!ok) break;
+        uint32_t bar = full0 + s * 8;
+        if (clean) {
+          bar = smem_u32(&c->vloc[nclean & 1]);
+          if (lane == 0) {
+            if (i == 0) mbar_expect_tx(&c->vloc[nclean & 1], 4 * kSlot);
+            if (leader) mbar_arrive(&c->full[s]);
+          }
+        } else if (leader && lane == 0) {
+          mbar_expect_tx(&c->full[s], 2 * kSlot);
+        }
+        __syncwarp();
+        load_slot(y, (i >> 1) * nb, (int)rank * 256 + (i & 1) * 128, 2, bar);
+        if (lane == 0) {
+          c->own_mask = clean ? c->own_mask | 1 << s : c->own_mask & ~(1 << s);
+          if (clean && i == 0) c->nclean = nclean + 1;
+          if (clean) c->missing = (3 - i) * kSlot;
+        }
+        ++use;
+      }
+      nclean += clean;
+    };
+    Seg prev;
+    int prev_kt = 0, prev_y = 0;
+    bool have = false;
+    int qn = 0;
+    for (int n = 0; ok; ++n) {
+      const int r = n % kSegs;
+      if (!mbar_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
+      const Seg g = c->seg[r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->seg_empty[r]);
+      if (g.kt1 == 0) break;
+      int y = boxes(g, g.kt0);
+      // the query rows, once the segment before has done its products
+      if (qn > 0 && !pair_wait(&c->qempty, (qn - 1) & 1, w)) break;
+      if (leader && lane == 0) mbar_expect_tx(&c->qfull, 2 * (8 + ROPE) * kPanel);
+      __syncwarp();
+      if (lane < 8 + ROPE)
+        pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64, g.row0 + rank * 64,
+                 qfull);
+      ++qn;
+      if (lane == 0) c->q_issued = qn;
+      for (int kt = g.kt0; kt < g.kt1 && ok; ++kt) {
+        const int ynext = kt + 1 < g.kt1 ? boxes(g, kt + 1) : none;   // in flight during the waits
+        for (int i = 0; i < kKSlots && ok; ++i) {
+          const int s = take();
+          if (!ok) break;
+          const int panels = i < 4 ? 2 : 1;
+          if (leader && lane == 0) mbar_expect_tx(&c->full[s], 2 * panels * kPanel);
+          __syncwarp();
+          load_slot(y, (int)rank * nb, i * 128, panels, full0 + s * 8);
+          if (lane == 0) c->own_mask &= ~(1 << s);
+          ++use;
+        }
+        if (have && ok) load_v(prev, prev_kt, prev_y);
+        prev = g;
+        prev_kt = kt;
+        prev_y = y;
+        have = true;
+        y = ynext;
       }
     }
-    float d = q[0] * c[0];
+    if (have && ok && !*w.abort) load_v(prev, prev_kt, prev_y);
+    if (lane == 0) c->issued = use;
+    // the ring's last releases and the last query release have arrived: none
+    // is on its way to a CTA that has ended
+    if (!*w.abort) {
+      for (int u = max(0, use - kSlots); u < use; ++u)
+        if (!pair_wait(&c->empty[u % kSlots], (u / kSlots) & 1, w)) break;
+      if (qn > 0) pair_wait(&c->qempty, (qn - 1) & 1, w);
+    }
+  } else if (work && leader && warp == 1 && lane == 0) {
+    // ---------------------------------------------------------------- S = Q K^T
+    constexpr uint32_t id = idesc_f16(kTile, kTile, Elt<T>::is_f16, false, false);
+    const uint64_t dq = sdesc_kmajor(smem_u32(sm), 0), dk = sdesc_kmajor(ring, 0);
+    int tile = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int r = n % kSegs;
+      if (!mbar_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
+      const int len = c->seg[r].kt1 - c->seg[r].kt0;
+      const bool end = c->seg[r].kt1 == 0;
+      mbar_arrive(&c->seg_empty[r]);
+      if (end) break;
+      if (!(ok = pair_wait<true>(&c->qfull, n & 1, w))) break;
+      for (int t = 0; t < len && ok; ++t, ++tile) {
+        const int buf = tile & 1;
+        if (tile >= 2 && !(ok = pair_wait<true>(&c->sfree[buf], (tile / 2 - 1) & 1, w))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + kColS + buf * 64;
+        int use = kpos(tile);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) d = fmaf(q[i], c[i], d);
-    d = fmaf(qr[0], r[0], fmaf(qr[1], r[1], d));
-    const float x = warp_sum(d) * a.scale;
-    const float top = fmaxf(m, x);
-    const float f = m == top ? 1.f : ex2((m - top) * kLog2e), e = x == top ? 1.f : ex2((x - top) * kLog2e);
-    l = l * f + e;
-    m = top;
+        for (int i = 0; i < kKSlots; ++i, ++use) {
+          const int s = use % kSlots;
+          if (!(ok = pair_wait<true>(&c->full[s], (use / kSlots) & 1, w))) break;
+          tc_fence_after();
+          const uint64_t a = dq + desc_off(2 * i * kPanel), b = dk + desc_off(s * kSlot);
+          pair_mma_k64<2, 2>(d, a, b, id, i > 0);
+          if (i < 4) pair_mma_k64<2, 2>(d, a + desc_off(kPanel), b + desc_off(kPanel), id, 1);
+          pair_commit(&c->empty[s]);
+        }
+        if (ok) pair_commit(&c->sfull[buf]);
+      }
+      if (ok) pair_commit(&c->qempty);
+    }
+    if (*w.abort) {
+      pair_commit_own(&c->settle[0]);
+      mbar_settle(&c->settle[0], 0, status);
+    }
+  } else if (work && leader && warp == 2 && lane == 0) {
+    // ---------------------------------------------------------------- O += P V
+    constexpr uint32_t id = idesc_f16(kTile, 256, Elt<T>::is_f16, false, true);
+    const uint64_t dp = sdesc_kmajor(smem_u32(sm + kOffP), 0), dv = sdesc_mnmajor(ring, 0, 64);
+    int tile = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int r = n % kSegs;
+      if (!mbar_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
+      const int len = c->seg[r].kt1 - c->seg[r].kt0;
+      const bool end = c->seg[r].kt1 == 0;
+      mbar_arrive(&c->seg_empty[r]);
+      if (end) break;
+      if (n > 0 && !(ok = pair_wait<true>(&c->ofree, (n - 1) & 1, w))) break;
+      for (int t = 0; t < len && ok; ++t, ++tile) {
+        if (!(ok = pair_wait<true>(&c->pready, tile & 1, w))) break;
+        tc_fence_after();
+        int use = vpos(tile);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = o[i] * f + e * c[i];
+        for (int i = 0; i < 4; ++i, ++use) {
+          const int s = use % kSlots;
+          if (!(ok = pair_wait<true>(&c->full[s], (use / kSlots) & 1, w))) break;
+          tc_fence_after();
+          pair_mma_k64<2, 128>(tmem + (i & 1) * 128, dp + desc_off((i >> 1) * kPanel), dv + desc_off(s * kSlot), id,
+                               t > 0 || i > 1);
+          pair_commit(&c->empty[s]);
+        }
+        if (ok) pair_commit(&c->pfree);
+      }
+    }
+    if (*w.abort) {
+      pair_commit_own(&c->settle[1]);
+      mbar_settle(&c->settle[1], 0, status);
+    }
+  } else if (work && warp >= 4) {
+    // ---------------------------------------------------------------- softmax, epilogue
+    // Thread: row r of this CTA's 64, keys 64 h .. 64 h + 63 of a tile, and
+    // features 256 h .. 256 h + 255 of O.
+    const int l = tid - 128, r = l & 63, h = l >> 6, wq = warp & 3;
+    const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t prow = smem_u32(sm + kOffP) + h * kPanel + r * 128;
+    const uint32_t pready = map_to(smem_u32(&c->pready), lead), ofree = map_to(smem_u32(&c->ofree), lead);
+    const uint32_t sfree0 = map_to(smem_u32(&c->sfree[0]), lead);
+    uint64_t* xch = &c->xch[wq & 1];
+    const float cs = args.a.scale * kLog2e;
+    int tile = 0, nx = 0, nbound = 0;
+    // exchange of one value with the thread of the row's other half
+    auto swap = [&](float v, float* o) {
+      c->xbuf[nx & 1][l] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xch);
+      if (!mbar_wait(xch, nx & 1, w)) return false;
+      *o = c->xbuf[nx & 1][l ^ 64];
+      ++nx;
+      return true;
+    };
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int sr = n % kSegs;
+      if (!mbar_wait(&c->seg_full[sr], (n / kSegs) & 1, w)) break;
+      const Seg g = c->seg[sr];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->seg_empty[sr]);
+      if (g.kt1 == 0) break;
+      const int myrow = (int)rank * 64 + r;
+      const int limit = p.mode == 3 ? g.base + (g.i0 + myrow) / p.G : g.base;   // last key this row sees
+      const int least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;             // ... the tile's first row
+      float mtop = -INFINITY, mref = -INFINITY, lsum = 0.f;
+      for (int kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
+        const int buf = tile & 1;
+        if (!(ok = pair_wait(&c->sfull[buf], (tile >> 1) & 1, w))) break;
+        tc_fence_after();
+        float x[64];
+        tmem_ld32(tq + kColS + buf * 64, x);
+        tmem_ld32(tq + kColS + buf * 64 + 32, x + 32);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(sfree0 + buf * 8);
+        const bool edge = (kt + 1) * kTile > least + 1;
+        const int key0 = kt * kTile + h * 64;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i] *= cs;
+        if (edge) {
+          const int see = min(limit, g.kend - 1) - key0;   // last column this row sees
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i > see) x[i] = -INFINITY;
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int i = 1; i < 64; ++i) mx = fmaxf(mx, x[i]);
+        float other;
+        if (!(ok = swap(mx, &other))) break;
+        mx = fmaxf(mx, other);
+        mtop = fmaxf(mtop, mx);
+        // a stale reference keeps P below 2^8, which both types hold exactly
+        // as well as values below one; O is rescaled only beyond that
+        const bool raise = mx > mref + kRaise || (mref == -INFINITY && mx > mref);
+        float f = 1.f;
+        if (raise) {
+          f = ex2(mref - mtop);
+          mref = mtop;
+          lsum *= f;
+        }
+        const float ref = mref == -INFINITY ? 0.f : mref;
+        uint32_t pk[32];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float a = ex2(x[2 * i] - ref), b = ex2(x[2 * i + 1] - ref);
+          s0 += a;
+          s1 += b;
+          pk[i] = Elt<T>::pack(a, b);
+        }
+        lsum += s0 + s1;
+        // P and O belong to the products of the tile before until they end
+        if (tile > 0 && !(ok = pair_wait(&c->pfree, (tile - 1) & 1, w))) break;
+        if (kt > g.kt0 && __any_sync(~0u, raise)) {
+          tc_fence_after();
+          for (int q = 0; q < 256; q += 32) {
+            float o[32];
+            tmem_ld32(tq + q, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st32(tq + q, o);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          sts128(prow + ((i ^ (r & 7)) << 4), make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
+        if (edge) {
+          // values of masked keys: rows no query row sees become zeros (they
+          // may hold anything), and non-finite values of the others, which
+          // would reach rows that do not see them as 0 x inf (a row that
+          // sees them has a non-finite score from the same cache row)
+          if (!(ok = pair_wait(&c->vloc[nbound & 1], (nbound >> 1) & 1, w))) break;
+          ++nbound;
+          const int use = vpos(tile);
+          for (int i = 0; i < 4; ++i) {
+            const int k = l & 63, key = kt * kTile + (i >> 1) * 64 + k;
+            if (key <= least) continue;
+            const uint32_t a = ring + ((use + i) % kSlots) * kSlot + (l >> 6) * kPanel + k * 128;
+            for (int q = 0; q < 8; ++q) {
+              const uint32_t at = a + ((q ^ (k & 7)) << 4);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (key < g.kend) {
+                v = lds128(at);
+                float e[8];
+                unpack8<T>(v, e);
+                bool fine = true;
+#pragma unroll
+                for (int z = 0; z < 8; ++z) fine &= fabsf(e[z]) < INFINITY;
+                if (fine) continue;
+#pragma unroll
+                for (int z = 0; z < 8; ++z) e[z] = fabsf(e[z]) < INFINITY ? e[z] : 0.f;
+                v = pack8<T>(e);
+              }
+              sts128(at, v);
+            }
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(pready);
+      }
+      if (!ok) break;
+      float other;
+      if (!(ok = swap(lsum, &other))) break;
+      lsum = h ? other + lsum : lsum + other;   // one order for both halves
+      if (!(ok = pair_wait(&c->pfree, (tile - 1) & 1, w))) break;
+      tc_fence_after();
+      const bool mine = myrow < g.nrows;
+      const size_t row = (size_t)g.row0 + myrow;
+      if (g.slot < 0) {
+        const float inv = lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
+        T* dst = (T*)args.a.out + row * 512 + h * 256;
+        for (int q = 0; q < 256; q += 32) {
+          float o[32];
+          tmem_ld32(tq + q, o);
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + q)[i] = pack8<T>(o + 8 * i);
+          }
+        }
+        if (mine && h == 0) {
+          args.a.smax[row] = mtop * 0.69314718055994531f;
+          args.a.ssum[row] = lsum > 0.f ? lsum * ex2(mref - mtop) : lsum;
+        }
+      } else {
+        float* dst = args.part + ((size_t)g.slot * kTile + myrow) * 512 + h * 256;
+        for (int q = 0; q < 256; q += 32) {
+          float o[32];
+          tmem_ld32(tq + q, o);
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(dst + q)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        // relative to the true max: l and O carry the same factor
+        if (mine && h == 0) {
+          args.stats[2 * (g.slot * kTile + myrow)] = make_float2(mtop, mref);
+          args.stats[2 * (g.slot * kTile + myrow) + 1] = make_float2(lsum, 0.f);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(ofree);
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] *= inv;
-  store_row512((T*)a.out + (size_t)item * 512, lane, o);
-  if (lane == 0) {
-    a.smax[item] = m;
-    a.ssum[item] = l;
+
+  // ---------------------------------------------------------------- end
+  __syncthreads();
+  cluster_sync();
+  if (tid == 0 && (c->abort || load_from(map_to(smem_u32(&c->abort), rank ^ 1)))) {
+    // Loads on their way.  The first CTA's barriers count those of both, and
+    // the two may have stopped at different places (at most the ring's depth
+    // apart): every started phase gets what it lacks, then the last phase of
+    // every slot is waited for.
+    if (leader) {
+      const int mine = c->issued, peer = load_from(map_to(smem_u32(&c->issued), 1));
+      const int peer_own = load_from(map_to(smem_u32(&c->own_mask), 1));
+      for (int u = min(mine, peer); u < max(mine, peer); ++u) {
+        const int s = u % kSlots, v = u - kKSlots, k = v < 0 ? u : v / kPer < ntiles - 1 ? v % kPer : kKSlots;
+        const uint32_t bytes = k == 4 && kKSlots == 5 ? kPanel : kSlot;   // the rope slot holds one panel
+        if ((u < mine ? c->own_mask : peer_own) >> s & 1) continue;
+        if (u < mine)
+          complete_tx(&c->full[s], bytes);
+        else
+          mbar_expect_tx(&c->full[s], bytes);
+      }
+      const int end = max(mine, peer);
+      for (int u = max(0, end - kSlots); u < end; ++u)
+        if (u < mine || !(peer_own >> (u % kSlots) & 1)) mbar_settle(&c->full[u % kSlots], (u / kSlots) & 1, status);
+      const int q = c->q_issued, pq = load_from(map_to(smem_u32(&c->q_issued), 1));
+      if (q > pq) complete_tx(&c->qfull, (8 + ROPE) * kPanel);
+      if (q < pq) mbar_expect_tx(&c->qfull, (8 + ROPE) * kPanel);
+      if (max(q, pq) > 0) mbar_settle(&c->qfull, (max(q, pq) - 1) & 1, status);
+    }
+    if (c->missing) complete_tx(&c->vloc[(c->nclean - 1) & 1], c->missing);
+    for (int i = max(0, c->nclean - 2); i < c->nclean; ++i) mbar_settle(&c->vloc[i & 1], (i >> 1) & 1, status);
+  }
+  cluster_sync();
+  if (warp == 3)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ------------------------------------------------------------------ merge
+// Pieces of row tiles: the CTAs (x, y) of the pair x whose last piece begins a
+// row tile take the rows 2 y, 2 y + 1 of it and add that tile's pieces in
+// order.  CTA (0, 0) also sums up the error words.
+template <typename T>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int e = 0;
+    for (int i = threadIdx.x; i < 2 * args.max_pairs; i += 256) e = max(e, args.status[i]);
+    e = __syncthreads_or(e == 1) ? 1 : __syncthreads_or(e == kErrSeqLens) ? kErrSeqLens
+        : __syncthreads_or(e == kErrPage) ? kErrPage : 0;
+    if (threadIdx.x == 0) *reinterpret_cast<int*>(args.a.ws) = e;
+  }
+  const int pair = blockIdx.x;
+  int slot = 2 * pair + 1;
+  Piece pc = args.piece[slot];
+  if (!pc.valid) pc = args.piece[slot = 2 * pair];
+  if (!pc.valid || !pc.first) return;
+  const int r = blockIdx.y * 2 + (threadIdx.x >> 7), col = (threadIdx.x & 127) * 4;
+  if (r >= pc.nrows) return;
+  // pieces: this one, then every following pair's first, up to the tile's end
+  float m = -INFINITY;
+  int n = 1;
+  for (int s = slot;;) {
+    m = fmaxf(m, args.stats[2 * (s * kTile + r)].x);
+    if (args.piece[s].last) break;
+    s = 2 * (pair + n++);
+  }
+  float lsum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0, s = slot; i < n; ++i) {
+    const float2 mm = args.stats[2 * (s * kTile + r)];
+    const float li = args.stats[2 * (s * kTile + r) + 1].x;
+    if (mm.x != -INFINITY || li != 0.f) {
+      const float f = ex2(mm.y - m);
+      const float4 v = *reinterpret_cast<const float4*>(args.part + ((size_t)s * kTile + r) * 512 + col);
+      lsum += li * f;
+      o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+    }
+    s = 2 * (pair + i + 1);
+  }
+  const float inv = lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
+  const size_t row = (size_t)pc.row0 + r;
+  uint2 out;
+  out.x = Elt<T>::pack(o.x * inv, o.y * inv);
+  out.y = Elt<T>::pack(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>((T*)args.a.out + row * 512 + col) = out;
+  if (col == 0) {
+    args.a.smax[row] = m * 0.69314718055994531f;
+    args.a.ssum[row] = lsum;
   }
 }
 
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+constexpr size_t kOffStatus = 256;
+const size_t kOffPiece = kOffStatus + up256(kMaxSms * sizeof(int));
+const size_t kOffStats = kOffPiece + up256(2 * kMaxPairs * sizeof(Piece));
+const size_t kOffPart = kOffStats + up256(2 * kMaxPairs * kTile * 2 * sizeof(float2));
+
 }  // namespace
 
-size_t paged_workspace(const Paged&) { return 256; }
+size_t paged_workspace(const Paged&) { return kOffPart + (size_t)2 * kMaxPairs * kTile * 512 * sizeof(float); }
 
 template <typename T>
-cudaError_t launch_paged(const PagedArgs& a, int, cudaStream_t st) {
-  cudaError_t e = cudaMemsetAsync(a.ws, 0, 4, st);
+cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
+  const Paged& p = a.pg;
+  Args g;
+  g.a = a;
+  g.max_pairs = nsm / 2;
+  g.box = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
+  g.status = reinterpret_cast<int*>(a.ws + kOffStatus);
+  g.piece = reinterpret_cast<Piece*>(a.ws + kOffPiece);
+  g.stats = reinterpret_cast<float2*>(a.ws + kOffStats);
+  g.part = reinterpret_cast<float*>(a.ws + kOffPart);
+  Maps2 m;
+  const bool f16 = Elt<T>::is_f16, rope = p.row == 576;
+  const uint64_t rows = (uint64_t)p.T * p.G;
+  if (!encode_map2d(&m.q, f16, a.q, 512, rows, 64) ||
+      !encode_map2d(&m.qr, f16, rope ? a.qr : a.q, rope ? 64 : 512, rows, 64) ||
+      !encode_map2d(&m.kv, f16, a.cache, p.row, (uint64_t)p.num_pages * p.page_size, g.box))
+    return cudaErrorInvalidValue;
+  auto kern = rope ? paged_kernel<T, true> : paged_kernel<T, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  const long long n = ((long long)a.pg.T * a.pg.G + kWarps - 1) / kWarps;
-  paged_kernel<T><<<(unsigned)n, kWarps * 32, 0, st>>>(a);
+  kern<<<2 * g.max_pairs, kThreads, kSmem, st>>>(m, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  paged_merge_kernel<T><<<dim3(g.max_pairs, kTile / 2), 256, 0, st>>>(g);
   return cudaGetLastError();
 }
 
