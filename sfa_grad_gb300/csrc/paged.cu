@@ -99,49 +99,22 @@ __device__ __forceinline__ uint32_t map_to(uint32_t a, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   return r;
 }
+// Arrival at a barrier of either CTA.  What it announces lies in this CTA's
+// shared or tensor memory, complete before it (tcgen05.wait, proxy fence), so
+// CTA scope does: a release at cluster scope measured 1100 clk a call.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ int load_from(uint32_t cluster_addr) {
   int v;
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
-// Bounded wait whose acquire covers both CTAs of the pair.
-template <bool POLL>
-__device__ __forceinline__ bool pair_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  if (POLL)
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, "
-        "p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  else
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, "
-        "0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(10000u)
-        : "memory");
-  return ok != 0;
-}
-template <bool POLL = false>
-__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, const Waiter& w) {
-  const uint32_t a = smem_u32(bar);
-  if (pair_test<POLL>(a, parity)) return true;
-  const unsigned long long t0 = gtime_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (pair_test<POLL>(a, parity)) return true;
-    if (!POLL || (it & 31u) == 0) {
-      if (*w.abort) return false;
-      if (gtime_ns() - t0 > w.limit_ns) break;
-    }
-  }
-  *w.abort = 1;
-  atomicExch(w.gerr, kErrTimeout);
-  return false;
+// Wait by a whole warp: one answer for all lanes, and the lanes together again
+// before what follows (tcgen05.ld and .st want a converged warp).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Waiter& w) {
+  const bool ok = mbar_wait(bar, parity, w);
+  return __all_sync(~0u, ok);
 }
 
 // ------------------------------------------------------------------ tensor cores, both SMs of the pair
@@ -431,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++j;
       }
       const int r = n % kSegs;
-      if (n >= kSegs && !mbar_wait(&c->seg_empty[r], (n / kSegs - 1) & 1, w)) break;
+      if (n >= kSegs && !warp_wait(&c->seg_empty[r], (n / kSegs - 1) & 1, w)) break;
       if (lane == 0) {
         c->seg[r] = g;
         mbar_arrive(&c->seg_full[r]);
@@ -460,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     auto take = [&]() {   // the next slot, free
       const int s = use % kSlots;
-      if (use >= kSlots && !pair_wait(&c->empty[s], (use / kSlots - 1) & 1, w)) ok = false;
+      if (use >= kSlots && !warp_wait(&c->empty[s], (use / kSlots - 1) & 1, w)) ok = false;
       return s;
     };
     auto load_slot = [&](int y, int box0, int x, int panels, uint32_t bar) {
@@ -503,14 +476,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int qn = 0;
     for (int n = 0; ok; ++n) {
       const int r = n % kSegs;
-      if (!mbar_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
+      if (!warp_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
       const Seg g = c->seg[r];
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->seg_empty[r]);
       if (g.kt1 == 0) break;
       int y = boxes(g, g.kt0);
       // the query rows, once the segment before has done its products
-      if (qn > 0 && !pair_wait(&c->qempty, (qn - 1) & 1, w)) break;
+      if (qn > 0 && !warp_wait(&c->qempty, (qn - 1) & 1, w)) break;
       if (leader && lane == 0) mbar_expect_tx(&c->qfull, 2 * (8 + ROPE) * kPanel);
       __syncwarp();
       if (lane < 8 + ROPE)
@@ -544,8 +517,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // is on its way to a CTA that has ended
     if (!*w.abort) {
       for (int u = max(0, use - kSlots); u < use; ++u)
-        if (!pair_wait(&c->empty[u % kSlots], (u / kSlots) & 1, w)) break;
-      if (qn > 0) pair_wait(&c->qempty, (qn - 1) & 1, w);
+        if (!warp_wait(&c->empty[u % kSlots], (u / kSlots) & 1, w)) break;
+      if (qn > 0) warp_wait(&c->qempty, (qn - 1) & 1, w);
     }
   } else if (work && leader && warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- S = Q K^T
@@ -560,17 +533,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool end = c->seg[r].kt1 == 0;
       mbar_arrive(&c->seg_empty[r]);
       if (end) break;
-      if (!(ok = pair_wait<true>(&c->qfull, n & 1, w))) break;
+      if (!(ok = mbar_wait_poll(&c->qfull, n & 1, w))) break;
       for (int t = 0; t < len && ok; ++t, ++tile) {
         const int buf = tile & 1;
-        if (tile >= 2 && !(ok = pair_wait<true>(&c->sfree[buf], (tile / 2 - 1) & 1, w))) break;
+        if (tile >= 2 && !(ok = mbar_wait_poll(&c->sfree[buf], (tile / 2 - 1) & 1, w))) break;
         tc_fence_after();
         const uint32_t d = tmem + kColS + buf * 64;
         int use = kpos(tile);
 #pragma unroll
         for (int i = 0; i < kKSlots; ++i, ++use) {
           const int s = use % kSlots;
-          if (!(ok = pair_wait<true>(&c->full[s], (use / kSlots) & 1, w))) break;
+          if (!(ok = mbar_wait_poll(&c->full[s], (use / kSlots) & 1, w))) break;
           tc_fence_after();
           const uint64_t a = dq + desc_off(2 * i * kPanel), b = dk + desc_off(s * kSlot);
           pair_mma_k64<2, 2>(d, a, b, id, i > 0);
@@ -581,15 +554,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (ok) pair_commit(&c->qempty);
     }
-    if (*w.abort) {
-      pair_commit_own(&c->settle[0]);
-      mbar_settle(&c->settle[0], 0, status);
-    }
+    // every product done, and the other CTA's last arrivals received
+    pair_commit_own(&c->settle[0]);
+    mbar_settle(&c->settle[0], 0, status);
+    for (int t = max(0, tile - 2); t < tile && ok; ++t) ok = mbar_wait(&c->sfree[t & 1], (t >> 1) & 1, w);
   } else if (work && leader && warp == 2 && lane == 0) {
     // ---------------------------------------------------------------- O += P V
     constexpr uint32_t id = idesc_f16(kTile, 256, Elt<T>::is_f16, false, true);
     const uint64_t dp = sdesc_kmajor(smem_u32(sm + kOffP), 0), dv = sdesc_mnmajor(ring, 0, 64);
-    int tile = 0;
+    int tile = 0, segs = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int r = n % kSegs;
@@ -598,15 +571,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool end = c->seg[r].kt1 == 0;
       mbar_arrive(&c->seg_empty[r]);
       if (end) break;
-      if (n > 0 && !(ok = pair_wait<true>(&c->ofree, (n - 1) & 1, w))) break;
+      ++segs;
+      if (n > 0 && !(ok = mbar_wait_poll(&c->ofree, (n - 1) & 1, w))) break;
       for (int t = 0; t < len && ok; ++t, ++tile) {
-        if (!(ok = pair_wait<true>(&c->pready, tile & 1, w))) break;
+        if (!(ok = mbar_wait_poll(&c->pready, tile & 1, w))) break;
         tc_fence_after();
         int use = vpos(tile);
 #pragma unroll
         for (int i = 0; i < 4; ++i, ++use) {
           const int s = use % kSlots;
-          if (!(ok = pair_wait<true>(&c->full[s], (use / kSlots) & 1, w))) break;
+          if (!(ok = mbar_wait_poll(&c->full[s], (use / kSlots) & 1, w))) break;
           tc_fence_after();
           pair_mma_k64<2, 128>(tmem + (i & 1) * 128, dp + desc_off((i >> 1) * kPanel), dv + desc_off(s * kSlot), id,
                                t > 0 || i > 1);
@@ -615,10 +589,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok) pair_commit(&c->pfree);
       }
     }
-    if (*w.abort) {
-      pair_commit_own(&c->settle[1]);
-      mbar_settle(&c->settle[1], 0, status);
-    }
+    pair_commit_own(&c->settle[1]);
+    mbar_settle(&c->settle[1], 0, status);
+    if (ok && segs > 0) mbar_wait(&c->ofree, (segs - 1) & 1, w);
   } else if (work && warp >= 4) {
     // ---------------------------------------------------------------- softmax, epilogue
     // Thread: row r of this CTA's 64, keys 64 h .. 64 h + 63 of a tile, and
@@ -636,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       c->xbuf[nx & 1][l] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(xch);
-      if (!mbar_wait(xch, nx & 1, w)) return false;
+      if (!warp_wait(xch, nx & 1, w)) return false;
       *o = c->xbuf[nx & 1][l ^ 64];
       ++nx;
       return true;
@@ -644,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int sr = n % kSegs;
-      if (!mbar_wait(&c->seg_full[sr], (n / kSegs) & 1, w)) break;
+      if (!warp_wait(&c->seg_full[sr], (n / kSegs) & 1, w)) break;
       const Seg g = c->seg[sr];
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->seg_empty[sr]);
@@ -655,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float mtop = -INFINITY, mref = -INFINITY, lsum = 0.f;
       for (int kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
         const int buf = tile & 1;
-        if (!(ok = pair_wait(&c->sfull[buf], (tile >> 1) & 1, w))) break;
+        if (!(ok = warp_wait(&c->sfull[buf], (tile >> 1) & 1, w))) break;
         tc_fence_after();
         float x[64];
         tmem_ld32(tq + kColS + buf * 64, x);
@@ -701,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         lsum += s0 + s1;
         // P and O belong to the products of the tile before until they end
-        if (tile > 0 && !(ok = pair_wait(&c->pfree, (tile - 1) & 1, w))) break;
+        if (tile > 0 && !(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
         if (kt > g.kt0 && __any_sync(~0u, raise)) {
           tc_fence_after();
           for (int q = 0; q < 256; q += 32) {
@@ -720,7 +693,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // may hold anything), and non-finite values of the others, which
           // would reach rows that do not see them as 0 x inf (a row that
           // sees them has a non-finite score from the same cache row)
-          if (!(ok = pair_wait(&c->vloc[nbound & 1], (nbound >> 1) & 1, w))) break;
+          if (!(ok = warp_wait(&c->vloc[nbound & 1], (nbound >> 1) & 1, w))) break;
           ++nbound;
           const int use = vpos(tile);
           for (int i = 0; i < 4; ++i) {
@@ -755,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float other;
       if (!(ok = swap(lsum, &other))) break;
       lsum = h ? other + lsum : lsum + other;   // one order for both halves
-      if (!(ok = pair_wait(&c->pfree, (tile - 1) & 1, w))) break;
+      if (!(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
       tc_fence_after();
       const bool mine = myrow < g.nrows;
       const size_t row = (size_t)g.row0 + myrow;
@@ -861,6 +834,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
   for (int s = slot;;) {
     m = fmaxf(m, args.stats[2 * (s * kTile + r)].x);
     if (args.piece[s].last) break;
+    // a call that gave up a wait leaves the chain without its end
+    if (pair + n >= args.max_pairs || !args.piece[2 * (pair + n)].valid) break;
     s = 2 * (pair + n++);
   }
   float lsum = 0.f;
