@@ -284,6 +284,18 @@ sfa_status fail(cudaError_t e, int line) {
 
 void set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 int device_sm_count() { return sm_count(); }
+bool encode_map_panels(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows,
+                       uint32_t box_panels) {
+  EncodeTiled fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 64 * 2};
+  cuuint32_t box[3] = {64, box_rows, box_panels};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool encode_map2d(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
   return encode2d(m, f16, base, cols, rows, box_rows);
 }

@@ -98,6 +98,10 @@ int device_sm_count();
 // 2-D map of rows x cols 16-bit elements, boxes of 64 columns x box_rows rows
 // with 128-byte swizzle; false when the driver refuses it (api.cu).
 bool encode_map2d(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
+// The same rows as (64 columns, rows, cols / 64 panels), boxes of 64 x
+// box_rows x box_panels.
+bool encode_map_panels(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows,
+                       uint32_t box_panels);
 
 // Deterministic key-side reduction (det.cu): counting sort of the chunk's
 // (kv row, token, slot) entries by row (count, then launch_blk_scan over the

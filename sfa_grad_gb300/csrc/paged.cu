@@ -18,15 +18,18 @@
 // kernel merges them in order: few rows over a long cache spread over all
 // SMs, and the result does not depend on timing.
 //
-// Warps of a CTA: 0 TMA loads, 1 S MMAs, 2 P V MMAs (both only in the pair's
-// first CTA), 3 the walk over the work, 4..7 softmax and epilogue.
+// Warps of a CTA: 0..3 TMA loads (ring slots w and w + 4), 4 S MMAs, 5 P V MMAs
+// (both only in the pair's first CTA), 6 the walk over the work, 8..15 softmax
+// and epilogue.
 #include "kernels.h"
 #include "rows.cuh"
 
 namespace sfa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kLoaders = 4;                 // warps that load
+constexpr int kSoft = 8;                    // softmax warps, from warp 8
 constexpr int kTile = 128;                  // keys of a tile, rows of a row tile
 constexpr int kSlots = 8;                   // ring slots, two 64 x 64 panels each
 constexpr uint32_t kPanel = 8192;           // 64 rows of 128 bytes
@@ -39,6 +42,13 @@ constexpr int kSegs = 4;                    // work descriptors in flight
 constexpr int kMinUnits = 2;                // key tiles a pair takes at least
 constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
 constexpr int kMaxPairs = kMaxSms / 2;
+constexpr float kLn2 = 0.69314718055994531f;
+// The tensor core adds each step of 16 products to a score in fp32 rounding
+// towards zero: about 0.36 x 2^-23 of the partial sum a step, 36 steps with
+// partial sums half the score on the mean.  Measured, scores are short by
+// 9 (bf16) and 12 (fp16) x 2^-24 of themselves; the scale makes that up.
+template <typename T>
+constexpr float kUnbias = 1.0f + (Elt<T>::is_f16 ? 12 : 9) * 5.9604645e-8f * 1.0f;
 
 // One piece of work: key tiles kt0 .. kt1 - 1 of a row tile.
 struct Seg {
@@ -66,18 +76,19 @@ struct Ctl {
   uint64_t xch[2];
   uint64_t settle[2];
   Seg seg[kSegs];
-  float xbuf[2][128];
-  int scan[16];
-  long long scan64[16];
+  float xbuf[2][4][64];
+  long long scan64[2 * kThreads / 32];
   long long total_units;
   long long start_off;    // units into the first sequence
   int start_seq, start_row;
   int bad, npairs;
   uint32_t tmem;
   int abort;
-  int issued, q_issued;   // ring slots and query tiles this CTA has loaded
-  int nclean, missing;    // value tiles loaded on vloc; bytes the last of them lacks
-  int own_mask;           // bit s: slot s was last loaded on vloc
+  // what this CTA's loaders have issued, for the end after a wait that gave up
+  int loads[kSlots];      // uses of a slot
+  int own[kSlots];        // its last use counts on vloc
+  int ncleaned[kLoaders]; // value slots on vloc
+  int q_issued;
 };
 
 constexpr uint32_t kSmem = kOffCtl + sizeof(Ctl) + 1024;
@@ -143,13 +154,20 @@ __device__ __forceinline__ void pair_commit_own(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-// One 64-column box into this CTA's shared memory; the bytes count on `bar`, a
-// barrier of either CTA (cluster address).
+// A box into this CTA's shared memory; the bytes count on `bar`, a barrier of
+// either CTA (cluster address).
 __device__ __forceinline__ void pair_tma(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
       "%3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_tma3(uint32_t dst, const CUtensorMap* map, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
@@ -235,14 +253,14 @@ __device__ void plan_work(const Paged& p, Ctl* c, int pair, int max_pairs) {
     const long long du = __shfl_up_sync(~0u, u, o), dt = __shfl_up_sync(~0u, t, o);
     if (lane >= o) u += du, t += dt;
   }
-  if (lane == 31) c->scan64[w] = u, c->scan64[8 + w] = t;
+  if (lane == 31) c->scan64[w] = u, c->scan64[kThreads / 32 + w] = t;
   const bool any = __syncthreads_or(bad);
   long long total = 0, toks_all = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < w) u += c->scan64[i], t += c->scan64[8 + i];
+    if (i < w) u += c->scan64[i], t += c->scan64[kThreads / 32 + i];
     total += c->scan64[i];
-    toks_all += c->scan64[8 + i];
+    toks_all += c->scan64[kThreads / 32 + i];
   }
   const bool wrong = any || (p.tnd && toks_all > p.T);
   const long long n = (total + kMinUnits - 1) / kMinUnits;
@@ -294,12 +312,15 @@ struct Args {
   int max_pairs, box;      // box: rows of a cache box (16, 32 or 64)
   int* status;             // one word a CTA
   Piece* piece;
-  float2* stats;           // (slot, row) x {m, l}
+  float4* stats;           // (slot, row) x {max, the max P is relative to, sum, -}
   float* part;             // (slot, row, 512)
 };
 
 struct Maps2 {
-  CUtensorMap q, qr, kv;   // boxes of 64 columns; kv: box rows = Args::box
+  CUtensorMap q, qr;   // boxes of 64 columns x 64 rows
+  // the cache as (64 columns, rows, panels): boxes of Args::box rows, of two
+  // panels when box = 64 and of one else; panels past the row are zeros
+  CUtensorMap kv;
 };
 
 template <typename T, bool ROPE>
@@ -320,28 +341,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     *status = 0;
     c->abort = 0;
-    c->issued = 0;
     c->q_issued = 0;
-    c->own_mask = 0;
-    c->nclean = 0;
-    c->missing = 0;
-    for (int i = 0; i < kSlots; ++i) mbar_init(&c->full[i], 1), mbar_init(&c->empty[i], 1);
+    for (int i = 0; i < kLoaders; ++i) c->ncleaned[i] = 0;
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&c->full[i], 1);
+      mbar_init(&c->empty[i], 1);
+      c->loads[i] = c->own[i] = 0;
+    }
     mbar_init(&c->qfull, 1);
     mbar_init(&c->qempty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->sfull[i], 1);
-      mbar_init(&c->sfree[i], 8);
-      mbar_init(&c->xch[i], 2);
+      mbar_init(&c->sfree[i], 2 * kSoft);
+      mbar_init(&c->xch[i], 4);
       mbar_init(&c->settle[i], 1);
-      mbar_init(&c->vloc[i], 1);
+      mbar_init(&c->vloc[i], 4);
     }
-    mbar_init(&c->pready, 8);
+    mbar_init(&c->pready, 2 * kSoft);
     mbar_init(&c->pfree, 1);
-    mbar_init(&c->ofree, 8);
-    for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], leader ? 7 : 5);
+    mbar_init(&c->ofree, 2 * kSoft);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], kLoaders + kSoft + (leader ? 2 : 0));
     mbar_fence_init();
   }
-  if (warp == 3) {
+  if (warp == 6) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -370,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (c->bad && tid == 0) *status = kErrSeqLens;
   __syncthreads();
 
-  if (work && warp == 3) {
+  if (work && warp == 6) {
     // ---------------------------------------------------------------- the walk
     int b = c->start_seq;
     long long left = u1 - u0;
@@ -411,69 +433,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (g.kt1 == 0) break;
     }
-  } else if (work && warp == 0) {
+  } else if (work && warp < kLoaders) {
     // ---------------------------------------------------------------- TMA loads
     const int nb = 64 / args.box;                   // boxes of 64 rows
     const int none = p.num_pages * p.page_size;     // a row outside the map: zeros
     const uint32_t full0 = map_to(smem_u32(&c->full[0]), lead), qfull = map_to(smem_u32(&c->qfull), lead);
-    int use = 0, nclean = 0;
+    // lane's part of a slot: one box of both panels, or box bx of panel pn
+    const int pn = nb == 1 ? 0 : lane / nb, bx = nb == 1 ? 0 : lane - pn * nb;
+    const bool issues = nb == 1 ? lane == 0 : pn < 2;
+    const uint32_t dst0 = ring + pn * kPanel + bx * args.box * 128;
+    int nloads[2] = {0, 0}, own[2] = {0, 0}, nclean = 0;   // of slots warp, warp + 4
     bool ok = true;
-    // lane l < 2 nb: cache row of the tile's box l
-    auto boxes = [&](const Seg& g, int kt) {
-      int y = none;
+    // lane l < 2 nb: page of the tile's box l, then its cache row
+    auto fetch = [&](const Seg& g, int kt) {
       const int key = kt * kTile + lane * args.box;
-      if (lane < 2 * nb && key < g.kend) {
-        const int page = __ldg(p.table + (size_t)g.seq * p.max_pages + key / p.page_size);
-        if (page >= 0 && page < p.num_pages)
-          y = page * p.page_size + key % p.page_size;
-        else
-          *status = kErrPage;
+      return lane < 2 * nb && key < g.kend ? __ldg(p.table + (size_t)g.seq * p.max_pages + key / p.page_size) : -2;
+    };
+    auto rows = [&](int kt, int page) {
+      if (page >= 0 && page < p.num_pages) return page * p.page_size + (kt * kTile + lane * args.box) % p.page_size;
+      if (page != -2) *status = kErrPage;
+      return none;
+    };
+    // ring use u, if it is this warp's: box rows from box0 on, panels from z
+    auto load = [&](int u, int y, int box0, int z, bool clean) {
+      if ((u & (kLoaders - 1)) != warp || !ok) return;
+      const int s = u % kSlots, k = u / kSlots;
+      if (k > 0 && !warp_wait(&c->empty[s], (k - 1) & 1, w)) {
+        ok = false;
+        return;
       }
-      return y;
-    };
-    auto take = [&]() {   // the next slot, free
-      const int s = use % kSlots;
-      if (use >= kSlots && !warp_wait(&c->empty[s], (use / kSlots - 1) & 1, w)) ok = false;
-      return s;
-    };
-    auto load_slot = [&](int y, int box0, int x, int panels, uint32_t bar) {
-      const int s = use % kSlots, pn = lane / nb, bx = lane - pn * nb;
-      const int yy = __shfl_sync(~0u, y, box0 + bx);
-      if (pn < panels)
-        pair_tma(ring + s * kSlot + pn * kPanel + bx * args.box * 128, &maps.kv, x + pn * 64, yy, bar);
-    };
-    // values of a tile; where a row of keys is masked for some query row, the
-    // softmax warps clean them first, so they land on this CTA's own barrier
-    auto load_v = [&](const Seg& g, int kt, int y) {
-      const bool clean = (kt + 1) * kTile > (p.mode == 3 ? g.base + g.i0 / p.G : g.base) + 1;
-      for (int i = 0; i < 4 && ok; ++i) {
-        const int s = take();
-        if (!ok) break;
-        uint32_t bar = full0 + s * 8;
-        if (clean) {
-          bar = smem_u32(&c->vloc[nclean & 1]);
-          if (lane == 0) {
-            if (i == 0) mbar_expect_tx(&c->vloc[nclean & 1], 4 * kSlot);
-            if (leader) mbar_arrive(&c->full[s]);
-          }
-        } else if (leader && lane == 0) {
-          mbar_expect_tx(&c->full[s], 2 * kSlot);
-        }
-        __syncwarp();
-        load_slot(y, (i >> 1) * nb, (int)rank * 256 + (i & 1) * 128, 2, bar);
+      uint32_t bar = full0 + s * 8;
+      if (clean) {
+        // values with masked keys: the softmax warps clean them first, so
+        // they land on this CTA's own barrier
+        uint64_t* v = &c->vloc[nclean & 1];
+        bar = smem_u32(v);
         if (lane == 0) {
-          c->own_mask = clean ? c->own_mask | 1 << s : c->own_mask & ~(1 << s);
-          if (clean && i == 0) c->nclean = nclean + 1;
-          if (clean) c->missing = (3 - i) * kSlot;
+          mbar_expect_tx(v, kSlot);
+          if (leader) mbar_arrive(&c->full[s]);
         }
-        ++use;
+        ++nclean;
+      } else if (leader && lane == 0) {
+        mbar_expect_tx(&c->full[s], 2 * kSlot);
       }
-      nclean += clean;
+      const int yy = __shfl_sync(~0u, y, box0 + bx);
+      if (issues) pair_tma3(dst0 + s * kSlot, &maps.kv, yy, z + pn, bar);
+      nloads[s >> 2] = k + 1;
+      own[s >> 2] = clean;
+    };
+    auto load_v = [&](const Seg& g, int kt, int y, int u) {
+      const bool clean = (kt + 1) * kTile > (p.mode == 3 ? g.base + g.i0 / p.G : g.base) + 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load(u + i, y, (i >> 1) * nb, (int)rank * 4 + (i & 1) * 2, clean);
     };
     Seg prev;
-    int prev_kt = 0, prev_y = 0;
-    bool have = false;
-    int qn = 0;
+    int prev_kt = 0, prev_y = 0, tile = 0, qn = 0;
     for (int n = 0; ok; ++n) {
       const int r = n % kSegs;
       if (!warp_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
@@ -481,46 +495,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->seg_empty[r]);
       if (g.kt1 == 0) break;
-      int y = boxes(g, g.kt0);
-      // the query rows, once the segment before has done its products
-      if (qn > 0 && !warp_wait(&c->qempty, (qn - 1) & 1, w)) break;
-      if (leader && lane == 0) mbar_expect_tx(&c->qfull, 2 * (8 + ROPE) * kPanel);
-      __syncwarp();
-      if (lane < 8 + ROPE)
-        pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64, g.row0 + rank * 64,
-                 qfull);
-      ++qn;
-      if (lane == 0) c->q_issued = qn;
-      for (int kt = g.kt0; kt < g.kt1 && ok; ++kt) {
-        const int ynext = kt + 1 < g.kt1 ? boxes(g, kt + 1) : none;   // in flight during the waits
-        for (int i = 0; i < kKSlots && ok; ++i) {
-          const int s = take();
-          if (!ok) break;
-          const int panels = i < 4 ? 2 : 1;
-          if (leader && lane == 0) mbar_expect_tx(&c->full[s], 2 * panels * kPanel);
-          __syncwarp();
-          load_slot(y, (int)rank * nb, i * 128, panels, full0 + s * 8);
-          if (lane == 0) c->own_mask &= ~(1 << s);
-          ++use;
-        }
-        if (have && ok) load_v(prev, prev_kt, prev_y);
+      int page = fetch(g, g.kt0);
+      if (warp == 0) {
+        // the query rows, once the segment before has done its products
+        if (qn > 0 && !warp_wait(&c->qempty, (qn - 1) & 1, w)) break;
+        if (leader && lane == 0) mbar_expect_tx(&c->qfull, 2 * (8 + ROPE) * kPanel);
+        __syncwarp();
+        if (lane < 8 + ROPE)
+          pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64, g.row0 + rank * 64,
+                   qfull);
+        ++qn;
+      }
+      for (int kt = g.kt0; kt < g.kt1 && ok; ++kt, ++tile) {
+        const int y = rows(kt, page);
+        if (kt + 1 < g.kt1) page = fetch(g, kt + 1);   // in flight during the waits
+        const int u = kpos(tile);
+#pragma unroll
+        for (int i = 0; i < kKSlots; ++i) load(u + i, y, (int)rank * nb, 2 * i, false);
+        if (tile > 0) load_v(prev, prev_kt, prev_y, u + kKSlots);
         prev = g;
         prev_kt = kt;
         prev_y = y;
-        have = true;
-        y = ynext;
       }
     }
-    if (have && ok && !*w.abort) load_v(prev, prev_kt, prev_y);
-    if (lane == 0) c->issued = use;
-    // the ring's last releases and the last query release have arrived: none
+    if (tile > 0) load_v(prev, prev_kt, prev_y, vpos(tile - 1));
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        c->loads[warp + 4 * i] = nloads[i];
+        c->own[warp + 4 * i] = own[i];
+      }
+      c->ncleaned[warp] = nclean;
+      if (warp == 0) c->q_issued = qn;
+    }
+    // the slots' last releases and the last query release have arrived: none
     // is on its way to a CTA that has ended
-    if (!*w.abort) {
-      for (int u = max(0, use - kSlots); u < use; ++u)
-        if (!warp_wait(&c->empty[u % kSlots], (u / kSlots) & 1, w)) break;
+    if (__all_sync(~0u, !*w.abort)) {
+      for (int i = 0; i < 2; ++i)
+        if (nloads[i] > 0) warp_wait(&c->empty[warp + 4 * i], (nloads[i] - 1) & 1, w);
       if (qn > 0) warp_wait(&c->qempty, (qn - 1) & 1, w);
     }
-  } else if (work && leader && warp == 1 && lane == 0) {
+  } else if (work && leader && warp == 4 && lane == 0) {
     // ---------------------------------------------------------------- S = Q K^T
     constexpr uint32_t id = idesc_f16(kTile, kTile, Elt<T>::is_f16, false, false);
     const uint64_t dq = sdesc_kmajor(smem_u32(sm), 0), dk = sdesc_kmajor(ring, 0);
@@ -558,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_commit_own(&c->settle[0]);
     mbar_settle(&c->settle[0], 0, status);
     for (int t = max(0, tile - 2); t < tile && ok; ++t) ok = mbar_wait(&c->sfree[t & 1], (t >> 1) & 1, w);
-  } else if (work && leader && warp == 2 && lane == 0) {
+  } else if (work && leader && warp == 5 && lane == 0) {
     // ---------------------------------------------------------------- O += P V
     constexpr uint32_t id = idesc_f16(kTile, 256, Elt<T>::is_f16, false, true);
     const uint64_t dp = sdesc_kmajor(smem_u32(sm + kOffP), 0), dv = sdesc_mnmajor(ring, 0, 64);
@@ -592,25 +606,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_commit_own(&c->settle[1]);
     mbar_settle(&c->settle[1], 0, status);
     if (ok && segs > 0) mbar_wait(&c->ofree, (segs - 1) & 1, w);
-  } else if (work && warp >= 4) {
+  } else if (work && warp >= 8) {
     // ---------------------------------------------------------------- softmax, epilogue
-    // Thread: row r of this CTA's 64, keys 64 h .. 64 h + 63 of a tile, and
-    // features 256 h .. 256 h + 255 of O.
-    const int l = tid - 128, r = l & 63, h = l >> 6, wq = warp & 3;
+    // Thread: row r of this CTA's 64, keys 64 h + 32 g .. + 31 of a tile, and
+    // features 256 h + 128 g .. + 127 of O; the four threads of a row exchange
+    // its max.
+    const int wq = warp & 3, cg = (warp >> 2) & 1;
+    const int l = wq * 32 + lane, r = l & 63, h = l >> 6, t = tid - 256;
     const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t prow = smem_u32(sm + kOffP) + h * kPanel + r * 128;
     const uint32_t pready = map_to(smem_u32(&c->pready), lead), ofree = map_to(smem_u32(&c->ofree), lead);
     const uint32_t sfree0 = map_to(smem_u32(&c->sfree[0]), lead);
     uint64_t* xch = &c->xch[wq & 1];
-    const float cs = args.a.scale * kLog2e;
+    const float scale = args.a.scale * kUnbias<T>, cs = scale * kLog2e;
     int tile = 0, nx = 0, nbound = 0;
-    // exchange of one value with the thread of the row's other half
-    auto swap = [&](float v, float* o) {
-      c->xbuf[nx & 1][l] = v;
+    // one value of each of the row's four threads
+    auto exchange = [&](float v, float* o) {
+      c->xbuf[nx & 1][2 * h + cg][r] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(xch);
       if (!warp_wait(xch, nx & 1, w)) return false;
-      *o = c->xbuf[nx & 1][l ^ 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = c->xbuf[nx & 1][i][r];
       ++nx;
       return true;
     };
@@ -625,37 +642,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int myrow = (int)rank * 64 + r;
       const int limit = p.mode == 3 ? g.base + (g.i0 + myrow) / p.G : g.base;   // last key this row sees
       const int least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;             // ... the tile's first row
+      // the max so far and the one P is relative to, times scale log2(e)
       float mtop = -INFINITY, mref = -INFINITY, lsum = 0.f;
       for (int kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
         const int buf = tile & 1;
         if (!(ok = warp_wait(&c->sfull[buf], (tile >> 1) & 1, w))) break;
         tc_fence_after();
-        float x[64];
-        tmem_ld32(tq + kColS + buf * 64, x);
-        tmem_ld32(tq + kColS + buf * 64 + 32, x + 32);
+        float x[32];
+        tmem_ld32(tq + kColS + buf * 64 + cg * 32, x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(sfree0 + buf * 8);
         const bool edge = (kt + 1) * kTile > least + 1;
-        const int key0 = kt * kTile + h * 64;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] *= cs;
+        for (int i = 0; i < 32; ++i) x[i] *= cs;
         if (edge) {
-          const int see = min(limit, g.kend - 1) - key0;   // last column this row sees
+          const int see = min(limit, g.kend - 1) - (kt * kTile + h * 64 + cg * 32);   // last column this row sees
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
+          for (int i = 0; i < 32; ++i)
             if (i > see) x[i] = -INFINITY;
         }
-        float mx = x[0];
+        float mx[4];
 #pragma unroll
-        for (int i = 1; i < 64; ++i) mx = fmaxf(mx, x[i]);
-        float other;
-        if (!(ok = swap(mx, &other))) break;
-        mx = fmaxf(mx, other);
-        mtop = fmaxf(mtop, mx);
-        // a stale reference keeps P below 2^8, which both types hold exactly
-        // as well as values below one; O is rescaled only beyond that
-        const bool raise = mx > mref + kRaise || (mref == -INFINITY && mx > mref);
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = x[i];
+#pragma unroll
+          for (int q = 4; q < 32; q += 4) mx[i] = fmaxf(mx[i], x[i + q]);
+        }
+        if (!(ok = exchange(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mx))) break;
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        mtop = fmaxf(mtop, top);
+        // a stale reference keeps P below 2^8, which both types hold as
+        // exactly as values below one; O is rescaled only beyond that
+        const bool raise = top > mref + kRaise;
         float f = 1.f;
         if (raise) {
           f = ex2(mref - mtop);
@@ -663,10 +682,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           lsum *= f;
         }
         const float ref = mref == -INFINITY ? 0.f : mref;
-        uint32_t pk[32];
+        uint32_t pk[16];
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           const float a = ex2(x[2 * i] - ref), b = ex2(x[2 * i + 1] - ref);
           s0 += a;
           s1 += b;
@@ -677,17 +696,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (tile > 0 && !(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
         if (kt > g.kt0 && __any_sync(~0u, raise)) {
           tc_fence_after();
-          for (int q = 0; q < 256; q += 32) {
+          for (int q = 0; q < 128; q += 32) {
             float o[32];
-            tmem_ld32(tq + q, o);
+            tmem_ld32(tq + cg * 128 + q, o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(tq + q, o);
+            tmem_st32(tq + cg * 128 + q, o);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          sts128(prow + ((i ^ (r & 7)) << 4), make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
+        for (int i = 0; i < 4; ++i)
+          sts128(prow + (((cg * 4 + i) ^ (r & 7)) << 4),
+                 make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
         if (edge) {
           // values of masked keys: rows no query row sees become zeros (they
           // may hold anything), and non-finite values of the others, which
@@ -697,10 +717,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++nbound;
           const int use = vpos(tile);
           for (int i = 0; i < 4; ++i) {
-            const int k = l & 63, key = kt * kTile + (i >> 1) * 64 + k;
+            const int k = t & 63, key = kt * kTile + (i >> 1) * 64 + k;
             if (key <= least) continue;
-            const uint32_t a = ring + ((use + i) % kSlots) * kSlot + (l >> 6) * kPanel + k * 128;
-            for (int q = 0; q < 8; ++q) {
+            const uint32_t a = ring + ((use + i) % kSlots) * kSlot + ((t >> 6) & 1) * kPanel + k * 128;
+            for (int q = (t >> 7) * 4; q < (t >> 7) * 4 + 4; ++q) {
               const uint32_t at = a + ((q ^ (k & 7)) << 4);
               uint4 v = make_uint4(0, 0, 0, 0);
               if (key < g.kend) {
@@ -725,46 +745,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive_at(pready);
       }
       if (!ok) break;
-      float other;
-      if (!(ok = swap(lsum, &other))) break;
-      lsum = h ? other + lsum : lsum + other;   // one order for both halves
+      float ls[4];
+      if (!(ok = exchange(lsum, ls))) break;
+      lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
       if (!(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
       tc_fence_after();
       const bool mine = myrow < g.nrows;
       const size_t row = (size_t)g.row0 + myrow;
+      const int col = h * 256 + cg * 128;
       if (g.slot < 0) {
         const float inv = lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
-        T* dst = (T*)args.a.out + row * 512 + h * 256;
-        for (int q = 0; q < 256; q += 32) {
+        T* dst = (T*)args.a.out + row * 512 + col;
+        for (int q = 0; q < 128; q += 32) {
           float o[32];
-          tmem_ld32(tq + q, o);
+          tmem_ld32(tq + cg * 128 + q, o);
           if (mine) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= inv;
 #pragma unroll
             for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + q)[i] = pack8<T>(o + 8 * i);
           }
+          __syncwarp();
         }
-        if (mine && h == 0) {
-          args.a.smax[row] = mtop * 0.69314718055994531f;
+        if (mine && h == 0 && cg == 0) {
+          args.a.smax[row] = mtop * kLn2;
           args.a.ssum[row] = lsum > 0.f ? lsum * ex2(mref - mtop) : lsum;
         }
       } else {
-        float* dst = args.part + ((size_t)g.slot * kTile + myrow) * 512 + h * 256;
-        for (int q = 0; q < 256; q += 32) {
+        float* dst = args.part + ((size_t)g.slot * kTile + myrow) * 512 + col;
+        for (int q = 0; q < 128; q += 32) {
           float o[32];
-          tmem_ld32(tq + q, o);
+          tmem_ld32(tq + cg * 128 + q, o);
           if (mine) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               reinterpret_cast<float4*>(dst + q)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
+          __syncwarp();
         }
-        // relative to the true max: l and O carry the same factor
-        if (mine && h == 0) {
-          args.stats[2 * (g.slot * kTile + myrow)] = make_float2(mtop, mref);
-          args.stats[2 * (g.slot * kTile + myrow) + 1] = make_float2(lsum, 0.f);
-        }
+        if (mine && h == 0 && cg == 0)
+          args.stats[g.slot * kTile + myrow] = make_float4(mtop, mref, lsum, 0.f);
       }
       tc_fence_before();
       __syncwarp();
@@ -777,34 +797,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   if (tid == 0 && (c->abort || load_from(map_to(smem_u32(&c->abort), rank ^ 1)))) {
     // Loads on their way.  The first CTA's barriers count those of both, and
-    // the two may have stopped at different places (at most the ring's depth
+    // the two may have stopped at different places (a slot's uses at most one
     // apart): every started phase gets what it lacks, then the last phase of
     // every slot is waited for.
     if (leader) {
-      const int mine = c->issued, peer = load_from(map_to(smem_u32(&c->issued), 1));
-      const int peer_own = load_from(map_to(smem_u32(&c->own_mask), 1));
-      for (int u = min(mine, peer); u < max(mine, peer); ++u) {
-        const int s = u % kSlots, v = u - kKSlots, k = v < 0 ? u : v / kPer < ntiles - 1 ? v % kPer : kKSlots;
-        const uint32_t bytes = k == 4 && kKSlots == 5 ? kPanel : kSlot;   // the rope slot holds one panel
-        if ((u < mine ? c->own_mask : peer_own) >> s & 1) continue;
-        if (u < mine)
-          complete_tx(&c->full[s], bytes);
-        else
-          mbar_expect_tx(&c->full[s], bytes);
+      for (int i = 0; i < kSlots; ++i) {
+        const int mine = c->loads[i], peer = load_from(map_to(smem_u32(&c->loads[i]), 1));
+        const int peer_own = load_from(map_to(smem_u32(&c->own[i]), 1));
+        int phases = mine;
+        if (mine > peer && !c->own[i]) complete_tx(&c->full[i], kSlot);
+        if (peer > mine && !peer_own) {
+          mbar_expect_tx(&c->full[i], kSlot);
+          phases = peer;
+        }
+        if (phases > 0) mbar_settle(&c->full[i], (phases - 1) & 1, status);
       }
-      const int end = max(mine, peer);
-      for (int u = max(0, end - kSlots); u < end; ++u)
-        if (u < mine || !(peer_own >> (u % kSlots) & 1)) mbar_settle(&c->full[u % kSlots], (u / kSlots) & 1, status);
       const int q = c->q_issued, pq = load_from(map_to(smem_u32(&c->q_issued), 1));
       if (q > pq) complete_tx(&c->qfull, (8 + ROPE) * kPanel);
       if (q < pq) mbar_expect_tx(&c->qfull, (8 + ROPE) * kPanel);
       if (max(q, pq) > 0) mbar_settle(&c->qfull, (max(q, pq) - 1) & 1, status);
     }
-    if (c->missing) complete_tx(&c->vloc[(c->nclean - 1) & 1], c->missing);
-    for (int i = max(0, c->nclean - 2); i < c->nclean; ++i) mbar_settle(&c->vloc[i & 1], (i >> 1) & 1, status);
+    // vloc: the tiles some loader has begun and others have not
+    int most = 0;
+    for (int i = 0; i < kLoaders; ++i) most = max(most, c->ncleaned[i]);
+    for (int m = max(0, most - 2); m < most; ++m) {
+      int n = 0;
+      for (int i = 0; i < kLoaders; ++i) n += c->ncleaned[i] > m;
+      if (n < kLoaders) mbar_arrive_n(&c->vloc[m & 1], kLoaders - n);
+      mbar_settle(&c->vloc[m & 1], (m >> 1) & 1, status);
+    }
   }
   cluster_sync();
-  if (warp == 3)
+  if (warp == 6)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
@@ -832,7 +856,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
   float m = -INFINITY;
   int n = 1;
   for (int s = slot;;) {
-    m = fmaxf(m, args.stats[2 * (s * kTile + r)].x);
+    m = fmaxf(m, args.stats[s * kTile + r].x);
     if (args.piece[s].last) break;
     // a call that gave up a wait leaves the chain without its end
     if (pair + n >= args.max_pairs || !args.piece[2 * (pair + n)].valid) break;
@@ -841,8 +865,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
   float lsum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0, s = slot; i < n; ++i) {
-    const float2 mm = args.stats[2 * (s * kTile + r)];
-    const float li = args.stats[2 * (s * kTile + r) + 1].x;
+    const float4 mm = args.stats[s * kTile + r];
+    const float li = mm.z;
     if (mm.x != -INFINITY || li != 0.f) {
       const float f = ex2(mm.y - m);
       const float4 v = *reinterpret_cast<const float4*>(args.part + ((size_t)s * kTile + r) * 512 + col);
@@ -858,7 +882,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
   out.y = Elt<T>::pack(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>((T*)args.a.out + row * 512 + col) = out;
   if (col == 0) {
-    args.a.smax[row] = m * 0.69314718055994531f;
+    args.a.smax[row] = m * kLn2;
     args.a.ssum[row] = lsum;
   }
 }
@@ -867,7 +891,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr size_t kOffStatus = 256;
 const size_t kOffPiece = kOffStatus + up256(kMaxSms * sizeof(int));
 const size_t kOffStats = kOffPiece + up256(2 * kMaxPairs * sizeof(Piece));
-const size_t kOffPart = kOffStats + up256(2 * kMaxPairs * kTile * 2 * sizeof(float2));
+const size_t kOffPart = kOffStats + up256(2 * kMaxPairs * kTile * sizeof(float4));
 
 }  // namespace
 
@@ -882,14 +906,14 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   g.box = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
   g.status = reinterpret_cast<int*>(a.ws + kOffStatus);
   g.piece = reinterpret_cast<Piece*>(a.ws + kOffPiece);
-  g.stats = reinterpret_cast<float2*>(a.ws + kOffStats);
+  g.stats = reinterpret_cast<float4*>(a.ws + kOffStats);
   g.part = reinterpret_cast<float*>(a.ws + kOffPart);
   Maps2 m;
   const bool f16 = Elt<T>::is_f16, rope = p.row == 576;
   const uint64_t rows = (uint64_t)p.T * p.G;
   if (!encode_map2d(&m.q, f16, a.q, 512, rows, 64) ||
       !encode_map2d(&m.qr, f16, rope ? a.qr : a.q, rope ? 64 : 512, rows, 64) ||
-      !encode_map2d(&m.kv, f16, a.cache, p.row, (uint64_t)p.num_pages * p.page_size, g.box))
+      !encode_map_panels(&m.kv, f16, a.cache, p.row, (uint64_t)p.num_pages * p.page_size, g.box, g.box == 64 ? 2 : 1))
     return cudaErrorInvalidValue;
   auto kern = rope ? paged_kernel<T, true> : paged_kernel<T, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
