@@ -3,7 +3,7 @@
 //   x_j = scale [q || q_rope] . row_j,  out = sum_j exp(x_j - m) row_j[:512] / l
 //
 // Query rows (token, head) are packed 128 to a row tile, keys pass in tiles of
-// 128 with a running max m and sum l.  A row tile belongs to a pair of CTAs
+// 256 with a running max m and sum l.  A row tile belongs to a pair of CTAs
 // (one cluster), each with 64 of its rows: O needs 512 fp32 columns a row, so
 // 128 rows would fill the tensor memory of an SM and leave nothing for S,
 // while M = 64 on one SM runs at half rate.  With cta_group::2 and M = 128
@@ -18,9 +18,9 @@
 // kernel merges them in order: few rows over a long cache spread over all
 // SMs, and the result does not depend on timing.
 //
-// Warps of a CTA: 0..3 TMA loads (ring slots w and w + 4), 4 S MMAs, 5 P V MMAs
-// (both only in the pair's first CTA), 6 the walk over the work, 8..15 softmax
-// and epilogue.
+// Warps of a CTA: 0..3 TMA loads (ring slots 2 w and 2 w + 1), 4 the MMAs (only
+// in the pair's first CTA), 6 the walk over the work, 8..15 softmax and
+// epilogue.
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -30,25 +30,38 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kLoaders = 4;                 // warps that load
 constexpr int kSoft = 8;                    // softmax warps, from warp 8
-constexpr int kTile = 128;                  // keys of a tile, rows of a row tile
-constexpr int kSlots = 8;                   // ring slots, two 64 x 64 panels each
+constexpr int kRows = 128;                  // rows of a row tile
+constexpr int kKeys = 256;                  // keys of a tile
+constexpr int kSlots = 7;                   // ring slots
 constexpr uint32_t kPanel = 8192;           // 64 rows of 128 bytes
-constexpr uint32_t kSlot = 2 * kPanel;
-constexpr uint32_t kOffP = 9 * kPanel;      // P: 64 rows x 128 keys
-constexpr uint32_t kOffRing = kOffP + 2 * kPanel;
+constexpr uint32_t kSlot = 2 * kPanel;      // keys: 128 rows x 64 features; values: 64 rows x 128 features
+constexpr int kVSlots = 8;                  // ring slots of a tile's values
+constexpr uint32_t kOffP = 9 * kPanel;      // P: 64 rows x 256 keys
+constexpr uint32_t kOffRing = kOffP + 4 * kPanel;
 constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
-constexpr uint32_t kColS = 256;             // tensor memory: O, then two S tiles of 64 columns
+constexpr uint32_t kColS = 256;             // tensor memory: O, then two S tiles of 128 columns
 constexpr int kSegs = 4;                    // work descriptors in flight
-constexpr int kMinUnits = 2;                // key tiles a pair takes at least
+constexpr int kMinUnits = 1;                // key tiles a pair takes at least
 constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
 constexpr int kMaxPairs = kMaxSms / 2;
-constexpr float kLn2 = 0.69314718055994531f;
+constexpr bool kSpin = true;                // the MMA issuers poll
+// How scores are scaled.  The sign is taken out first, so that a larger score
+// is a larger weight, and a scale of zero becomes one that leaves every finite
+// score zero and a masked one -inf.
+struct Scale {
+  bool negative;
+  float scale, log2;   // |scale|, times log2(e)
+};
 // The tensor core adds each step of 16 products to a score in fp32 rounding
 // towards zero: about 0.36 x 2^-23 of the partial sum a step, 36 steps with
 // partial sums half the score on the mean.  Measured, scores are short by
 // 9 (bf16) and 12 (fp16) x 2^-24 of themselves; the scale makes that up.
 template <typename T>
-constexpr float kUnbias = 1.0f + (Elt<T>::is_f16 ? 12 : 9) * 5.9604645e-8f * 1.0f;
+__device__ __forceinline__ Scale score_scale(float scale) {
+  constexpr float unbias = 1.0f + (Elt<T>::is_f16 ? 12 : 9) * 5.9604645e-8f;
+  const float s = fabsf(scale) * unbias;
+  return {scale < 0.f, s, fmaxf(s * kLog2e, 1e-30f)};
+}
 
 // One piece of work: key tiles kt0 .. kt1 - 1 of a row tile.
 struct Seg {
@@ -71,10 +84,10 @@ struct Ctl {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t qfull, qempty;
   uint64_t sfull[2], sfree[2];
-  uint64_t pready, pfree, ofree, vloc[2];
+  uint64_t pready, pfree, ofree, vloc[kLoaders];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t xch[2];
-  uint64_t settle[2];
+  uint64_t settle;
   Seg seg[kSegs];
   float xbuf[2][4][64];
   long long scan64[2 * kThreads / 32];
@@ -86,8 +99,6 @@ struct Ctl {
   int abort;
   // what this CTA's loaders have issued, for the end after a wait that gave up
   int loads[kSlots];      // uses of a slot
-  int own[kSlots];        // its last use counts on vloc
-  int ncleaned[kLoaders]; // value slots on vloc
   int q_issued;
 };
 
@@ -116,15 +127,43 @@ __device__ __forceinline__ uint32_t map_to(uint32_t a, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+__device__ __forceinline__ void expect_at(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ int load_from(uint32_t cluster_addr) {
   int v;
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
+// Bounded waits of this kernel: as common.cuh's, with the limit in SM clocks
+// (a read of the global timer costs more than most waits here last) and looked
+// at every 64 polls.
+struct Limit {
+  volatile int* abort;
+  int* gerr;
+  long long clocks;
+};
+template <bool POLL>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Limit& w) {
+  const uint32_t a = smem_u32(bar);
+  if (POLL ? mbar_poll(a, parity) : mbar_test(a, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (POLL ? mbar_poll(a, parity) : mbar_test(a, parity)) return true;
+    if (!POLL || (it & 63u) == 0) {
+      if (*w.abort) return false;
+      if (clock64() - t0 > w.clocks) break;
+    }
+  }
+  *w.abort = 1;
+  atomicExch(w.gerr, kErrTimeout);
+  return false;
+}
 // Wait by a whole warp: one answer for all lanes, and the lanes together again
 // before what follows (tcgen05.ld and .st want a converged warp).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Waiter& w) {
-  const bool ok = mbar_wait(bar, parity, w);
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Limit& w) {
+  const bool ok = wait_bar<false>(bar, parity, w);
   return __all_sync(~0u, ok);
 }
 
@@ -170,10 +209,6 @@ __device__ __forceinline__ void pair_tma3(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
   uint32_t r[32];
 #pragma unroll
@@ -200,30 +235,31 @@ __device__ __forceinline__ SeqWork seq_work(const Paged& p, int b) {
   s.qlen = p.act_q ? __ldg(p.act_q + b) : p.S1;
   s.kvlen = __ldg(p.act_kv + b);
   s.rows = s.qlen * p.G;
-  s.tiles = (s.rows + kTile - 1) / kTile;
+  s.tiles = (s.rows + kRows - 1) / kRows;
   return s;
 }
 __device__ __forceinline__ int tile_keys(const Paged& p, const SeqWork& s, int j) {
   if (p.mode == 0) return s.kvlen;
-  const int tok = min((j + 1) * kTile - 1, s.rows - 1) / p.G;
+  const int tok = min((j + 1) * kRows - 1, s.rows - 1) / p.G;
   return max(0, s.kvlen - s.qlen + tok + 1);
 }
 __device__ __forceinline__ int tile_units(const Paged& p, const SeqWork& s, int j) {
-  return max(1, (tile_keys(p, s, j) + kTile - 1) / kTile);
+  return max(1, (tile_keys(p, s, j) + kKeys - 1) / kKeys);
 }
 // Key tiles of row tiles 0 .. n-1, n < tiles (mode 3).  Tile j ends at token
-// (128 j + 127) / G, so its units are max(1, (j + e) / G) rounded down with
-// e = (127 + G (base + 128)) / 128 rounded down: ones while j + e < 2 G, then
-// a sum over i / G.
+// (128 j + 127) / G, so its units are max(1, (j + e) / d) rounded down with d =
+// 2 G and e = (127 + G (base + 256)) / 128 rounded down: ones while j + e <
+// 2 d, then a sum over i / d.
 __device__ __forceinline__ long long units_before(const Paged& p, const SeqWork& s, int n) {
   if (n <= 0) return 0;
-  if (p.mode == 0) return (long long)n * max(1, (s.kvlen + kTile - 1) / kTile);
-  const long long x = 127 + (long long)p.G * (s.kvlen - s.qlen + kTile);
-  const long long e = x >> 7;
-  const long long ones = min((long long)n, max(0LL, 2LL * p.G - e));
-  auto sum = [&](long long m) {   // sum of i / G over i < m
-    const long long q = (long long)((unsigned)m / (unsigned)p.G), r = m - q * p.G;
-    return (long long)p.G * (q * (q - 1) / 2) + q * r;
+  if (p.mode == 0) return (long long)n * max(1, (s.kvlen + kKeys - 1) / kKeys);
+  const int d = kKeys / kRows * p.G;
+  const long long x = kRows - 1 + (long long)p.G * (s.kvlen - s.qlen + kKeys);
+  const long long e = x >> 7;   // / kRows, rounded down
+  const long long ones = min((long long)n, max(0LL, 2LL * d - e));
+  auto sum = [&](long long m) {   // sum of i / d over i < m
+    const long long q = (long long)((unsigned)m / (unsigned)d), r = m - q * d;
+    return d * (q * (q - 1) / 2) + q * r;
   };
   return ones + (ones < n ? sum(n + e) - sum(ones + e) : 0);
 }
@@ -309,7 +345,8 @@ __device__ __forceinline__ int find_tile(const Paged& p, const SeqWork& s, long 
 
 struct Args {
   PagedArgs a;
-  int max_pairs, box;      // box: rows of a cache box (16, 32 or 64)
+  int max_pairs;
+  int kbox, vbox;          // rows of a box of keys (16 .. 128) and of values (16 .. 64)
   int* status;             // one word a CTA
   Piece* piece;
   float4* stats;           // (slot, row) x {max, the max P is relative to, sum, -}
@@ -318,9 +355,9 @@ struct Args {
 
 struct Maps2 {
   CUtensorMap q, qr;   // boxes of 64 columns x 64 rows
-  // the cache as (64 columns, rows, panels): boxes of Args::box rows, of two
-  // panels when box = 64 and of one else; panels past the row are zeros
-  CUtensorMap kv;
+  // the cache as (64 columns, rows, panels); k: boxes of kbox rows of a
+  // panel, v: of vbox rows, of two panels when vbox = 64
+  CUtensorMap k, v;
 };
 
 template <typename T, bool ROPE>
@@ -334,33 +371,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cta_rank();
   const int pair = blockIdx.x >> 1;
   const bool leader = rank == 0;
-  constexpr int kKSlots = ROPE ? 5 : 4;       // ring slots of a tile's keys (S), 4 more for its values
-  constexpr int kPer = kKSlots + 4;
+  constexpr int kKSlots = ROPE ? 9 : 8;       // ring slots of a tile's keys
+  constexpr int kPer = kKSlots + kVSlots;
   int* status = args.status + blockIdx.x;
 
   if (tid == 0) {
     *status = 0;
     c->abort = 0;
     c->q_issued = 0;
-    for (int i = 0; i < kLoaders; ++i) c->ncleaned[i] = 0;
+    for (int i = 0; i < kLoaders; ++i) mbar_init(&c->vloc[i], 1);
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&c->full[i], 1);
+      mbar_init(&c->full[i], 2);
       mbar_init(&c->empty[i], 1);
-      c->loads[i] = c->own[i] = 0;
+      c->loads[i] = 0;
     }
-    mbar_init(&c->qfull, 1);
+    mbar_init(&c->qfull, 2);
     mbar_init(&c->qempty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->sfull[i], 1);
       mbar_init(&c->sfree[i], 2 * kSoft);
       mbar_init(&c->xch[i], 4);
-      mbar_init(&c->settle[i], 1);
-      mbar_init(&c->vloc[i], 4);
     }
+    mbar_init(&c->settle, 1);
     mbar_init(&c->pready, 2 * kSoft);
     mbar_init(&c->pfree, 1);
     mbar_init(&c->ofree, 2 * kSoft);
-    for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], kLoaders + kSoft + (leader ? 2 : 0));
+    for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], kLoaders + kSoft + (leader ? 1 : 0));
     mbar_fence_init();
   }
   if (warp == 6) {
@@ -374,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = c->tmem;
-  const Waiter w{&c->abort, status, args.a.wait_ns};
+  const Limit w{&c->abort, status, (long long)(args.a.wait_ns * 21 / 10)};   // SM clock at most 2.1 GHz
   const bool work = c->start_seq >= 0;
   const long long u0 = c->total_units * pair / c->npairs, u1 = c->total_units * (pair + 1) / c->npairs;
   const int ntiles = work ? (int)(u1 - u0) : 0;
@@ -411,9 +447,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int units = tile_units(p, s, j);
         g.seq = b;
-        g.row0 = row + j * kTile;
-        g.i0 = j * kTile;
-        g.nrows = min(kTile, s.rows - g.i0);
+        g.row0 = row + j * kRows;
+        g.i0 = j * kRows;
+        g.nrows = min(kRows, s.rows - g.i0);
         g.kt0 = kt;
         g.kt1 = (int)min((long long)units, kt + left);
         g.kend = tile_keys(p, s, j);
@@ -435,56 +471,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (work && warp < kLoaders) {
     // ---------------------------------------------------------------- TMA loads
-    const int nb = 64 / args.box;                   // boxes of 64 rows
-    const int none = p.num_pages * p.page_size;     // a row outside the map: zeros
+    const int none = p.num_pages * p.page_size;     // a row outside the maps: zeros
     const uint32_t full0 = map_to(smem_u32(&c->full[0]), lead), qfull = map_to(smem_u32(&c->qfull), lead);
-    // lane's part of a slot: one box of both panels, or box bx of panel pn
-    const int pn = nb == 1 ? 0 : lane / nb, bx = nb == 1 ? 0 : lane - pn * nb;
-    const bool issues = nb == 1 ? lane == 0 : pn < 2;
-    const uint32_t dst0 = ring + pn * kPanel + bx * args.box * 128;
-    int nloads[2] = {0, 0}, own[2] = {0, 0}, nclean = 0;   // of slots warp, warp + 4
+    // a tile's cache rows come in kKeys / vbox boxes, lane l knows box l's; a
+    // slot of keys takes 128 / kbox boxes, one of values 64 / vbox boxes of
+    // each panel (or one of both)
+    const int nk = 128 / args.kbox, nv = 64 / args.vbox, kstep = args.kbox / args.vbox;
+    const int vp = nv == 1 ? 0 : lane / nv, vb = nv == 1 ? 0 : lane - vp * nv;
+    const bool vissues = nv == 1 ? lane == 0 : vp < 2;
+    const uint32_t kdst = ring + lane * args.kbox * 128, vdst = ring + vp * kPanel + vb * args.vbox * 128;
+    int nclean = 0;
     bool ok = true;
-    // lane l < 2 nb: page of the tile's box l, then its cache row
     auto fetch = [&](const Seg& g, int kt) {
-      const int key = kt * kTile + lane * args.box;
-      return lane < 2 * nb && key < g.kend ? __ldg(p.table + (size_t)g.seq * p.max_pages + key / p.page_size) : -2;
+      const int key = kt * kKeys + lane * args.vbox;
+      return lane < 4 * nv && key < g.kend ? __ldg(p.table + (size_t)g.seq * p.max_pages + key / p.page_size) : -2;
     };
     auto rows = [&](int kt, int page) {
-      if (page >= 0 && page < p.num_pages) return page * p.page_size + (kt * kTile + lane * args.box) % p.page_size;
+      if (page >= 0 && page < p.num_pages) return page * p.page_size + (kt * kKeys + lane * args.vbox) % p.page_size;
       if (page != -2) *status = kErrPage;
       return none;
     };
-    // ring use u, if it is this warp's: box rows from box0 on, panels from z
-    auto load = [&](int u, int y, int box0, int z, bool clean) {
-      if ((u & (kLoaders - 1)) != warp || !ok) return;
+    // ring use u, if it is this warp's: its slot, once free
+    auto take = [&](int u) {
+      // a slot stays with one warp, which so knows that its last use was loaded
       const int s = u % kSlots, k = u / kSlots;
-      if (k > 0 && !warp_wait(&c->empty[s], (k - 1) & 1, w)) {
-        ok = false;
+      if (s >> 1 != warp || !ok) return -1;
+      if (k > 0 && !(ok = warp_wait(&c->empty[s], (k - 1) & 1, w))) return -1;
+      return s;
+    };
+    auto load_k = [&](int u, int y, int panel) {
+      const int s = take(u);
+      if (s < 0) return;
+      if (lane == 0) {
+        expect_at(full0 + s * 8, kSlot);
+        c->loads[s] = u / kSlots + 1;
+      }
+      const int yy = __shfl_sync(~0u, y, (int)rank * 2 * nv + min(lane * kstep, 2 * nv - 1));
+      if (lane < nk) pair_tma3(kdst + s * kSlot, &maps.k, yy, panel, full0 + s * 8);
+    };
+    // 64 keys from key0 on, 128 features; y0: lane of their first box
+    auto load_v = [&](int u, const Seg& g, int key0, int y, int y0, int panel) {
+      const int s = take(u);
+      if (s < 0) return;
+      const int yy = __shfl_sync(~0u, y, y0 + vb);
+      // keys past `least` that a box brings in
+      const int least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;
+      const int loaded = min(64, (max(0, g.kend - key0) + args.vbox - 1) / args.vbox * args.vbox);
+      if (loaded == 0 || least + 1 >= key0 + loaded) {
+        if (lane == 0) {
+          expect_at(full0 + s * 8, kSlot);
+          c->loads[s] = u / kSlots + 1;
+        }
+        __syncwarp();
+        if (vissues) pair_tma3(vdst + s * kSlot, &maps.v, yy, panel + vp, full0 + s * 8);
         return;
       }
-      uint32_t bar = full0 + s * 8;
-      if (clean) {
-        // values with masked keys: the softmax warps clean them first, so
-        // they land on this CTA's own barrier
-        uint64_t* v = &c->vloc[nclean & 1];
-        bar = smem_u32(v);
-        if (lane == 0) {
-          mbar_expect_tx(v, kSlot);
-          if (leader) mbar_arrive(&c->full[s]);
-        }
-        ++nclean;
-      } else if (leader && lane == 0) {
-        mbar_expect_tx(&c->full[s], 2 * kSlot);
-      }
-      const int yy = __shfl_sync(~0u, y, box0 + bx);
-      if (issues) pair_tma3(dst0 + s * kSlot, &maps.kv, yy, z + pn, bar);
-      nloads[s >> 2] = k + 1;
-      own[s >> 2] = clean;
-    };
-    auto load_v = [&](const Seg& g, int kt, int y, int u) {
-      const bool clean = (kt + 1) * kTile > (p.mode == 3 ? g.base + g.i0 / p.G : g.base) + 1;
+      // Values of masked keys: rows no query row sees become zeros (they may
+      // hold anything), and non-finite values of the others, which would
+      // reach rows that do not see them as 0 x inf (a row that sees them has
+      // a non-finite score from the same cache row).
+      if (lane == 0) mbar_expect_tx(&c->vloc[warp], kSlot);
+      __syncwarp();
+      if (vissues) pair_tma3(vdst + s * kSlot, &maps.v, yy, panel + vp, smem_u32(&c->vloc[warp]));
+      mbar_settle(&c->vloc[warp], nclean++ & 1, status);   // the copy is on its way, whatever else gave up
+      __syncwarp();
+      for (int k = max(0, least + 1 - key0) + (lane >> 4); k < loaded; k += 2) {
+        const uint32_t at = ring + s * kSlot + ((lane >> 3) & 1) * kPanel + k * 128 + ((lane & 7) << 4);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (key0 + k < g.kend) {
+          v = lds128(at);
+          float e[8];
+          unpack8<T>(v, e);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load(u + i, y, (i >> 1) * nb, (int)rank * 4 + (i & 1) * 2, clean);
+          for (int z = 0; z < 8; ++z) e[z] = fabsf(e[z]) < INFINITY ? e[z] : 0.f;
+          v = pack8<T>(e);
+        }
+        sts128(at, v);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        arrive_at(full0 + s * 8);
+        c->loads[s] = u / kSlots + 1;
+      }
+    };
+    auto load_values = [&](const Seg& g, int kt, int y, int u) {
+#pragma unroll
+      for (int i = 0; i < kVSlots; ++i)
+        load_v(u + i, g, kt * kKeys + (i >> 1) * 64, y, (i >> 1) * nv, (int)rank * 4 + (i & 1) * 2);
     };
     Seg prev;
     int prev_kt = 0, prev_y = 0, tile = 0, qn = 0;
@@ -499,7 +573,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (warp == 0) {
         // the query rows, once the segment before has done its products
         if (qn > 0 && !warp_wait(&c->qempty, (qn - 1) & 1, w)) break;
-        if (leader && lane == 0) mbar_expect_tx(&c->qfull, 2 * (8 + ROPE) * kPanel);
+        if (lane == 0) {
+          expect_at(qfull, (8 + ROPE) * kPanel);
+          c->q_issued = qn + 1;
+        }
         __syncwarp();
         if (lane < 8 + ROPE)
           pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64, g.row0 + rank * 64,
@@ -511,121 +588,117 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (kt + 1 < g.kt1) page = fetch(g, kt + 1);   // in flight during the waits
         const int u = kpos(tile);
 #pragma unroll
-        for (int i = 0; i < kKSlots; ++i) load(u + i, y, (int)rank * nb, 2 * i, false);
-        if (tile > 0) load_v(prev, prev_kt, prev_y, u + kKSlots);
+        for (int i = 0; i < kKSlots; ++i) load_k(u + i, y, i);
+        if (tile > 0) load_values(prev, prev_kt, prev_y, u + kKSlots);
         prev = g;
         prev_kt = kt;
         prev_y = y;
       }
     }
-    if (tile > 0) load_v(prev, prev_kt, prev_y, vpos(tile - 1));
-    if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
-        c->loads[warp + 4 * i] = nloads[i];
-        c->own[warp + 4 * i] = own[i];
-      }
-      c->ncleaned[warp] = nclean;
-      if (warp == 0) c->q_issued = qn;
-    }
+    if (tile > 0) load_values(prev, prev_kt, prev_y, vpos(tile - 1));
     // the slots' last releases and the last query release have arrived: none
     // is on its way to a CTA that has ended
     if (__all_sync(~0u, !*w.abort)) {
-      for (int i = 0; i < 2; ++i)
-        if (nloads[i] > 0) warp_wait(&c->empty[warp + 4 * i], (nloads[i] - 1) & 1, w);
+      const int uses = tile * kPer;
+      for (int u = max(0, uses - kSlots); u < uses; ++u)
+        if (u % kSlots >> 1 == warp) warp_wait(&c->empty[u % kSlots], (u / kSlots) & 1, w);
       if (qn > 0) warp_wait(&c->qempty, (qn - 1) & 1, w);
     }
   } else if (work && leader && warp == 4 && lane == 0) {
-    // ---------------------------------------------------------------- S = Q K^T
-    constexpr uint32_t id = idesc_f16(kTile, kTile, Elt<T>::is_f16, false, false);
+    // ---------------------------------------------------------------- MMAs
+    // In the ring's order, S one tile ahead: S(0) S(1) PV(0) S(2) PV(1) ...
+    // One thread takes every slot in turn: two, one for each product, could
+    // meet a slot's barrier a whole phase early and mistake it for a phase
+    // late.
+    constexpr uint32_t ids = idesc_f16(kRows, kKeys, Elt<T>::is_f16, false, false);
+    constexpr uint32_t idv = idesc_f16(kRows, 256, Elt<T>::is_f16, false, true);
     const uint64_t dq = sdesc_kmajor(smem_u32(sm), 0), dk = sdesc_kmajor(ring, 0);
-    int tile = 0;
+    const uint64_t dp = sdesc_kmajor(smem_u32(sm + kOffP), 0), dv = sdesc_mnmajor(ring, 0, 64);
+    int use = 0, segs = 0, s_left = 0, pv_left = 0, pv_next = 0, pv_segs = 0, done = 0;
     bool ok = true;
-    for (int n = 0; ok; ++n) {
-      const int r = n % kSegs;
-      if (!mbar_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
-      const int len = c->seg[r].kt1 - c->seg[r].kt0;
-      const bool end = c->seg[r].kt1 == 0;
-      mbar_arrive(&c->seg_empty[r]);
-      if (end) break;
-      if (!(ok = mbar_wait_poll(&c->qfull, n & 1, w))) break;
-      for (int t = 0; t < len && ok; ++t, ++tile) {
-        const int buf = tile & 1;
-        if (tile >= 2 && !(ok = mbar_wait_poll(&c->sfree[buf], (tile / 2 - 1) & 1, w))) break;
-        tc_fence_after();
-        const uint32_t d = tmem + kColS + buf * 64;
-        int use = kpos(tile);
-#pragma unroll
-        for (int i = 0; i < kKSlots; ++i, ++use) {
-          const int s = use % kSlots;
-          if (!(ok = mbar_wait_poll(&c->full[s], (use / kSlots) & 1, w))) break;
-          tc_fence_after();
-          const uint64_t a = dq + desc_off(2 * i * kPanel), b = dk + desc_off(s * kSlot);
-          pair_mma_k64<2, 2>(d, a, b, id, i > 0);
-          if (i < 4) pair_mma_k64<2, 2>(d, a + desc_off(kPanel), b + desc_off(kPanel), id, 1);
-          pair_commit(&c->empty[s]);
-        }
-        if (ok) pair_commit(&c->sfull[buf]);
+    auto slot = [&]() {   // the next slot, full
+      const int s = use % kSlots;
+      ok = wait_bar<kSpin>(&c->full[s], (use / kSlots) & 1, w);
+      ++use;
+      tc_fence_after();
+      return s;
+    };
+    auto products_s = [&](int t) {
+      if (s_left == 0) {   // a new piece
+        const int r = segs % kSegs;
+        if (!(ok = wait_bar<false>(&c->seg_full[r], (segs / kSegs) & 1, w))) return;
+        pv_next = s_left = c->seg[r].kt1 - c->seg[r].kt0;
+        mbar_arrive(&c->seg_empty[r]);
+        if (!(ok = wait_bar<kSpin>(&c->qfull, segs & 1, w))) return;
+        ++segs;
       }
-      if (ok) pair_commit(&c->qempty);
+      if (t >= 2 && !(ok = wait_bar<kSpin>(&c->sfree[t & 1], (t / 2 - 1) & 1, w))) return;
+      const uint32_t d = tmem + kColS + (t & 1) * 128;
+#pragma unroll
+      for (int i = 0; i < kKSlots; ++i) {
+        const int s = slot();
+        if (!ok) return;
+        pair_mma_k64<2, 2>(d, dq + desc_off(i * kPanel), dk + desc_off(s * kSlot), ids, i > 0);
+        pair_commit(&c->empty[s]);
+      }
+      pair_commit(&c->sfull[t & 1]);
+      if (--s_left == 0) pair_commit(&c->qempty);
+    };
+    auto products_v = [&](int t, int len) {
+      const bool first = pv_left == 0;
+      if (first) {
+        pv_left = len;
+        if (pv_segs++ > 0 && !(ok = wait_bar<kSpin>(&c->ofree, (pv_segs - 2) & 1, w))) return;
+      }
+      if (!(ok = wait_bar<kSpin>(&c->pready, t & 1, w))) return;
+#pragma unroll
+      for (int i = 0; i < kVSlots; ++i) {
+        const int s = slot();
+        if (!ok) return;
+        pair_mma_k64<2, 128>(tmem + (i & 1) * 128, dp + desc_off((i >> 1) * kPanel), dv + desc_off(s * kSlot), idv,
+                             !first || i > 1);
+        pair_commit(&c->empty[s]);
+      }
+      pair_commit(&c->pfree);
+      --pv_left;
+      ++done;
+    };
+    products_s(0);
+    for (int t = 0; t < ntiles && ok; ++t) {
+      const int len = pv_left == 0 ? pv_next : 0;   // of the piece that tile t begins
+      if (t + 1 < ntiles) products_s(t + 1);
+      if (ok) products_v(t, len);
+    }
+    if (ok) {   // the end mark
+      const int r = segs % kSegs;
+      if (wait_bar<false>(&c->seg_full[r], (segs / kSegs) & 1, w)) mbar_arrive(&c->seg_empty[r]);
     }
     // every product done, and the other CTA's last arrivals received
-    pair_commit_own(&c->settle[0]);
-    mbar_settle(&c->settle[0], 0, status);
-    for (int t = max(0, tile - 2); t < tile && ok; ++t) ok = mbar_wait(&c->sfree[t & 1], (t >> 1) & 1, w);
-  } else if (work && leader && warp == 5 && lane == 0) {
-    // ---------------------------------------------------------------- O += P V
-    constexpr uint32_t id = idesc_f16(kTile, 256, Elt<T>::is_f16, false, true);
-    const uint64_t dp = sdesc_kmajor(smem_u32(sm + kOffP), 0), dv = sdesc_mnmajor(ring, 0, 64);
-    int tile = 0, segs = 0;
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
-      const int r = n % kSegs;
-      if (!mbar_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
-      const int len = c->seg[r].kt1 - c->seg[r].kt0;
-      const bool end = c->seg[r].kt1 == 0;
-      mbar_arrive(&c->seg_empty[r]);
-      if (end) break;
-      ++segs;
-      if (n > 0 && !(ok = mbar_wait_poll(&c->ofree, (n - 1) & 1, w))) break;
-      for (int t = 0; t < len && ok; ++t, ++tile) {
-        if (!(ok = mbar_wait_poll(&c->pready, tile & 1, w))) break;
-        tc_fence_after();
-        int use = vpos(tile);
-#pragma unroll
-        for (int i = 0; i < 4; ++i, ++use) {
-          const int s = use % kSlots;
-          if (!(ok = mbar_wait_poll(&c->full[s], (use / kSlots) & 1, w))) break;
-          tc_fence_after();
-          pair_mma_k64<2, 128>(tmem + (i & 1) * 128, dp + desc_off((i >> 1) * kPanel), dv + desc_off(s * kSlot), id,
-                               t > 0 || i > 1);
-          pair_commit(&c->empty[s]);
-        }
-        if (ok) pair_commit(&c->pfree);
-      }
+    pair_commit_own(&c->settle);
+    mbar_settle(&c->settle, 0, status);
+    if (ok) {
+      for (int t = max(0, ntiles - 2); t < ntiles && ok; ++t) ok = wait_bar<false>(&c->sfree[t & 1], (t >> 1) & 1, w);
+      if (ok) wait_bar<false>(&c->ofree, (pv_segs - 1) & 1, w);
     }
-    pair_commit_own(&c->settle[1]);
-    mbar_settle(&c->settle[1], 0, status);
-    if (ok && segs > 0) mbar_wait(&c->ofree, (segs - 1) & 1, w);
   } else if (work && warp >= 8) {
     // ---------------------------------------------------------------- softmax, epilogue
-    // Thread: row r of this CTA's 64, keys 64 h + 32 g .. + 31 of a tile, and
+    // Thread: row r of this CTA's 64, keys 128 h + 64 g .. + 63 of a tile, and
     // features 256 h + 128 g .. + 127 of O; the four threads of a row exchange
     // its max.
     const int wq = warp & 3, cg = (warp >> 2) & 1;
-    const int l = wq * 32 + lane, r = l & 63, h = l >> 6, t = tid - 256;
+    const int l = wq * 32 + lane, r = l & 63, h = l >> 6;
     const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t prow = smem_u32(sm + kOffP) + h * kPanel + r * 128;
+    const uint32_t prow = smem_u32(sm + kOffP) + (2 * h + cg) * kPanel + r * 128;
     const uint32_t pready = map_to(smem_u32(&c->pready), lead), ofree = map_to(smem_u32(&c->ofree), lead);
     const uint32_t sfree0 = map_to(smem_u32(&c->sfree[0]), lead);
-    uint64_t* xch = &c->xch[wq & 1];
-    const float scale = args.a.scale * kUnbias<T>, cs = scale * kLog2e;
-    int tile = 0, nx = 0, nbound = 0;
+    const Scale sc = score_scale<T>(args.a.scale);
+    int tile = 0, nx = 0;
     // one value of each of the row's four threads
     auto exchange = [&](float v, float* o) {
       c->xbuf[nx & 1][2 * h + cg][r] = v;
       __syncwarp();
-      if (lane == 0) mbar_arrive(xch);
-      if (!warp_wait(xch, nx & 1, w)) return false;
+      if (lane == 0) mbar_arrive(&c->xch[wq & 1]);
+      if (!warp_wait(&c->xch[wq & 1], nx & 1, w)) return false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = c->xbuf[nx & 1][i][r];
       ++nx;
@@ -640,56 +713,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&c->seg_empty[sr]);
       if (g.kt1 == 0) break;
       const int myrow = (int)rank * 64 + r;
-      const int limit = p.mode == 3 ? g.base + (g.i0 + myrow) / p.G : g.base;   // last key this row sees
-      const int least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;             // ... the tile's first row
-      // the max so far and the one P is relative to, times scale log2(e)
+      const int least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;   // last key the tile's first row sees
+      // ... and this row, counted from the thread's first column of tile 0
+      const int last = min(p.mode == 3 ? g.base + (g.i0 + myrow) / p.G : g.base, g.kend - 1) - (h * 128 + cg * 64);
+      // the max so far and the one P is relative to (scores before the scale)
       float mtop = -INFINITY, mref = -INFINITY, lsum = 0.f;
       for (int kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
-        const int buf = tile & 1;
-        if (!(ok = warp_wait(&c->sfull[buf], (tile >> 1) & 1, w))) break;
+        if (!(ok = warp_wait(&c->sfull[tile & 1], (tile >> 1) & 1, w))) break;
         tc_fence_after();
+        const bool edge = (kt + 1) * kKeys > least + 1;
+        // half a thread's scores; they are read twice, for the max and for P
         float x[32];
-        tmem_ld32(tq + kColS + buf * 64 + cg * 32, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(sfree0 + buf * 8);
-        const bool edge = (kt + 1) * kTile > least + 1;
+        auto scores = [&](int half) {
+          tmem_ld32(tq + kColS + (tile & 1) * 128 + cg * 64 + half * 32, x);
+          if (sc.negative) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] *= cs;
-        if (edge) {
-          const int see = min(limit, g.kend - 1) - (kt * kTile + h * 64 + cg * 32);   // last column this row sees
+            for (int i = 0; i < 32; ++i) x[i] = -x[i];
+          }
+          if (edge) {
+            const int see = last - kt * kKeys - half * 32;   // last column this row sees
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i > see) x[i] = -INFINITY;
+            for (int i = 0; i < 32; ++i)
+              if (i > see) x[i] = -INFINITY;
+          }
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          scores(half);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(x[i], x[i + 1]));
         }
         float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = x[i];
-#pragma unroll
-          for (int q = 4; q < 32; q += 4) mx[i] = fmaxf(mx[i], x[i + q]);
-        }
-        if (!(ok = exchange(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mx))) break;
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (!(ok = exchange(top, mx))) break;
+        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         mtop = fmaxf(mtop, top);
         // a stale reference keeps P below 2^8, which both types hold as
         // exactly as values below one; O is rescaled only beyond that
-        const bool raise = top > mref + kRaise;
+        const bool raise = (top - mref) * sc.log2 > kRaise;
         float f = 1.f;
         if (raise) {
-          f = ex2(mref - mtop);
+          f = ex2((mref - mtop) * sc.log2);
           mref = mtop;
           lsum *= f;
         }
-        const float ref = mref == -INFINITY ? 0.f : mref;
-        uint32_t pk[16];
+        const float ref = mref == -INFINITY ? 0.f : mref * sc.log2;
+        uint32_t pk[32];
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = ex2(x[2 * i] - ref), b = ex2(x[2 * i + 1] - ref);
-          s0 += a;
-          s1 += b;
-          pk[i] = Elt<T>::pack(a, b);
+        for (int half = 0; half < 2; ++half) {
+          scores(half);
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(sfree0 + (tile & 1) * 8);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = ex2(fmaf(x[2 * i], sc.log2, -ref)), b = ex2(fmaf(x[2 * i + 1], sc.log2, -ref));
+            s0 += a;
+            s1 += b;
+            pk[half * 16 + i] = Elt<T>::pack(a, b);
+          }
         }
         lsum += s0 + s1;
         // P and O belong to the products of the tile before until they end
@@ -705,40 +790,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sts128(prow + (((cg * 4 + i) ^ (r & 7)) << 4),
-                 make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
-        if (edge) {
-          // values of masked keys: rows no query row sees become zeros (they
-          // may hold anything), and non-finite values of the others, which
-          // would reach rows that do not see them as 0 x inf (a row that
-          // sees them has a non-finite score from the same cache row)
-          if (!(ok = warp_wait(&c->vloc[nbound & 1], (nbound >> 1) & 1, w))) break;
-          ++nbound;
-          const int use = vpos(tile);
-          for (int i = 0; i < 4; ++i) {
-            const int k = t & 63, key = kt * kTile + (i >> 1) * 64 + k;
-            if (key <= least) continue;
-            const uint32_t a = ring + ((use + i) % kSlots) * kSlot + ((t >> 6) & 1) * kPanel + k * 128;
-            for (int q = (t >> 7) * 4; q < (t >> 7) * 4 + 4; ++q) {
-              const uint32_t at = a + ((q ^ (k & 7)) << 4);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (key < g.kend) {
-                v = lds128(at);
-                float e[8];
-                unpack8<T>(v, e);
-                bool fine = true;
-#pragma unroll
-                for (int z = 0; z < 8; ++z) fine &= fabsf(e[z]) < INFINITY;
-                if (fine) continue;
-#pragma unroll
-                for (int z = 0; z < 8; ++z) e[z] = fabsf(e[z]) < INFINITY ? e[z] : 0.f;
-                v = pack8<T>(e);
-              }
-              sts128(at, v);
-            }
-          }
-        }
+        for (int i = 0; i < 8; ++i)
+          sts128(prow + ((i ^ (r & 7)) << 4), make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -768,11 +821,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (mine && h == 0 && cg == 0) {
-          args.a.smax[row] = mtop * kLn2;
-          args.a.ssum[row] = lsum > 0.f ? lsum * ex2(mref - mtop) : lsum;
+          args.a.smax[row] = mtop == -INFINITY ? mtop : mtop * sc.scale;
+          args.a.ssum[row] = lsum > 0.f ? lsum * ex2((mref - mtop) * sc.log2) : lsum;
         }
       } else {
-        float* dst = args.part + ((size_t)g.slot * kTile + myrow) * 512 + col;
+        float* dst = args.part + ((size_t)g.slot * kRows + myrow) * 512 + col;
         for (int q = 0; q < 128; q += 32) {
           float o[32];
           tmem_ld32(tq + cg * 128 + q, o);
@@ -784,7 +837,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (mine && h == 0 && cg == 0)
-          args.stats[g.slot * kTile + myrow] = make_float4(mtop, mref, lsum, 0.f);
+          args.stats[g.slot * kRows + myrow] = make_float4(mtop, mref, lsum, 0.f);
       }
       tc_fence_before();
       __syncwarp();
@@ -798,33 +851,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0 && (c->abort || load_from(map_to(smem_u32(&c->abort), rank ^ 1)))) {
     // Loads on their way.  The first CTA's barriers count those of both, and
     // the two may have stopped at different places (a slot's uses at most one
-    // apart): every started phase gets what it lacks, then the last phase of
-    // every slot is waited for.
+    // apart): a phase that one of them has begun gets the other's arrival,
+    // then the last phase of every slot is waited for.
     if (leader) {
-      for (int i = 0; i < kSlots; ++i) {
-        const int mine = c->loads[i], peer = load_from(map_to(smem_u32(&c->loads[i]), 1));
-        const int peer_own = load_from(map_to(smem_u32(&c->own[i]), 1));
-        int phases = mine;
-        if (mine > peer && !c->own[i]) complete_tx(&c->full[i], kSlot);
-        if (peer > mine && !peer_own) {
-          mbar_expect_tx(&c->full[i], kSlot);
-          phases = peer;
-        }
-        if (phases > 0) mbar_settle(&c->full[i], (phases - 1) & 1, status);
-      }
-      const int q = c->q_issued, pq = load_from(map_to(smem_u32(&c->q_issued), 1));
-      if (q > pq) complete_tx(&c->qfull, (8 + ROPE) * kPanel);
-      if (q < pq) mbar_expect_tx(&c->qfull, (8 + ROPE) * kPanel);
-      if (max(q, pq) > 0) mbar_settle(&c->qfull, (max(q, pq) - 1) & 1, status);
-    }
-    // vloc: the tiles some loader has begun and others have not
-    int most = 0;
-    for (int i = 0; i < kLoaders; ++i) most = max(most, c->ncleaned[i]);
-    for (int m = max(0, most - 2); m < most; ++m) {
-      int n = 0;
-      for (int i = 0; i < kLoaders; ++i) n += c->ncleaned[i] > m;
-      if (n < kLoaders) mbar_arrive_n(&c->vloc[m & 1], kLoaders - n);
-      mbar_settle(&c->vloc[m & 1], (m >> 1) & 1, status);
+      auto finish = [&](uint64_t* bar, int mine, int peer) {
+        if (mine != peer) mbar_arrive(bar);
+        if (max(mine, peer) > 0) mbar_settle(bar, (max(mine, peer) - 1) & 1, status);
+      };
+      for (int i = 0; i < kSlots; ++i) finish(&c->full[i], c->loads[i], load_from(map_to(smem_u32(&c->loads[i]), 1)));
+      finish(&c->qfull, c->q_issued, load_from(map_to(smem_u32(&c->q_issued), 1)));
     }
   }
   cluster_sync();
@@ -852,11 +887,12 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
   if (!pc.valid || !pc.first) return;
   const int r = blockIdx.y * 2 + (threadIdx.x >> 7), col = (threadIdx.x & 127) * 4;
   if (r >= pc.nrows) return;
+  const Scale sc = score_scale<T>(args.a.scale);
   // pieces: this one, then every following pair's first, up to the tile's end
   float m = -INFINITY;
   int n = 1;
   for (int s = slot;;) {
-    m = fmaxf(m, args.stats[s * kTile + r].x);
+    m = fmaxf(m, args.stats[s * kRows + r].x);
     if (args.piece[s].last) break;
     // a call that gave up a wait leaves the chain without its end
     if (pair + n >= args.max_pairs || !args.piece[2 * (pair + n)].valid) break;
@@ -865,11 +901,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
   float lsum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0, s = slot; i < n; ++i) {
-    const float4 mm = args.stats[s * kTile + r];
+    const float4 mm = args.stats[s * kRows + r];
     const float li = mm.z;
     if (mm.x != -INFINITY || li != 0.f) {
-      const float f = ex2(mm.y - m);
-      const float4 v = *reinterpret_cast<const float4*>(args.part + ((size_t)s * kTile + r) * 512 + col);
+      const float f = ex2((mm.y - m) * sc.log2);
+      const float4 v = *reinterpret_cast<const float4*>(args.part + ((size_t)s * kRows + r) * 512 + col);
       lsum += li * f;
       o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
     }
@@ -882,7 +918,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
   out.y = Elt<T>::pack(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>((T*)args.a.out + row * 512 + col) = out;
   if (col == 0) {
-    args.a.smax[row] = m * kLn2;
+    args.a.smax[row] = m == -INFINITY ? m : m * sc.scale;
     args.a.ssum[row] = lsum;
   }
 }
@@ -891,11 +927,11 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr size_t kOffStatus = 256;
 const size_t kOffPiece = kOffStatus + up256(kMaxSms * sizeof(int));
 const size_t kOffStats = kOffPiece + up256(2 * kMaxPairs * sizeof(Piece));
-const size_t kOffPart = kOffStats + up256(2 * kMaxPairs * kTile * sizeof(float4));
+const size_t kOffPart = kOffStats + up256(2 * kMaxPairs * kRows * sizeof(float4));
 
 }  // namespace
 
-size_t paged_workspace(const Paged&) { return kOffPart + (size_t)2 * kMaxPairs * kTile * 512 * sizeof(float); }
+size_t paged_workspace(const Paged&) { return kOffPart + (size_t)2 * kMaxPairs * kRows * 512 * sizeof(float); }
 
 template <typename T>
 cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
@@ -903,17 +939,19 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   Args g;
   g.a = a;
   g.max_pairs = nsm / 2;
-  g.box = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
+  g.kbox = p.page_size % 128 == 0 ? 128 : p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
+  g.vbox = g.kbox < 64 ? g.kbox : 64;
   g.status = reinterpret_cast<int*>(a.ws + kOffStatus);
   g.piece = reinterpret_cast<Piece*>(a.ws + kOffPiece);
   g.stats = reinterpret_cast<float4*>(a.ws + kOffStats);
   g.part = reinterpret_cast<float*>(a.ws + kOffPart);
   Maps2 m;
   const bool f16 = Elt<T>::is_f16, rope = p.row == 576;
-  const uint64_t rows = (uint64_t)p.T * p.G;
+  const uint64_t rows = (uint64_t)p.T * p.G, cached = (uint64_t)p.num_pages * p.page_size;
   if (!encode_map2d(&m.q, f16, a.q, 512, rows, 64) ||
       !encode_map2d(&m.qr, f16, rope ? a.qr : a.q, rope ? 64 : 512, rows, 64) ||
-      !encode_map_panels(&m.kv, f16, a.cache, p.row, (uint64_t)p.num_pages * p.page_size, g.box, g.box == 64 ? 2 : 1))
+      !encode_map_panels(&m.k, f16, a.cache, p.row, cached, g.kbox, 1) ||
+      !encode_map_panels(&m.v, f16, a.cache, p.row, cached, g.vbox, g.vbox == 64 ? 2 : 1))
     return cudaErrorInvalidValue;
   auto kern = rope ? paged_kernel<T, true> : paged_kernel<T, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
@@ -921,7 +959,7 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   kern<<<2 * g.max_pairs, kThreads, kSmem, st>>>(m, g);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<T><<<dim3(g.max_pairs, kTile / 2), 256, 0, st>>>(g);
+  paged_merge_kernel<T><<<dim3(g.max_pairs, kRows / 2), 256, 0, st>>>(g);
   return cudaGetLastError();
 }
 
