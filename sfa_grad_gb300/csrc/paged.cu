@@ -44,7 +44,6 @@ constexpr int kSegs = 4;                    // work descriptors in flight
 constexpr int kMinUnits = 1;                // key tiles a pair takes at least
 constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
 constexpr int kMaxPairs = kMaxSms / 2;
-constexpr bool kSpin = true;                // the MMA issuers poll
 // How scores are scaled.  The sign is taken out first, so that a larger score
 // is a larger weight, and a scale of zero becomes one that leaves every finite
 // score zero and a masked one -inf.
@@ -137,61 +136,81 @@ __device__ __forceinline__ int load_from(uint32_t cluster_addr) {
   return v;
 }
 // Bounded waits of this kernel: as common.cuh's, with the limit in SM clocks
-// (a read of the global timer costs more than most waits here last) and looked
-// at every 64 polls.
+// (a read of the global timer costs more than most waits here last).
 struct Limit {
   volatile int* abort;
   int* gerr;
   long long clocks;
 };
-template <bool POLL>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Limit& w) {
   const uint32_t a = smem_u32(bar);
-  if (POLL ? mbar_poll(a, parity) : mbar_test(a, parity)) return true;
+  if (mbar_test(a, parity)) return true;
   const long long t0 = clock64();
-  for (uint32_t it = 1;; ++it) {
-    if (POLL ? mbar_poll(a, parity) : mbar_test(a, parity)) return true;
-    if (!POLL || (it & 63u) == 0) {
-      if (*w.abort) return false;
-      if (clock64() - t0 > w.clocks) break;
+  while (!mbar_test(a, parity)) {
+    if (*w.abort) return false;
+    if (clock64() - t0 > w.clocks) {
+      *w.abort = 1;
+      atomicExch(w.gerr, kErrTimeout);
+      return false;
     }
   }
-  *w.abort = 1;
-  atomicExch(w.gerr, kErrTimeout);
-  return false;
+  return true;
 }
 // Wait by a whole warp: one answer for all lanes, and the lanes together again
 // before what follows (tcgen05.ld and .st want a converged warp).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Limit& w) {
-  const bool ok = wait_bar<false>(bar, parity, w);
+  const bool ok = wait_bar(bar, parity, w);
   return __all_sync(~0u, ok);
 }
 
 // ------------------------------------------------------------------ tensor cores, both SMs of the pair
+// The MMA warp runs as a whole and one elected lane issues: descriptors then
+// stay in uniform registers.  Four MMAs of N = 256 from a single-lane branch
+// measured 650 clk (their descriptors move to uniform registers one by one),
+// from a converged warp 257, the tensor core's own time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
+}
+// Steps 0..2, and 3, of a contraction over 64 elements; SA, SB: a step in
+// encoded descriptor units.
 template <uint32_t SA, uint32_t SB>
-__device__ __forceinline__ void pair_mma_k64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc_first) {
+__device__ __forceinline__ void pair_mma_first3(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t acc_first) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %5, %6, %3, 1;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %7, %8, %3, 1;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %9, %10, %3, 1;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc_first), "l"(a + SA), "l"(b + SB), "l"(a + 2 * SA), "l"(b + 2 * SB),
-      "l"(a + 3 * SA), "l"(b + 3 * SB)
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %9, 0;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %5, %6, %3, 1;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %7, %8, %3, 1;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc_first), "l"(a + SA), "l"(b + SB), "l"(a + 2 * SA), "l"(b + 2 * SB), "r"(el)
       : "memory");
 }
-// Arrives on `bar` of both CTAs once this thread's MMAs so far are complete.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+template <uint32_t SA, uint32_t SB>
+__device__ __forceinline__ void pair_mma_last(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %4, 0;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, 1;\n}" ::"r"(d),
+      "l"(a + 3 * SA), "l"(b + 3 * SB), "r"(idesc), "r"(el)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once the elected lane's MMAs so far are
+// complete.
+__device__ __forceinline__ void pair_commit(uint32_t el, uint64_t* bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)3), "r"(el)
       : "memory");
 }
 // ... of this CTA only.
-__device__ __forceinline__ void pair_commit_own(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void pair_commit_own(uint32_t el, uint64_t* bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+      "r"(el)
+      : "memory");
 }
 // A box into this CTA's shared memory; the bytes count on `bar`, a barrier of
 // either CTA (cluster address).
@@ -209,17 +228,15 @@ __device__ __forceinline__ void pair_tma3(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-  uint32_t r[32];
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  uint32_t r[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -555,47 +572,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         c->loads[s] = u / kSlots + 1;
       }
     };
-    auto load_values = [&](const Seg& g, int kt, int y, int u) {
-#pragma unroll
-      for (int i = 0; i < kVSlots; ++i)
-        load_v(u + i, g, kt * kKeys + (i >> 1) * 64, y, (i >> 1) * nv, (int)rank * 4 + (i & 1) * 2);
-    };
-    Seg prev;
-    int prev_kt = 0, prev_y = 0, tile = 0, qn = 0;
-    for (int n = 0; ok; ++n) {
-      const int r = n % kSegs;
-      if (!warp_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
-      const Seg g = c->seg[r];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->seg_empty[r]);
-      if (g.kt1 == 0) break;
-      int page = fetch(g, g.kt0);
-      if (warp == 0) {
-        // the query rows, once the segment before has done its products
-        if (qn > 0 && !warp_wait(&c->qempty, (qn - 1) & 1, w)) break;
-        if (lane == 0) {
-          expect_at(qfull, (8 + ROPE) * kPanel);
-          c->q_issued = qn + 1;
-        }
+    // one copy of the code for every tile: keys of the next, values of the last
+    Seg g, prev;
+    g.kt1 = 0;
+    int kt = 0, page = -2, prev_kt = 0, prev_y = 0, tile = 0, n = 0, qn = 0;
+    for (bool more = true; ok;) {
+      if (kt >= g.kt1) {   // a new piece
+        const int r = n % kSegs;
+        if (!warp_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
+        g = c->seg[r];
         __syncwarp();
-        if (lane < 8 + ROPE)
-          pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64, g.row0 + rank * 64,
-                   qfull);
-        ++qn;
+        if (lane == 0) mbar_arrive(&c->seg_empty[r]);
+        ++n;
+        more = g.kt1 != 0;
+        kt = g.kt0;
+        if (more) page = fetch(g, kt);
+        if (more && warp == 0) {
+          // the query rows, once the segment before has done its products
+          if (qn > 0 && !warp_wait(&c->qempty, (qn - 1) & 1, w)) break;
+          if (lane == 0) {
+            expect_at(qfull, (8 + ROPE) * kPanel);
+            c->q_issued = qn + 1;
+          }
+          __syncwarp();
+          if (lane < 8 + ROPE)
+            pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64, g.row0 + rank * 64,
+                     qfull);
+          ++qn;
+        }
       }
-      for (int kt = g.kt0; kt < g.kt1 && ok; ++kt, ++tile) {
-        const int y = rows(kt, page);
+      int y = none;
+      if (more) {
+        y = rows(kt, page);
         if (kt + 1 < g.kt1) page = fetch(g, kt + 1);   // in flight during the waits
         const int u = kpos(tile);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kKSlots; ++i) load_k(u + i, y, i);
-        if (tile > 0) load_values(prev, prev_kt, prev_y, u + kKSlots);
-        prev = g;
-        prev_kt = kt;
-        prev_y = y;
       }
+      if (tile > 0) {
+        const int u = vpos(tile - 1);
+#pragma unroll 1
+        for (int i = 0; i < kVSlots; ++i)
+          load_v(u + i, prev, prev_kt * kKeys + (i >> 1) * 64, prev_y, (i >> 1) * nv, (int)rank * 4 + (i & 1) * 2);
+      }
+      if (!more) break;
+      prev = g;
+      prev_kt = kt++;
+      prev_y = y;
+      ++tile;
     }
-    if (tile > 0) load_values(prev, prev_kt, prev_y, vpos(tile - 1));
     // the slots' last releases and the last query release have arrived: none
     // is on its way to a CTA that has ended
     if (__all_sync(~0u, !*w.abort)) {
@@ -604,82 +629,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (u % kSlots >> 1 == warp) warp_wait(&c->empty[u % kSlots], (u / kSlots) & 1, w);
       if (qn > 0) warp_wait(&c->qempty, (qn - 1) & 1, w);
     }
-  } else if (work && leader && warp == 4 && lane == 0) {
+  } else if (work && leader && warp == 4) {
     // ---------------------------------------------------------------- MMAs
     // In the ring's order, S one tile ahead: S(0) S(1) PV(0) S(2) PV(1) ...
-    // One thread takes every slot in turn: two, one for each product, could
+    // One warp takes every slot in turn: two, one for each product, could
     // meet a slot's barrier a whole phase early and mistake it for a phase
-    // late.
+    // late.  The next slot's barrier is looked at before a slot's last MMA,
+    // while the tensor core still has the others to do.
+    const uint32_t el = elect_one();
     constexpr uint32_t ids = idesc_f16(kRows, kKeys, Elt<T>::is_f16, false, false);
     constexpr uint32_t idv = idesc_f16(kRows, 256, Elt<T>::is_f16, false, true);
     const uint64_t dq = sdesc_kmajor(smem_u32(sm), 0), dk = sdesc_kmajor(ring, 0);
     const uint64_t dp = sdesc_kmajor(smem_u32(sm + kOffP), 0), dv = sdesc_mnmajor(ring, 0, 64);
-    int use = 0, segs = 0, s_left = 0, pv_left = 0, pv_next = 0, pv_segs = 0, done = 0;
+    int use = 0, segs = 0, s_left = 0, pv_left = 0, pv_next = 0, pv_segs = 0;
     bool ok = true;
+    bool ready = false;   // the next slot is known to be full
     auto slot = [&]() {   // the next slot, full
       const int s = use % kSlots;
-      ok = wait_bar<kSpin>(&c->full[s], (use / kSlots) & 1, w);
+      if (!ready) ok = warp_wait(&c->full[s], (use / kSlots) & 1, w);
       ++use;
-      tc_fence_after();
       return s;
+    };
+    auto peek = [&]() {
+      ready = __all_sync(~0u, mbar_poll(smem_u32(&c->full[use % kSlots]), (use / kSlots) & 1));
     };
     auto products_s = [&](int t) {
       if (s_left == 0) {   // a new piece
         const int r = segs % kSegs;
-        if (!(ok = wait_bar<false>(&c->seg_full[r], (segs / kSegs) & 1, w))) return;
+        if (!(ok = warp_wait(&c->seg_full[r], (segs / kSegs) & 1, w))) return;
         pv_next = s_left = c->seg[r].kt1 - c->seg[r].kt0;
-        mbar_arrive(&c->seg_empty[r]);
-        if (!(ok = wait_bar<kSpin>(&c->qfull, segs & 1, w))) return;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->seg_empty[r]);
+        if (!(ok = warp_wait(&c->qfull, segs & 1, w))) return;
         ++segs;
       }
-      if (t >= 2 && !(ok = wait_bar<kSpin>(&c->sfree[t & 1], (t / 2 - 1) & 1, w))) return;
+      if (t >= 2 && !(ok = warp_wait(&c->sfree[t & 1], (t / 2 - 1) & 1, w))) return;
+      tc_fence_after();   // the softmax warps' reads of this S buffer
       const uint32_t d = tmem + kColS + (t & 1) * 128;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < kKSlots; ++i) {
         const int s = slot();
         if (!ok) return;
-        pair_mma_k64<2, 2>(d, dq + desc_off(i * kPanel), dk + desc_off(s * kSlot), ids, i > 0);
-        pair_commit(&c->empty[s]);
+        const uint64_t a = dq + desc_off(i * kPanel), b = dk + desc_off(s * kSlot);
+        pair_mma_first3<2, 2>(el, d, a, b, ids, i > 0);
+        peek();
+        pair_mma_last<2, 2>(el, d, a, b, ids);
+        pair_commit(el, &c->empty[s]);
       }
-      pair_commit(&c->sfull[t & 1]);
-      if (--s_left == 0) pair_commit(&c->qempty);
+      pair_commit(el, &c->sfull[t & 1]);
+      if (--s_left == 0) pair_commit(el, &c->qempty);
     };
     auto products_v = [&](int t, int len) {
       const bool first = pv_left == 0;
       if (first) {
         pv_left = len;
-        if (pv_segs++ > 0 && !(ok = wait_bar<kSpin>(&c->ofree, (pv_segs - 2) & 1, w))) return;
+        if (pv_segs++ > 0 && !(ok = warp_wait(&c->ofree, (pv_segs - 2) & 1, w))) return;
       }
-      if (!(ok = wait_bar<kSpin>(&c->pready, t & 1, w))) return;
-#pragma unroll
+      if (!(ok = warp_wait(&c->pready, t & 1, w))) return;
+      tc_fence_after();   // ... and reads and rescaling of O
+#pragma unroll 1
       for (int i = 0; i < kVSlots; ++i) {
         const int s = slot();
         if (!ok) return;
-        pair_mma_k64<2, 128>(tmem + (i & 1) * 128, dp + desc_off((i >> 1) * kPanel), dv + desc_off(s * kSlot), idv,
-                             !first || i > 1);
-        pair_commit(&c->empty[s]);
+        const uint32_t d = tmem + (i & 1) * 128;
+        const uint64_t a = dp + desc_off((i >> 1) * kPanel), b = dv + desc_off(s * kSlot);
+        pair_mma_first3<2, 128>(el, d, a, b, idv, !first || i > 1);
+        peek();
+        pair_mma_last<2, 128>(el, d, a, b, idv);
+        pair_commit(el, &c->empty[s]);
       }
-      pair_commit(&c->pfree);
+      pair_commit(el, &c->pfree);
       --pv_left;
-      ++done;
     };
-    products_s(0);
-    for (int t = 0; t < ntiles && ok; ++t) {
+    for (int t = -1; t < ntiles && ok; ++t) {
       const int len = pv_left == 0 ? pv_next : 0;   // of the piece that tile t begins
       if (t + 1 < ntiles) products_s(t + 1);
-      if (ok) products_v(t, len);
+      if (t >= 0 && ok) products_v(t, len);
     }
     if (ok) {   // the end mark
       const int r = segs % kSegs;
-      if (wait_bar<false>(&c->seg_full[r], (segs / kSegs) & 1, w)) mbar_arrive(&c->seg_empty[r]);
+      ok = warp_wait(&c->seg_full[r], (segs / kSegs) & 1, w);
+      if (ok && lane == 0) mbar_arrive(&c->seg_empty[r]);
     }
     // every product done, and the other CTA's last arrivals received
-    pair_commit_own(&c->settle);
+    pair_commit_own(el, &c->settle);
     mbar_settle(&c->settle, 0, status);
-    if (ok) {
-      for (int t = max(0, ntiles - 2); t < ntiles && ok; ++t) ok = wait_bar<false>(&c->sfree[t & 1], (t >> 1) & 1, w);
-      if (ok) wait_bar<false>(&c->ofree, (pv_segs - 1) & 1, w);
-    }
+    __syncwarp();
+    for (int t = max(0, ntiles - 2); t < ntiles && ok; ++t) ok = warp_wait(&c->sfree[t & 1], (t >> 1) & 1, w);
+    if (ok) warp_wait(&c->ofree, (pv_segs - 1) & 1, w);
   } else if (work && warp >= 8) {
     // ---------------------------------------------------------------- softmax, epilogue
     // Thread: row r of this CTA's 64, keys 128 h + 64 g .. + 63 of a tile, and
@@ -738,7 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         };
         float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           scores(half);
 #pragma unroll
@@ -758,9 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           lsum *= f;
         }
         const float ref = mref == -INFINITY ? 0.f : mref * sc.log2;
-        uint32_t pk[32];
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           scores(half);
           if (half == 1) {
@@ -768,30 +803,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_at(sfree0 + (tile & 1) * 8);
           }
+          uint32_t pk[16];
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float a = ex2(fmaf(x[2 * i], sc.log2, -ref)), b = ex2(fmaf(x[2 * i + 1], sc.log2, -ref));
             s0 += a;
             s1 += b;
-            pk[half * 16 + i] = Elt<T>::pack(a, b);
+            pk[i] = Elt<T>::pack(a, b);
           }
-        }
-        lsum += s0 + s1;
-        // P and O belong to the products of the tile before until they end
-        if (tile > 0 && !(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
-        if (kt > g.kt0 && __any_sync(~0u, raise)) {
-          tc_fence_after();
-          for (int q = 0; q < 128; q += 32) {
-            float o[32];
-            tmem_ld32(tq + cg * 128 + q, o);
+          lsum += s0 + s1;
+          // P and O belong to the products of the tile before until they end
+          if (half == 0) {
+            if (tile > 0 && !(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
+            if (kt > g.kt0 && __any_sync(~0u, raise)) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < 128; q += 16) {
+                float o[16];
+                tmem_ld16(tq + cg * 128 + q, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(tq + cg * 128 + q, o);
+                for (int i = 0; i < 16; ++i) o[i] *= f;
+                tmem_st16(tq + cg * 128 + q, o);
+              }
+            }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          sts128(prow + ((i ^ (r & 7)) << 4), make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
+          for (int i = 0; i < 4; ++i)
+            sts128(prow + (((half * 4 + i) ^ (r & 7)) << 4),
+                   make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
+        }
+        if (!ok) break;
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -806,38 +848,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool mine = myrow < g.nrows;
       const size_t row = (size_t)g.row0 + myrow;
       const int col = h * 256 + cg * 128;
-      if (g.slot < 0) {
-        const float inv = lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
-        T* dst = (T*)args.a.out + row * 512 + col;
-        for (int q = 0; q < 128; q += 32) {
-          float o[32];
-          tmem_ld32(tq + cg * 128 + q, o);
-          if (mine) {
+      const bool whole = g.slot < 0;
+      const float inv = !whole ? 1.f : lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
+      T* dst = (T*)args.a.out + row * 512 + col;
+      float* part = args.part + ((size_t)max(g.slot, 0) * kRows + myrow) * 512 + col;
+#pragma unroll 1
+      for (int q = 0; q < 128; q += 32) {
+        float o[32];
+        tmem_ld32(tq + cg * 128 + q, o);
+        if (mine && whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= inv;
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + q)[i] = pack8<T>(o + 8 * i);
-          }
-          __syncwarp();
+          for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + q)[i] = pack8<T>(o + 8 * i);
+        } else if (mine) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            reinterpret_cast<float4*>(part + q)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
-        if (mine && h == 0 && cg == 0) {
+        __syncwarp();
+      }
+      if (mine && h == 0 && cg == 0) {
+        if (whole) {
           args.a.smax[row] = mtop == -INFINITY ? mtop : mtop * sc.scale;
           args.a.ssum[row] = lsum > 0.f ? lsum * ex2((mref - mtop) * sc.log2) : lsum;
-        }
-      } else {
-        float* dst = args.part + ((size_t)g.slot * kRows + myrow) * 512 + col;
-        for (int q = 0; q < 128; q += 32) {
-          float o[32];
-          tmem_ld32(tq + cg * 128 + q, o);
-          if (mine) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(dst + q)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-          __syncwarp();
-        }
-        if (mine && h == 0 && cg == 0)
+        } else {
           args.stats[g.slot * kRows + myrow] = make_float4(mtop, mref, lsum, 0.f);
+        }
       }
       tc_fence_before();
       __syncwarp();
