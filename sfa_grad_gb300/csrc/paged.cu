@@ -666,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (t >= 2 && !(ok = warp_wait(&c->sfree[t & 1], (t / 2 - 1) & 1, w))) return;
       tc_fence_after();   // the softmax warps' reads of this S buffer
       const uint32_t d = tmem + kColS + (t & 1) * 128;
-#pragma unroll 1
+#pragma unroll 3
       for (int i = 0; i < kKSlots; ++i) {
         const int s = slot();
         if (!ok) return;
@@ -687,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!(ok = warp_wait(&c->pready, t & 1, w))) return;
       tc_fence_after();   // ... and reads and rescaling of O
-#pragma unroll 1
+#pragma unroll 2
       for (int i = 0; i < kVSlots; ++i) {
         const int s = slot();
         if (!ok) return;
@@ -849,23 +849,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const size_t row = (size_t)g.row0 + myrow;
       const int col = h * 256 + cg * 128;
       const bool whole = g.slot < 0;
-      const float inv = !whole ? 1.f : lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
-      T* dst = (T*)args.a.out + row * 512 + col;
-      float* part = args.part + ((size_t)max(g.slot, 0) * kRows + myrow) * 512 + col;
-#pragma unroll 1
-      for (int q = 0; q < 128; q += 32) {
-        float o[32];
-        tmem_ld32(tq + cg * 128 + q, o);
-        if (mine && whole) {
+      const float inv = lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
+      // O leaves through the 4 KB of the P buffer that this warp alone writes,
+      // so that a store covers 128 bytes of 4 rows instead of 16 bytes of 32
+      const uint32_t stage = prow - lane * 128;
+      const int row0 = (int)rank * 64 + (wq & 1) * 32;   // the warp's first row
+      char* dst = whole ? (char*)args.a.out + ((size_t)(g.row0 + row0) * 512 + col) * sizeof(T)
+                        : (char*)(args.part + ((size_t)g.slot * kRows + row0) * 512 + col);
+      const int stride = 512 * (whole ? (int)sizeof(T) : 4);
+      for (int q = 0; q < 128;) {
+        uint4 v[8];   // 128 bytes of the thread's row
+        if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= inv;
+          for (int half = 0; half < 2; ++half) {
+            float o[32];
+            tmem_ld32(tq + cg * 128 + q + half * 32, o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst + q)[i] = pack8<T>(o + 8 * i);
-        } else if (mine) {
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[half * 4 + i] = pack8<T>(o + 8 * i);
+          }
+          q += 64;
+        } else {
+          float o[32];
+          tmem_ld32(tq + cg * 128 + q, o);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(part + q)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            v[i] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                              __float_as_uint(o[4 * i + 3]));
+          q += 32;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sts128(stage + lane * 128 + ((i ^ (lane & 7)) << 4), v[i]);
+        __syncwarp();
+        const int piece = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = i * 4 + (lane >> 3);
+          const uint4 u = lds128(stage + k * 128 + ((piece ^ (k & 7)) << 4));
+          if (row0 + k < g.nrows) *reinterpret_cast<uint4*>(dst + (size_t)k * stride + piece * 16) = u;
+        }
+        dst += 128;
         __syncwarp();
       }
       if (mine && h == 0 && cg == 0) {
@@ -905,58 +929,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Pieces of row tiles: the CTAs (x, y) of the pair x whose last piece begins a
-// row tile take the rows 2 y, 2 y + 1 of it and add that tile's pieces in
-// order.  CTA (0, 0) also sums up the error words.
+// Pieces of row tiles, added in order.  The pair whose last piece begins a row
+// tile owns it.  A tile of few pieces takes a warp a row, one of many (few
+// rows over a long cache) a block a row, its warps a share of the pieces each.
+// Block 0 also sums up the error words.
+constexpr int kMergeThreads = 512;
+constexpr int kManyPieces = 16;
+
 template <typename T>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const Args args) {
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    int e = 0;
-    for (int i = threadIdx.x; i < 2 * args.max_pairs; i += 256) e = max(e, args.status[i]);
-    e = __syncthreads_or(e == 1) ? 1 : __syncthreads_or(e == kErrSeqLens) ? kErrSeqLens
-        : __syncthreads_or(e == kErrPage) ? kErrPage : 0;
-    if (threadIdx.x == 0) *reinterpret_cast<int*>(args.a.ws) = e;
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Args args) {
+  constexpr int kW = kMergeThreads / 32;
+  __shared__ int few_before[kMaxPairs + 1], many_before[kMaxPairs + 1], pieces[kMaxPairs], slot0[kMaxPairs];
+  __shared__ float part_sum[kW];
+  __shared__ float4 part[kW][128];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, np = args.max_pairs;
+  if (blockIdx.x == 0) {
+    const int e = tid < 2 * np ? args.status[tid] : 0;
+    const int t1 = __syncthreads_or(e == kErrTimeout), t2 = __syncthreads_or(e == kErrSeqLens),
+              t3 = __syncthreads_or(e == kErrPage);
+    if (tid == 0) *reinterpret_cast<int*>(args.a.ws) = t1 ? kErrTimeout : t2 ? kErrSeqLens : t3 ? kErrPage : 0;
   }
-  const int pair = blockIdx.x;
-  int slot = 2 * pair + 1;
-  Piece pc = args.piece[slot];
-  if (!pc.valid) pc = args.piece[slot = 2 * pair];
-  if (!pc.valid || !pc.first) return;
-  const int r = blockIdx.y * 2 + (threadIdx.x >> 7), col = (threadIdx.x & 127) * 4;
-  if (r >= pc.nrows) return;
-  const Scale sc = score_scale<T>(args.a.scale);
-  // pieces: this one, then every following pair's first, up to the tile's end
-  float m = -INFINITY;
-  int n = 1;
-  for (int s = slot;;) {
-    m = fmaxf(m, args.stats[s * kRows + r].x);
-    if (args.piece[s].last) break;
-    // a call that gave up a wait leaves the chain without its end
-    if (pair + n >= args.max_pairs || !args.piece[2 * (pair + n)].valid) break;
-    s = 2 * (pair + n++);
-  }
-  float lsum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0, s = slot; i < n; ++i) {
-    const float4 mm = args.stats[s * kRows + r];
-    const float li = mm.z;
-    if (mm.x != -INFINITY || li != 0.f) {
-      const float f = ex2((mm.y - m) * sc.log2);
-      const float4 v = *reinterpret_cast<const float4*>(args.part + ((size_t)s * kRows + r) * 512 + col);
-      lsum += li * f;
-      o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+  if (tid < np) {
+    int s = 2 * tid + 1, n = 0;
+    if (!args.piece[s].valid) s = 2 * tid;
+    const Piece pc = args.piece[s];
+    if (pc.valid && pc.first) {
+      // this piece, then every following pair's first, up to the tile's end
+      // (a call that gave up a wait leaves the chain without its end)
+      n = 1;
+      for (int q = s; !args.piece[q].last && tid + n < np && args.piece[2 * (tid + n)].valid; ++n) q = 2 * (tid + n);
     }
-    s = 2 * (pair + i + 1);
+    slot0[tid] = s;
+    pieces[tid] = n;
+    few_before[tid + 1] = n > 0 && n <= kManyPieces ? pc.nrows : 0;
+    many_before[tid + 1] = n > kManyPieces ? pc.nrows : 0;
   }
-  const float inv = lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
-  const size_t row = (size_t)pc.row0 + r;
-  uint2 out;
-  out.x = Elt<T>::pack(o.x * inv, o.y * inv);
-  out.y = Elt<T>::pack(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>((T*)args.a.out + row * 512 + col) = out;
-  if (col == 0) {
-    args.a.smax[row] = m == -INFINITY ? m : m * sc.scale;
-    args.a.ssum[row] = lsum;
+  __syncthreads();
+  if (tid == 0) {
+    few_before[0] = many_before[0] = 0;
+    for (int i = 0; i < np; ++i) few_before[i + 1] += few_before[i], many_before[i + 1] += many_before[i];
+  }
+  __syncthreads();
+  const Scale sc = score_scale<T>(args.a.scale);
+  auto owner = [&](const int* before, int task) {   // before[lo] <= task < before[lo + 1]
+    int lo = 0, hi = np;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (before[mid] <= task) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  // One warp's share of a row: pieces first, first + step, ... of n, relative
+  // to the max m of all of them.  Lane l holds columns 4 l + 128 i.
+  auto gather = [&](int pair, int r, int n, int first, int step, float m, float4* o) {
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = first; i < n; i += step) {
+      const int s = i == 0 ? slot0[pair] : 2 * (pair + i);
+      const float4 st = args.stats[s * kRows + r];
+      const float4* p = reinterpret_cast<const float4*>(args.part + ((size_t)s * kRows + r) * 512) + lane;
+      const float4 v[4] = {p[0], p[32], p[64], p[96]};
+      if (st.x == -INFINITY && st.z == 0.f) continue;
+      const float f = ex2((st.y - m) * sc.log2);
+      l += st.z * f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[k].x += v[k].x * f; o[k].y += v[k].y * f; o[k].z += v[k].z * f; o[k].w += v[k].w * f;
+      }
+    }
+    return l;
+  };
+  auto top = [&](int pair, int r, int n) {
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, args.stats[(i == 0 ? slot0[pair] : 2 * (pair + i)) * kRows + r].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    return m;
+  };
+  auto finish = [&](int pair, int r, float m, float l, const float4* o) {
+    const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+    const size_t row = (size_t)args.piece[slot0[pair]].row0 + r;
+    uint2* dst = reinterpret_cast<uint2*>((T*)args.a.out + row * 512) + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      dst[32 * k] = make_uint2(Elt<T>::pack(o[k].x * inv, o[k].y * inv), Elt<T>::pack(o[k].z * inv, o[k].w * inv));
+    if (lane == 0) {
+      args.a.smax[row] = m == -INFINITY ? m : m * sc.scale;
+      args.a.ssum[row] = l;
+    }
+  };
+  for (int task = blockIdx.x; task < many_before[np]; task += gridDim.x) {
+    const int pair = owner(many_before, task), r = task - many_before[pair], n = pieces[pair];
+    const float m = top(pair, r, n);
+    float4 o[4];
+    const float l = gather(pair, r, n, warp, kW, m, o);
+    __syncthreads();   // the row before has been read
+#pragma unroll
+    for (int k = 0; k < 4; ++k) part[warp][lane + 32 * k] = o[k];
+    if (lane == 0) part_sum[warp] = l;
+    __syncthreads();
+    if (warp == 0) {
+      float sum = 0.f;
+      for (int w = 0; w < kW; ++w) sum += part_sum[w];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float4 a = part[0][lane + 32 * k];
+        for (int w = 1; w < kW; ++w) {
+          const float4 v = part[w][lane + 32 * k];
+          a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        }
+        o[k] = a;
+      }
+      finish(pair, r, m, sum, o);
+    }
+  }
+  for (int task = warp * gridDim.x + blockIdx.x; task < few_before[np]; task += kW * gridDim.x) {
+    const int pair = owner(few_before, task), r = task - few_before[pair], n = pieces[pair];
+    const float m = top(pair, r, n);
+    float4 o[4];
+    const float l = gather(pair, r, n, 0, 1, m, o);
+    finish(pair, r, m, l, o);
   }
 }
 
@@ -996,7 +1090,7 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   kern<<<2 * g.max_pairs, kThreads, kSmem, st>>>(m, g);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<T><<<dim3(g.max_pairs, kRows / 2), 256, 0, st>>>(g);
+  paged_merge_kernel<T><<<2 * nsm, kMergeThreads, 0, st>>>(g);
   return cudaGetLastError();
 }
 
