@@ -2,7 +2,7 @@
 // latent part and the position rotation on the way (sfa_cache_append).
 //
 // One warp a token writes its 1152-byte row straight to its page; further
-// warps rotate the tokens' query rows, 16 heads each, so that a decoding step
+// warps rotate the tokens' query rows, 32 heads each, so that a decoding step
 // has one launch ahead of its attention.  Bound by the rows' bytes, and with
 // few tokens by the latency of the lengths, the block table and the row, read
 // one after the other.
@@ -13,8 +13,8 @@
 namespace sfa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kPieces = 4;
+constexpr int kWarps = 4;
+constexpr int kPieces = 8;   // 16-byte pieces a lane rotates at once (32 heads a warp)
 
 // Where a new token goes: its position, or -1 (left out).
 __device__ __forceinline__ int token_position(const AppendArgs& a, int t, int* seq) {
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendArgs a) {
     }
     return;
   }
-  // query rows: 16 heads of one token a warp
+  // query rows: 32 heads of one token a warp
   const int per = (a.pg.G + 4 * kPieces - 1) / (4 * kPieces);
   const long long item = (long long)(blockIdx.x - a.blocks_k) * kWarps + warp;
   if (item >= (long long)a.pg.T * per) return;

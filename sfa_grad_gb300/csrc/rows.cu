@@ -16,7 +16,8 @@ namespace sfa {
 namespace {
 
 constexpr int kWarps = 8;       // warps of a block
-constexpr int kPieces = 4;      // 16-byte pieces a lane rotates at once (16 rows of 64 a warp)
+constexpr int kGradBlocks = 3;  // blocks of the gradient's rows of 512 an SM
+constexpr int kPieces = 8;      // 16-byte pieces a lane rotates at once (32 rows of 64 a warp)
 
 __device__ __forceinline__ bool padded(const RowsArgs& a, int t) {
   if (!a.pos) return false;
@@ -39,7 +40,7 @@ __device__ void norm_rows(const RowsArgs& a, const T* x, const T* w, T* y, float
   if (rstd && lane == 0) rstd[row] = r;
 }
 
-// Rows of 64 of one token, heads h0 .. h0 + 15: rotated by the token's angles.
+// Rows of 64 of one token, heads h0 .. h0 + 31: rotated by the token's angles.
 template <typename T, bool INTER>
 __device__ void rotate_rows(const RowsArgs& a, const T* x, T* y, int heads, int t, int h0, float sgn) {
   const int lane = threadIdx.x & 31;
@@ -66,7 +67,7 @@ __device__ void rotate_rows(const RowsArgs& a, const T* x, T* y, int heads, int 
   }
 }
 
-// The rotated rows' warp items: 16 heads of one token each, the queries'
+// The rotated rows' warp items: 32 heads of one token each, the queries'
 // first, then one a token for the keys.
 template <typename T, bool INTER>
 __device__ void rotate_item(const RowsArgs& a, const T* qr, T* qro, const T* kr, T* kro, long long item, float sgn) {
@@ -99,38 +100,67 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(RowsArgs a) {
 }
 
 // Gradient of rows of 512: warps of `nblk` blocks take rows in strides, keep
-// their part of dw in registers and leave one fp32 sum a block in `part`.
+// their part of dw in registers and leave one fp32 sum a block in `part`.  A
+// row's 2 KB are on their way while the row before is worked on; packed, so
+// that the registers allow three blocks an SM.
 template <typename T>
 __device__ void norm_grad_rows(const RowsArgs& a, const T* x, const T* w, const float* rstd, const T* dy, T* dx,
                                int heads, int blk, int nblk, float* part, float* sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long rows = (long long)a.T * heads;
-  float g[16], acc[16];
-  load_row512(w, lane, g);
+  const long long rows = (long long)a.T * heads, step = (long long)nblk * kWarps;
+  const uint4* pw = reinterpret_cast<const uint4*>(w);
+  const uint4 g[2] = {pw[lane], pw[lane + 32]};
+  float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (long long row = (long long)blk * kWarps + warp; row < rows; row += (long long)nblk * kWarps) {
-    const bool pad = padded(a, (int)(row / heads));
-    const float r = __ldg(rstd + row);
-    float v[16], d[16], s = 0.f;
-    load_row512(x + row * 512, lane, v);
-    load_row512(dy + row * 512, lane, d);
+  uint4 nx[2], nd[2];
+  float nr = 0.f;
+  int npos = 0;
+  auto fetch = [&](long long row) {
+    const uint4* px = reinterpret_cast<const uint4*>(x + row * 512);
+    const uint4* pd = reinterpret_cast<const uint4*>(dy + row * 512);
+    nx[0] = __ldcs(px + lane); nx[1] = __ldcs(px + lane + 32);
+    nd[0] = __ldcs(pd + lane); nd[1] = __ldcs(pd + lane + 32);
+    nr = __ldg(rstd + row);
+    if (a.pos) npos = __ldg(a.pos + row / heads);
+  };
+  long long row = (long long)blk * kWarps + warp;
+  if (row < rows) fetch(row);
+  for (; row < rows; row += step) {
+    const uint4 rx[2] = {nx[0], nx[1]}, rd[2] = {nd[0], nd[1]};
+    const float r = nr;
+    const bool pad = a.pos && (npos < 0 || npos >= a.table_len);
+    if (row + step < rows) fetch(row + step);
+    uint4* out = reinterpret_cast<uint4*>(dx + row * 512);
     if (pad) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) d[i] = 0.f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[i] *= r;
-        acc[i] = fmaf(d[i], v[i], acc[i]);
-        d[i] *= g[i];
-        s = fmaf(d[i], v[i], s);
-      }
-      s = warp_sum(s) * (1.0f / 512.0f);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) d[i] = r * (d[i] - v[i] * s);
+      out[lane] = out[lane + 32] = make_uint4(0, 0, 0, 0);
+      continue;
     }
-    store_row512(dx + row * 512, lane, d);
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float v[8], d[8], gw[8];
+      unpack8<T>(rx[k], v);
+      unpack8<T>(rd[k], d);
+      unpack8<T>(g[k], gw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = v[i] * r;
+        acc[k * 8 + i] = fmaf(d[i], xh, acc[k * 8 + i]);
+        s = fmaf(d[i] * gw[i], xh, s);
+      }
+    }
+    s = warp_sum(s) * (1.0f / 512.0f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float v[8], d[8], gw[8];
+      unpack8<T>(rx[k], v);
+      unpack8<T>(rd[k], d);
+      unpack8<T>(g[k], gw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = r * (d[i] * gw[i] - v[i] * r * s);
+      __stcs(out + lane + 32 * k, pack8<T>(d));
+    }
   }
   // the block's warps in ascending order
   float* mine = sm + warp * 512;
@@ -146,7 +176,7 @@ __device__ void norm_grad_rows(const RowsArgs& a, const T* x, const T* w, const 
 }
 
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_grad_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kernel(RowsArgs a) {
   __shared__ float sm[kWarps * 512];
   int b = blockIdx.x;
   if (b < a.blocks_k) {
@@ -165,25 +195,25 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_grad_kernel(RowsArgs a)
                         (long long)b * kWarps + (threadIdx.x >> 5), -1.f);
 }
 
-// dw of 32 features: the blocks' partial sums in a fixed order.  Block
-// 0..15: keys, 16..31: queries.
-__global__ void __launch_bounds__(256) weight_grad_kernel(RowsArgs a) {
-  __shared__ float sm[8][32];
-  const bool q = blockIdx.x >= 16;
+// dw of 16 features: the blocks' partial sums in a fixed order, 64 chains of
+// them a feature.  Block 0..31: keys, 32..63: queries.
+__global__ void __launch_bounds__(1024) weight_grad_kernel(RowsArgs a) {
+  __shared__ float sm[64][17];
+  const bool q = blockIdx.x >= 32;
   float* out = q ? a.dqw : a.dkw;
   const int n = q ? a.blocks_q : a.blocks_k;
   if (!n) return;
   const float* part = a.part + (q ? (size_t)a.blocks_k * 512 : 0);
-  const int f = (blockIdx.x & 15) * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+  const int c = threadIdx.x & 15, w = threadIdx.x >> 4, f = (blockIdx.x & 31) * 16 + c;
   float s = 0.f;
-  for (int i = w; i < n; i += 8) s += part[(size_t)i * 512 + f];
-  sm[w][threadIdx.x & 31] = s;
+#pragma unroll 8
+  for (int i = w; i < n; i += 64) s += part[(size_t)i * 512 + f];
+  sm[w][c] = s;
   __syncthreads();
-  if (w == 0) {
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += sm[i][threadIdx.x];
-    out[f] = s;
+  if (threadIdx.x < 512) {   // warp k: feature k
+    const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    s = warp_sum(sm[lane][k] + sm[lane + 32][k]);
+    if (lane == 0) out[(blockIdx.x & 31) * 16 + k] = s;
   }
 }
 
@@ -196,9 +226,8 @@ long long rope_blocks(const RowsArgs& a) {
 }  // namespace
 
 int norm_grad_blocks(long long rows, int nsm) {
-  // enough warps to fill the GPU: 8 blocks of 8 warps an SM at most, each of
-  // at least one row a warp
-  const long long n = (rows + kWarps - 1) / kWarps, cap = 6LL * nsm;
+  // as many blocks as the GPU holds at once, each of at least one row a warp
+  const long long n = (rows + kWarps - 1) / kWarps, cap = (long long)kGradBlocks * nsm;
   return (int)(n < cap ? n : cap);
 }
 
@@ -228,7 +257,7 @@ cudaError_t launch_norm_rope_grad(RowsArgs a, int nsm, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (a.blocks_k || a.blocks_q) weight_grad_kernel<<<32, 256, 0, st>>>(a);
+  if (a.blocks_k || a.blocks_q) weight_grad_kernel<<<64, 1024, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -10,7 +10,7 @@ from typing import Optional
 
 import torch
 
-from . import DTYPES, LAYOUTS, _check, _on, _ptr, _stream, _workspace, lib
+from . import DTYPES, LAYOUTS, _check, _stream, _workspace, lib
 
 EXPORTS = ("sfa_norm_rope", "sfa_norm_rope_grad_workspace_size", "sfa_norm_rope_grad", "sfa_cache_append",
            "sfa_paged_workspace_size", "sfa_paged_fwd")
@@ -51,55 +51,67 @@ def _lib():
     return _ready
 
 
+# A call on few rows takes the GPU a few microseconds, so the checks below are
+# written to cost little: one comparison a property, messages only on failure.
 def _need(name: str, t: Optional[torch.Tensor], shape, dtype, device):
+    """Checks a tensor and returns its address."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _launch(device, stream, call, what):
+    """Runs call(stream handle) with `device` current."""
+    if device.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        rc = call(torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call(_stream(stream))
+    if rc:
+        _check(rc, what)
 
 
 # ------------------------------------------------------------------ norm and rotation
 def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved):
-    """Parameters, leading shape and heads from the row tensors that are there
-    (queries (..., N1, 512 / 64), keys (..., 1, 512 / 64))."""
-    first = next((t for t in (k, q, k_rope, q_rope) if t is not None), None)
+    """Parameters, leading shape, heads and addresses of the row tensors that
+    are there (queries (..., N1, 512 / 64), keys (..., 1, 512 / 64))."""
+    first = k if k is not None else q if q is not None else k_rope if k_rope is not None else q_rope
     if first is None:
         raise ValueError("at least one of q, q_rope, k, k_rope is required")
-    if first.dtype not in DTYPES:
+    dt, dev = first.dtype, first.device
+    if dt not in DTYPES:
         raise ValueError("rows must be bfloat16 or float16")
     if first.dim() < 2:
         raise ValueError("rows need a head dimension: (..., heads, 512) or (..., heads, 64)")
-    lead, dev, dt = tuple(first.shape[:-2]), first.device, first.dtype
-    heads = 1
-    for t in (q, q_rope):
-        if t is not None:
-            heads = t.shape[-2]
-            break
-    for name, t, h, w in (("q", q, heads, 512), ("q_rope", q_rope, heads, 64), ("k", k, 1, 512),
-                          ("k_rope", k_rope, 1, 64)):
-        if t is not None:
-            _need(name, t, lead + (h, w), dt, dev)
-    tokens = 1
-    for s in lead:
-        tokens *= s
-    if q_rope is not None or k_rope is not None:
-        if positions is None or cos_sin is None:
-            raise ValueError("positions and cos_sin are required with q_rope or k_rope")
+    lead = first.shape[:-2]
+    heads = q.shape[-2] if q is not None else q_rope.shape[-2] if q_rope is not None else 1
+    at = [None if t is None else _need(name, t, lead + (h, w), dt, dev)
+          for name, t, h, w in (("q", q, heads, 512), ("q_rope", q_rope, heads, 64), ("k", k, 1, 512),
+                                ("k_rope", k_rope, 1, 64))]
+    tokens = lead.numel()
+    if (positions is None or cos_sin is None) and (q_rope is not None or k_rope is not None):
+        raise ValueError("positions and cos_sin are required with q_rope or k_rope")
+    pos = cs = None
     if positions is not None:
         if positions.numel() != tokens:
             raise ValueError(f"positions: {positions.numel()} elements, expected {tokens}")
-        _need("positions", positions, positions.shape, torch.int32, dev)
+        pos = _need("positions", positions, positions.shape, torch.int32, dev)
         if cos_sin is None:
             raise ValueError("cos_sin is required with positions")
     if cos_sin is not None:
-        _need("cos_sin", cos_sin, (cos_sin.shape[0], 64), torch.float32, dev)
-    p = RowsParams(DTYPES[dt], 1 if interleaved else 0, tokens, heads, 0 if cos_sin is None else cos_sin.shape[0],
-                   float(eps))
-    return p, lead, heads, dt, dev
+        cs = _need("cos_sin", cos_sin, (cos_sin.shape[0], 64), torch.float32, dev)
+    p = RowsParams(DTYPES[dt], 1 if interleaved else 0, tokens, heads, 0 if cos_sin is None else cos_sin.shape[0], eps)
+    return p, lead, heads, dt, dev, pos, cs, at
 
 
 def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None, q_weight=None, q_rope=None, eps=1e-6,
@@ -110,28 +122,23 @@ def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None,
     sines).  Each of the four rows may be left out.  Returns (q, q_rope, k,
     k_rope, q_rstd, k_rstd), None where its input is; `outputs`: such a tuple
     to write into, where an output may be its own input."""
-    p, lead, heads, dt, dev = _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved)
-    if k is not None:
-        _need("k_weight", k_weight, (512,), dt, dev)
-    if q is not None:
-        _need("q_weight", q_weight, (512,), dt, dev)
+    p, lead, heads, dt, dev, pos, cs, (qa, qra, ka, kra) = _rows(q, q_rope, k, k_rope, positions, cos_sin, eps,
+                                                                 interleaved)
+    kw = None if k is None else _need("k_weight", k_weight, (512,), dt, dev)
+    qw = None if q is None else _need("q_weight", q_weight, (512,), dt, dev)
     if outputs is None:
         outputs = (None if q is None else torch.empty_like(q), None if q_rope is None else torch.empty_like(q_rope),
                    None if k is None else torch.empty_like(k), None if k_rope is None else torch.empty_like(k_rope),
                    None if q is None else torch.empty(lead + (heads,), dtype=torch.float32, device=dev),
                    None if k is None else torch.empty(lead + (1,), dtype=torch.float32, device=dev))
+        o = [None if t is None else t.data_ptr() for t in outputs]
     else:
-        for name, o, x in zip(("q", "q_rope", "k", "k_rope"), outputs, (q, q_rope, k, k_rope)):
-            if x is not None:
-                _need(f"outputs: {name}", o, x.shape, dt, dev)
-        for name, o, x, h in (("q_rstd", outputs[4], q, heads), ("k_rstd", outputs[5], k, 1)):
-            if x is not None and o is not None:
-                _need(f"outputs: {name}", o, lead + (h,), torch.float32, dev)
-    qo, qro, ko, kro, rq, rk = outputs
-    with _on(dev):
-        _check(_lib().sfa_norm_rope(ctypes.byref(p), _ptr(positions), _ptr(cos_sin), _ptr(q), _ptr(q_weight),
-                                    _ptr(q_rope), _ptr(k), _ptr(k_weight), _ptr(k_rope), _ptr(qo), _ptr(qro),
-                                    _ptr(ko), _ptr(kro), _ptr(rq), _ptr(rk), _stream(stream)), "sfa_norm_rope")
+        o = [None if x is None else _need(f"outputs: {name}", t, x.shape, dt, dev)
+             for name, t, x in zip(("q", "q_rope", "k", "k_rope"), outputs, (q, q_rope, k, k_rope))]
+        o += [None if x is None or t is None else _need(f"outputs: {name}", t, lead + (h,), torch.float32, dev)
+              for name, t, x, h in (("q_rstd", outputs[4], q, heads), ("k_rstd", outputs[5], k, 1))]
+    _launch(dev, stream, lambda st: _lib().sfa_norm_rope(ctypes.byref(p), pos, cs, qa, qw, qra, ka, kw, kra, *o, st),
+            "sfa_norm_rope")
     return outputs
 
 
@@ -142,28 +149,29 @@ def norm_rope_grad(positions, cos_sin, *, k=None, k_weight=None, k_rstd=None, dk
     and k_rstd (q, ...) are norm_rope's inputs and its saved rstd.  Returns
     (dq, dq_rope, dk, dk_rope, dq_weight, dk_weight); the weights' gradients
     are fp32, summed in a fixed order."""
-    p, lead, heads, dt, dev = _rows(dq, dq_rope, dk, dk_rope, positions, cos_sin, 0.0, interleaved)
+    p, lead, heads, dt, dev, pos, cs, (dqa, dqra, dka, dkra) = _rows(dq, dq_rope, dk, dk_rope, positions, cos_sin, 0.0,
+                                                                     interleaved)
+    saved = {}
     for name, d, x, w, r, h in (("k", dk, k, k_weight, k_rstd, 1), ("q", dq, q, q_weight, q_rstd, heads)):
-        if d is not None:
-            _need(name, x, d.shape, dt, dev)
-            _need(f"{name}_weight", w, (512,), dt, dev)
-            _need(f"{name}_rstd", r, lead + (h,), torch.float32, dev)
-    gq, gqr, gk, gkr = (None if d is None else torch.empty_like(d) for d in (dq, dq_rope, dk, dk_rope))
+        saved[name] = (None, None, None) if d is None else (
+            _need(name, x, d.shape, dt, dev), _need(f"{name}_weight", w, (512,), dt, dev),
+            _need(f"{name}_rstd", r, lead + (h,), torch.float32, dev))
+    out = [None if d is None else torch.empty_like(d) for d in (dq, dq_rope, dk, dk_rope)]
     new = torch.empty if p.T1 else torch.zeros       # no token: the weights' gradients are empty sums
-    wq = None if dq is None else new(512, dtype=torch.float32, device=dev)
-    wk = None if dk is None else new(512, dtype=torch.float32, device=dev)
+    out += [None if d is None else new(512, dtype=torch.float32, device=dev) for d in (dq, dk)]
     if p.T1 == 0:
-        return gq, gqr, gk, gkr, wq, wk
+        return tuple(out)
     ws, nbytes = None, 0
-    with _on(dev):
-        if dq is not None or dk is not None:
-            ws = _workspace(norm_rope_grad_workspace_size(p), dev, workspace)
-            nbytes = ws.numel() * ws.element_size()
-        _check(_lib().sfa_norm_rope_grad(ctypes.byref(p), _ptr(positions), _ptr(cos_sin), _ptr(q), _ptr(q_weight),
-                                         _ptr(q_rstd), _ptr(k), _ptr(k_weight), _ptr(k_rstd), _ptr(dq), _ptr(dq_rope),
-                                         _ptr(dk), _ptr(dk_rope), _ptr(gq), _ptr(gqr), _ptr(gk), _ptr(gkr), _ptr(wq),
-                                         _ptr(wk), _ptr(ws), nbytes, _stream(stream)), "sfa_norm_rope_grad")
-    return gq, gqr, gk, gkr, wq, wk
+    if dq is not None or dk is not None:
+        if workspace is None or workspace.device != dev:
+            workspace = _workspace(norm_rope_grad_workspace_size(p), dev, workspace)
+        ws, nbytes = _need("workspace", workspace, workspace.shape, workspace.dtype, dev), \
+            workspace.numel() * workspace.element_size()
+    o = [None if t is None else t.data_ptr() for t in out]
+    _launch(dev, stream, lambda st: _lib().sfa_norm_rope_grad(ctypes.byref(p), pos, cs, *saved["q"], *saved["k"], dqa,
+                                                              dqra, dka, dkra, *o, ws, nbytes, st),
+            "sfa_norm_rope_grad")
+    return tuple(out)
 
 
 def norm_rope_grad_workspace_size(p: RowsParams) -> int:
@@ -185,6 +193,7 @@ def make_paged_params(cache, block_table, act_seq_kv, *, tokens, heads, layout="
     if block_table.dim() != 2:
         raise ValueError("block_table: expected (B, max_pages)")
     b, dev = block_table.shape[0], cache.device
+    _need("cache", cache, cache.shape, cache.dtype, dev)
     _need("block_table", block_table, block_table.shape, torch.int32, dev)
     _need("act_seq_kv", act_seq_kv, (b,), torch.int32, dev)
     lay = LAYOUTS[layout.upper()]
@@ -193,8 +202,8 @@ def make_paged_params(cache, block_table, act_seq_kv, *, tokens, heads, layout="
     if lay == 0 and tokens != b * seq:
         raise ValueError(f"BSND rows of {tokens} tokens do not match {b} sequences of {seq}")
     return PagedParams(lay, DTYPES[cache.dtype], b, 0 if lay else seq, tokens if lay else 0, heads, 512,
-                       cache.shape[2] - 512, cache.shape[0], cache.shape[1], block_table.shape[1], float(scale),
-                       int(sparse_mode), 1 if interleaved else 0, int(wait_limit_us))
+                       cache.shape[2] - 512, cache.shape[0], cache.shape[1], block_table.shape[1], scale, sparse_mode,
+                       1 if interleaved else 0, wait_limit_us)
 
 
 def _leading(name, t, layout):
@@ -202,7 +211,7 @@ def _leading(name, t, layout):
     n = 2 if layout.upper() == "BSND" else 1
     if t.dim() != n + 2:
         raise ValueError(f"{name}: expected {'(B, S1' if n == 2 else '(T1'}, heads, width)")
-    lead = tuple(t.shape[:n])
+    lead = t.shape[:n]
     tokens = lead[0] * (lead[1] if n == 2 else 1)
     return lead, tokens, lead[1] if n == 2 else None
 
@@ -222,30 +231,28 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
     p = make_paged_params(cache, block_table, act_seq_kv, tokens=tokens, heads=heads, layout=layout, seq=seq,
                           act_seq_q=act_seq_q, interleaved=interleaved)
     dt, dev = cache.dtype, cache.device
-    _need("k", k, lead + (1, 512), dt, dev)
-    if k_weight is not None:
-        _need("k_weight", k_weight, (512,), dt, dev)
+    ka = _need("k", k, lead + (1, 512), dt, dev)
+    kw = None if k_weight is None else _need("k_weight", k_weight, (512,), dt, dev)
+    kra = cs = qra = qroa = None
     table_len = 0
     if p.Dr == 64:
-        _need("k_rope", k_rope, lead + (1, 64), dt, dev)
+        kra = _need("k_rope", k_rope, lead + (1, 64), dt, dev)
         if cos_sin is None:
             raise ValueError("cos_sin is required")
-        _need("cos_sin", cos_sin, (cos_sin.shape[0], 64), torch.float32, dev)
+        cs = _need("cos_sin", cos_sin, (cos_sin.shape[0], 64), torch.float32, dev)
         table_len = cos_sin.shape[0]
         if q_rope is not None:
-            _need("q_rope", q_rope, lead + (heads, 64), dt, dev)
+            qra = _need("q_rope", q_rope, lead + (heads, 64), dt, dev)
             if q_rope_out is None:
                 q_rope_out = torch.empty_like(q_rope)
-            _need("q_rope_out", q_rope_out, lead + (heads, 64), dt, dev)
+            qroa = _need("q_rope_out", q_rope_out, lead + (heads, 64), dt, dev)
     elif k_rope is not None or q_rope is not None:
         raise ValueError("rope rows given for a cache without them")
-    if error is not None:
-        _need("error", error, (1,), torch.int32, dev)
-    with _on(dev):
-        _check(_lib().sfa_cache_append(ctypes.byref(p), _ptr(cache), _ptr(block_table), _ptr(act_seq_q),
-                                       _ptr(act_seq_kv), _ptr(k), _ptr(k_rope), _ptr(k_weight), float(eps),
-                                       _ptr(cos_sin), table_len, _ptr(q_rope), _ptr(q_rope_out), _ptr(error),
-                                       _stream(stream)), "sfa_cache_append")
+    err = None if error is None else _need("error", error, (1,), torch.int32, dev)
+    aq = None if act_seq_q is None else act_seq_q.data_ptr()
+    _launch(dev, stream, lambda st: _lib().sfa_cache_append(ctypes.byref(p), cache.data_ptr(), block_table.data_ptr(),
+                                                            aq, act_seq_kv.data_ptr(), ka, kra, kw, eps, cs, table_len,
+                                                            qra, qroa, err, st), "sfa_cache_append")
     return cache, q_rope_out
 
 
@@ -268,9 +275,10 @@ def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="
     p = make_paged_params(cache, block_table, act_seq_kv, tokens=tokens, heads=heads, layout=layout, seq=seq,
                           act_seq_q=act_seq_q, scale=scale, sparse_mode=sparse_mode, wait_limit_us=wait_limit_us)
     dt, dev = cache.dtype, cache.device
-    _need("q", q, lead + (heads, 512), dt, dev)
+    qa = _need("q", q, lead + (heads, 512), dt, dev)
+    qra = None
     if p.Dr == 64:
-        _need("q_rope", q_rope, lead + (heads, 64), dt, dev)
+        qra = _need("q_rope", q_rope, lead + (heads, 64), dt, dev)
     elif q_rope is not None:
         raise ValueError("q_rope given for a cache without rope rows")
     st_shape = (lead[0], 1, lead[1], heads) if seq is not None else (1, tokens, heads)
@@ -280,13 +288,15 @@ def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="
         softmax_max = torch.empty(st_shape, dtype=torch.float32, device=dev)
     if softmax_sum is None:
         softmax_sum = torch.empty(st_shape, dtype=torch.float32, device=dev)
-    _need("out", out, q.shape, dt, dev)
-    _need("softmax_max", softmax_max, st_shape, torch.float32, dev)
-    _need("softmax_sum", softmax_sum, st_shape, torch.float32, dev)
-    with _on(dev):
-        ws = _workspace(paged_workspace_size(p), dev, workspace)
-        _check(_lib().sfa_paged_fwd(ctypes.byref(p), _ptr(q), _ptr(q_rope), _ptr(cache), _ptr(block_table),
-                                    _ptr(act_seq_q), _ptr(act_seq_kv), _ptr(out), _ptr(softmax_max),
-                                    _ptr(softmax_sum), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-               "sfa_paged_fwd")
+    oa = _need("out", out, q.shape, dt, dev)
+    ma = _need("softmax_max", softmax_max, st_shape, torch.float32, dev)
+    sa = _need("softmax_sum", softmax_sum, st_shape, torch.float32, dev)
+    if workspace is None or workspace.device != dev:
+        workspace = _workspace(paged_workspace_size(p), dev, workspace)
+    ws = _need("workspace", workspace, workspace.shape, workspace.dtype, dev)
+    aq = None if act_seq_q is None else act_seq_q.data_ptr()
+    _launch(dev, stream, lambda s: _lib().sfa_paged_fwd(ctypes.byref(p), qa, qra, cache.data_ptr(),
+                                                        block_table.data_ptr(), aq, act_seq_kv.data_ptr(), oa, ma, sa,
+                                                        ws, workspace.numel() * workspace.element_size(), s),
+            "sfa_paged_fwd")
     return out, softmax_max, softmax_sum
