@@ -41,7 +41,6 @@ constexpr uint32_t kOffRing = kOffP + 4 * kPanel;
 constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
 constexpr uint32_t kColS = 256;             // tensor memory: O, then two S tiles of 128 columns
 constexpr int kSegs = 4;                    // work descriptors in flight
-constexpr int kMinUnits = 1;                // key tiles a pair takes at least
 constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
 constexpr int kMaxPairs = kMaxSms / 2;
 // How scores are scaled.  The sign is taken out first, so that a larger score
@@ -90,12 +89,11 @@ struct Ctl {
   Seg seg[kSegs];
   float xbuf[2][4][64];
   long long scan64[2 * kThreads / 32];
-  long long total_units;
   long long start_off;    // units into the first sequence
   int start_seq, start_row;
-  int bad, npairs;
+  int bad, ntiles;        // ntiles: this pair's share
   uint32_t tmem;
-  int abort;
+  int abort, peer_abort;
   // what this CTA's loaders have issued, for the end after a wait that gave up
   int loads[kSlots];      // uses of a slot
   int q_issued;
@@ -129,6 +127,9 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
 __device__ __forceinline__ void expect_at(uint32_t cluster_addr, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void store_at(uint32_t cluster_addr, int v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ int load_from(uint32_t cluster_addr) {
   int v;
@@ -285,7 +286,7 @@ __device__ __forceinline__ long long seq_units(const Paged& p, const SeqWork& s)
 }
 
 // Block-wide: checks the lengths, sums the work, and finds where this pair's
-// share begins.
+// share begins (in Ctl after the next block barrier).
 __device__ void plan_work(const Paged& p, Ctl* c, int pair, int max_pairs) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -316,17 +317,17 @@ __device__ void plan_work(const Paged& p, Ctl* c, int pair, int max_pairs) {
     toks_all += c->scan64[kThreads / 32 + i];
   }
   const bool wrong = any || (p.tnd && toks_all > p.T);
-  const long long n = (total + kMinUnits - 1) / kMinUnits;
-  const int np = n < 1 ? 1 : n < max_pairs ? (int)n : max_pairs;
+  // shares of total / np, the first total % np pairs one more
+  const int np = total < 1 ? 1 : total < max_pairs ? (int)total : max_pairs;
+  const long long share = total >> 32 ? total / np : (unsigned)total / (unsigned)np;
+  const int rest = (int)(total - share * np);
+  const long long u0 = share * pair + min(pair, rest);
+  const int n = wrong || pair >= np ? 0 : (int)(share + (pair < rest));
   if (tid == 0) {
     c->bad = wrong;
-    c->total_units = total;
-    c->npairs = np;
-    c->start_seq = -1;
+    c->ntiles = n;
   }
-  __syncthreads();
-  const long long u0 = total * pair / np;
-  if (!wrong && pair < np && u0 >= u - units && u0 < u) {
+  if (n > 0 && u0 >= u - units && u0 < u) {
     long long at = u - units, row = t - toks;
     for (int b = b0; b < b1; ++b) {
       const SeqWork s = seq_work(p, b);
@@ -341,7 +342,6 @@ __device__ void plan_work(const Paged& p, Ctl* c, int pair, int max_pairs) {
       row += s.qlen;
     }
   }
-  __syncthreads();
 }
 
 // The first piece's row tile: the last j with units_before(j) <= off; all
@@ -392,29 +392,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr int kPer = kKSlots + kVSlots;
   int* status = args.status + blockIdx.x;
 
+  // programmatic launch: the merge may be set up from now on (it waits for
+  // this grid's end before it reads anything)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     *status = 0;
     c->abort = 0;
     c->q_issued = 0;
-    for (int i = 0; i < kLoaders; ++i) mbar_init(&c->vloc[i], 1);
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&c->full[i], 2);
-      mbar_init(&c->empty[i], 1);
-      c->loads[i] = 0;
-    }
     mbar_init(&c->qfull, 2);
     mbar_init(&c->qempty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&c->sfull[i], 1);
-      mbar_init(&c->sfree[i], 2 * kSoft);
-      mbar_init(&c->xch[i], 4);
-    }
     mbar_init(&c->settle, 1);
     mbar_init(&c->pready, 2 * kSoft);
     mbar_init(&c->pfree, 1);
     mbar_init(&c->ofree, 2 * kSoft);
-    for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], kLoaders + kSoft + (leader ? 1 : 0));
+    if (leader) {
+      // a piece at the beginning, a piece at the end: none until the walk says so
+      args.piece[2 * pair].valid = 0;
+      args.piece[2 * pair + 1].valid = 0;
+    }
     mbar_fence_init();
+  } else if (warp == 1) {
+    if (lane < kLoaders) mbar_init(&c->vloc[lane], 1);
+    if (lane < kSlots) {
+      mbar_init(&c->full[lane], 2);
+      mbar_init(&c->empty[lane], 1);
+      c->loads[lane] = 0;
+    }
+    mbar_fence_init();
+  } else if (warp == 2) {
+    if (lane < 2) {
+      mbar_init(&c->sfull[lane], 1);
+      mbar_init(&c->sfree[lane], 2 * kSoft);
+      mbar_init(&c->xch[lane], 4);
+    }
+    if (lane < kSegs) {
+      mbar_init(&c->seg_full[lane], 1);
+      mbar_init(&c->seg_empty[lane], kLoaders + kSoft + (leader ? 1 : 0));
+    }
+    mbar_fence_init();
+  } else if (warp == 3 && lane < 4) {
+    const CUtensorMap* m = lane == 0 ? &maps.q : lane == 1 ? &maps.qr : lane == 2 ? &maps.k : &maps.v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   }
   if (warp == 6) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c->tmem))
@@ -428,27 +446,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = c->tmem;
   const Limit w{&c->abort, status, (long long)(args.a.wait_ns * 21 / 10)};   // SM clock at most 2.1 GHz
-  const bool work = c->start_seq >= 0;
-  const long long u0 = c->total_units * pair / c->npairs, u1 = c->total_units * (pair + 1) / c->npairs;
-  const int ntiles = work ? (int)(u1 - u0) : 0;
+  const int ntiles = c->ntiles;
+  const bool work = ntiles > 0;
   // ring position of tile n's first key slot and value slot: K(0) K(1) V(0)
   // K(2) V(1) ... K(N-1) V(N-2) V(N-1)
   auto kpos = [&](int n) { return n == 0 ? 0 : kKSlots + (n - 1) * kPer; };
   auto vpos = [&](int n) { return kpos(n + 1) + (n + 1 < ntiles ? kKSlots : 0); };
   const uint32_t ring = smem_u32(sm + kOffRing), lead = 0;
 
-  if (tid == 0 && leader) {
-    // a piece at the beginning, a piece at the end: none until the walk says so
-    args.piece[2 * pair].valid = 0;
-    args.piece[2 * pair + 1].valid = 0;
-  }
   if (c->bad && tid == 0) *status = kErrSeqLens;
-  __syncthreads();
 
   if (work && warp == 6) {
     // ---------------------------------------------------------------- the walk
     int b = c->start_seq;
-    long long left = u1 - u0;
+    int left = ntiles;
     SeqWork s = seq_work(p, b);
     int j = find_tile(p, s, c->start_off);
     int kt = (int)(c->start_off - units_before(p, s, j));
@@ -468,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         g.i0 = j * kRows;
         g.nrows = min(kRows, s.rows - g.i0);
         g.kt0 = kt;
-        g.kt1 = (int)min((long long)units, kt + left);
+        g.kt1 = min(units, kt + left);
         g.kend = tile_keys(p, s, j);
         g.base = p.mode == 3 ? s.kvlen - s.qlen : s.kvlen - 1;
         g.slot = g.kt0 == 0 && g.kt1 == units ? -1 : n == 0 ? 2 * pair : 2 * pair + 1;
@@ -908,8 +919,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // ---------------------------------------------------------------- end
   __syncthreads();
+  if (tid == 0) store_at(map_to(smem_u32(&c->peer_abort), rank ^ 1), c->abort);
   cluster_sync();
-  if (tid == 0 && (c->abort || load_from(map_to(smem_u32(&c->abort), rank ^ 1)))) {
+  const bool gave_up = c->abort || c->peer_abort;   // the same in both CTAs
+  if (gave_up && tid == 0) {
     // Loads on their way.  The first CTA's barriers count those of both, and
     // the two may have stopped at different places (a slot's uses at most one
     // apart): a phase that one of them has begun gets the other's arrival,
@@ -923,7 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       finish(&c->qfull, c->q_issued, load_from(map_to(smem_u32(&c->q_issued), 1)));
     }
   }
-  cluster_sync();
+  if (gave_up) cluster_sync();
   if (warp == 6)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
@@ -940,34 +953,45 @@ template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Args args) {
   constexpr int kW = kMergeThreads / 32;
   __shared__ int few_before[kMaxPairs + 1], many_before[kMaxPairs + 1], pieces[kMaxPairs], slot0[kMaxPairs];
+  __shared__ Piece pc[2 * kMaxPairs];
   __shared__ float part_sum[kW];
   __shared__ float4 part[kW][128];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, np = args.max_pairs;
-  if (blockIdx.x == 0) {
-    const int e = tid < 2 * np ? args.status[tid] : 0;
-    const int t1 = __syncthreads_or(e == kErrTimeout), t2 = __syncthreads_or(e == kErrSeqLens),
-              t3 = __syncthreads_or(e == kErrPage);
-    if (tid == 0) *reinterpret_cast<int*>(args.a.ws) = t1 ? kErrTimeout : t2 ? kErrSeqLens : t3 ? kErrPage : 0;
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int e = tid < 2 * np ? args.status[tid] : 0;
+  if (tid < 2 * np) pc[tid] = args.piece[tid];
+  const int t1 = __syncthreads_or(e == kErrTimeout), t2 = __syncthreads_or(e == kErrSeqLens),
+            t3 = __syncthreads_or(e == kErrPage);
+  if (blockIdx.x == 0 && tid == 0)
+    *reinterpret_cast<int*>(args.a.ws) = t1 ? kErrTimeout : t2 ? kErrSeqLens : t3 ? kErrPage : 0;
   if (tid < np) {
-    int s = 2 * tid + 1, n = 0;
-    if (!args.piece[s].valid) s = 2 * tid;
-    const Piece pc = args.piece[s];
-    if (pc.valid && pc.first) {
+    const int s = pc[2 * tid + 1].valid ? 2 * tid + 1 : 2 * tid;
+    int n = 0;
+    if (pc[s].valid && pc[s].first) {
       // this piece, then every following pair's first, up to the tile's end
       // (a call that gave up a wait leaves the chain without its end)
       n = 1;
-      for (int q = s; !args.piece[q].last && tid + n < np && args.piece[2 * (tid + n)].valid; ++n) q = 2 * (tid + n);
+      for (int q = s; !pc[q].last && tid + n < np && pc[2 * (tid + n)].valid; ++n) q = 2 * (tid + n);
     }
     slot0[tid] = s;
     pieces[tid] = n;
-    few_before[tid + 1] = n > 0 && n <= kManyPieces ? pc.nrows : 0;
-    many_before[tid + 1] = n > kManyPieces ? pc.nrows : 0;
   }
   __syncthreads();
-  if (tid == 0) {
-    few_before[0] = many_before[0] = 0;
-    for (int i = 0; i < np; ++i) few_before[i + 1] += few_before[i], many_before[i + 1] += many_before[i];
+  if (warp < 2) {   // prefix sums of the rows of tiles of few and of many pieces
+    int* before = warp ? many_before : few_before;
+    int sum = 0;
+    for (int i0 = 0; i0 < np; i0 += 32) {
+      const int i = i0 + lane;
+      int v = i < np && pieces[i] > 0 && (pieces[i] > kManyPieces) == (warp == 1) ? pc[slot0[i]].nrows : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
+      }
+      if (i < np) before[i + 1] = sum + v;
+      sum += __shfl_sync(~0u, v, 31);
+    }
+    if (lane == 0) before[0] = 0;
   }
   __syncthreads();
   const Scale sc = score_scale<T>(args.a.scale);
@@ -1010,7 +1034,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Args a
   };
   auto finish = [&](int pair, int r, float m, float l, const float4* o) {
     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-    const size_t row = (size_t)args.piece[slot0[pair]].row0 + r;
+    const size_t row = (size_t)pc[slot0[pair]].row0 + r;
     uint2* dst = reinterpret_cast<uint2*>((T*)args.a.out + row * 512) + lane;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -1090,8 +1114,16 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   kern<<<2 * g.max_pairs, kThreads, kSmem, st>>>(m, g);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<T><<<2 * nsm, kMergeThreads, 0, st>>>(g);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * nsm);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T>, g);
 }
 
 template cudaError_t launch_paged<__nv_bfloat16>(const PagedArgs&, int, cudaStream_t);
