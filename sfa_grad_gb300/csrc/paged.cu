@@ -18,17 +18,17 @@
 // kernel merges them in order: few rows over a long cache spread over all
 // SMs, and the result does not depend on timing.
 //
-// Warps of a CTA: 0..3 TMA loads (ring slots 2 w and 2 w + 1), 4 the MMAs (only
-// in the pair's first CTA), 6 the walk over the work, 8..15 softmax and
-// epilogue.
+// Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
+// MMAs (only in the pair's first CTA), 6 the walk over the work with the page
+// table and the query rows, 8..15 softmax and epilogue.
 #include "kernels.h"
 #include "rows.cuh"
 
 namespace sfa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kLoaders = 4;                 // warps that load
+constexpr int kThreads = 544;
+constexpr int kTiles = 4;                   // tiles whose cache rows are known in advance
 constexpr int kSoft = 8;                    // softmax warps, from warp 8
 constexpr int kRows = 128;                  // rows of a row tile
 constexpr int kKeys = 256;                  // keys of a tile
@@ -40,7 +40,7 @@ constexpr uint32_t kOffP = 9 * kPanel;      // P: 64 rows x 256 keys
 constexpr uint32_t kOffRing = kOffP + 4 * kPanel;
 constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
 constexpr uint32_t kColS = 256;             // tensor memory: O, then two S tiles of 128 columns
-constexpr int kSegs = 4;                    // work descriptors in flight
+constexpr int kSegs = 8;                    // work descriptors in flight
 constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
 constexpr int kMaxPairs = kMaxSms / 2;
 // How scores are scaled.  The sign is taken out first, so that a larger score
@@ -63,12 +63,18 @@ __device__ __forceinline__ Scale score_scale(float scale) {
 
 // One piece of work: key tiles kt0 .. kt1 - 1 of a row tile.
 struct Seg {
-  int seq, row0, nrows;   // rows of q, row0 the first
+  int row0, nrows;        // rows of q, row0 the first
   int i0;                 // first row's index in its sequence (token * heads + head)
   int kt0, kt1;           // kt1 = 0: end of the work
   int kend;               // keys any row sees
   int base;               // mode 3: last key of the sequence's first new token; mode 0: of every token
   int slot;               // -1: whole row tile; else where the piece's result goes
+};
+
+// What the loads of a key tile need.
+struct Tile {
+  int y[kKeys / 16];      // cache row of each box of vbox keys
+  int key0, kend, least;  // first key; keys any row sees; last key the first row sees
 };
 
 // A piece's place in the workspace, for the merge.
@@ -82,11 +88,13 @@ struct Ctl {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t qfull, qempty;
   uint64_t sfull[2], sfree[2];
-  uint64_t pready, pfree, ofree, vloc[kLoaders];
+  uint64_t pready, pfree, ofree, vloc[kSlots];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t tile_full[kTiles], tile_empty[kTiles];
   uint64_t xch[2];
   uint64_t settle;
   Seg seg[kSegs];
+  Tile tile[kTiles];
   float xbuf[2][4][64];
   long long scan64[2 * kThreads / 32];
   long long start_off;    // units into the first sequence
@@ -389,7 +397,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1;
   const bool leader = rank == 0;
   constexpr int kKSlots = ROPE ? 9 : 8;       // ring slots of a tile's keys
-  constexpr int kPer = kKSlots + kVSlots;
   int* status = args.status + blockIdx.x;
 
   // programmatic launch: the merge may be set up from now on (it waits for
@@ -412,8 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_fence_init();
   } else if (warp == 1) {
-    if (lane < kLoaders) mbar_init(&c->vloc[lane], 1);
     if (lane < kSlots) {
+      mbar_init(&c->vloc[lane], 1);
       mbar_init(&c->full[lane], 2);
       mbar_init(&c->empty[lane], 1);
       c->loads[lane] = 0;
@@ -427,7 +434,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane < kSegs) {
       mbar_init(&c->seg_full[lane], 1);
-      mbar_init(&c->seg_empty[lane], kLoaders + kSoft + (leader ? 1 : 0));
+      mbar_init(&c->seg_empty[lane], kSoft + (leader ? 1 : 0));
+    }
+    if (lane < kTiles) {
+      mbar_init(&c->tile_full[lane], 1);
+      mbar_init(&c->tile_empty[lane], kSlots);
     }
     mbar_fence_init();
   } else if (warp == 3 && lane < 4) {
@@ -448,23 +459,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const Limit w{&c->abort, status, (long long)(args.a.wait_ns * 21 / 10)};   // SM clock at most 2.1 GHz
   const int ntiles = c->ntiles;
   const bool work = ntiles > 0;
-  // ring position of tile n's first key slot and value slot: K(0) K(1) V(0)
-  // K(2) V(1) ... K(N-1) V(N-2) V(N-1)
-  auto kpos = [&](int n) { return n == 0 ? 0 : kKSlots + (n - 1) * kPer; };
-  auto vpos = [&](int n) { return kpos(n + 1) + (n + 1 < ntiles ? kKSlots : 0); };
+  // the ring holds, slot after slot, K(0) K(1) V(0) K(2) V(1) ... K(N-1) V(N-2) V(N-1)
   const uint32_t ring = smem_u32(sm + kOffRing), lead = 0;
 
   if (c->bad && tid == 0) *status = kErrSeqLens;
 
   if (work && warp == 6) {
     // ---------------------------------------------------------------- the walk
-    int b = c->start_seq;
-    int left = ntiles;
+    // Pieces for the softmax and the MMAs, tiles for the loads, and the query
+    // rows.
+    const int none = p.num_pages * p.page_size;     // a row outside the maps: zeros
+    const int boxes = kKeys / args.vbox;
+    const uint32_t qfull = map_to(smem_u32(&c->qfull), lead);
+    int b = c->start_seq, left = ntiles, tile = 0;
     SeqWork s = seq_work(p, b);
     int j = find_tile(p, s, c->start_off);
     int kt = (int)(c->start_off - units_before(p, s, j));
     int row = p.tnd ? c->start_row * p.G : b * p.S1 * p.G;   // first row of the sequence
-    for (int n = 0;; ++n) {
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
       Seg g;
       g.kt1 = 0;
       if (left > 0) {
@@ -474,7 +487,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           j = 0;
         }
         const int units = tile_units(p, s, j);
-        g.seq = b;
         g.row0 = row + j * kRows;
         g.i0 = j * kRows;
         g.nrows = min(kRows, s.rows - g.i0);
@@ -490,83 +502,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++j;
       }
       const int r = n % kSegs;
-      if (n >= kSegs && !warp_wait(&c->seg_empty[r], (n / kSegs - 1) & 1, w)) break;
+      if (n >= kSegs && !(ok = warp_wait(&c->seg_empty[r], (n / kSegs - 1) & 1, w))) break;
       if (lane == 0) {
         c->seg[r] = g;
         mbar_arrive(&c->seg_full[r]);
       }
       if (g.kt1 == 0) break;
+      const int* table = p.table + (size_t)b * p.max_pages;
+      auto fetch = [&](int t) {
+        const int key = t * kKeys + lane * args.vbox;
+        return lane < boxes && key < g.kend ? __ldg(table + key / p.page_size) : -2;
+      };
+      int page = fetch(g.kt0);
+      for (int t = g.kt0; t < g.kt1; ++t, ++tile) {
+        int y = none;
+        if (page >= 0 && page < p.num_pages)
+          y = page * p.page_size + (t * kKeys + lane * args.vbox) % p.page_size;
+        else if (page != -2)
+          *status = kErrPage;
+        if (t + 1 < g.kt1) page = fetch(t + 1);   // in flight during the waits
+        const int i = tile % kTiles;
+        if (tile >= kTiles && !(ok = warp_wait(&c->tile_empty[i], (tile / kTiles - 1) & 1, w))) break;
+        if (lane < boxes) c->tile[i].y[lane] = y;
+        if (lane == 0) {
+          c->tile[i].key0 = t * kKeys;
+          c->tile[i].kend = g.kend;
+          c->tile[i].least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->tile_full[i]);
+        if (t == g.kt0) {
+          // the query rows, once the piece before has done its products
+          if (n > 0 && !(ok = warp_wait(&c->qempty, (n - 1) & 1, w))) break;
+          if (lane == 0) {
+            expect_at(qfull, (8 + ROPE) * kPanel);
+            c->q_issued = n + 1;
+          }
+          __syncwarp();
+          if (lane < 8 + ROPE)
+            pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64,
+                     g.row0 + rank * 64, qfull);
+        }
+      }
+      // (the last query release: none is on its way to a CTA that has ended)
+      if (ok && left == 0) ok = warp_wait(&c->qempty, n & 1, w);
     }
-  } else if (work && warp < kLoaders) {
+  } else if (work && (warp < 4 || warp == 5 || warp == 7 || warp == 16)) {
     // ---------------------------------------------------------------- TMA loads
-    const int none = p.num_pages * p.page_size;     // a row outside the maps: zeros
-    const uint32_t full0 = map_to(smem_u32(&c->full[0]), lead), qfull = map_to(smem_u32(&c->qfull), lead);
-    // a tile's cache rows come in kKeys / vbox boxes, lane l knows box l's; a
-    // slot of keys takes 128 / kbox boxes, one of values 64 / vbox boxes of
+    // Slot s: the ring's uses s, s + kSlots, ...
+    const int s = warp < 4 ? warp : warp == 5 ? 4 : warp == 7 ? 5 : 6;
+    const uint32_t bar = map_to(smem_u32(&c->full[s]), lead), dst = ring + s * kSlot;
+    // a slot of keys takes 128 / kbox boxes, one of values 64 / vbox boxes of
     // each panel (or one of both)
     const int nk = 128 / args.kbox, nv = 64 / args.vbox, kstep = args.kbox / args.vbox;
     const int vp = nv == 1 ? 0 : lane / nv, vb = nv == 1 ? 0 : lane - vp * nv;
     const bool vissues = nv == 1 ? lane == 0 : vp < 2;
-    const uint32_t kdst = ring + lane * args.kbox * 128, vdst = ring + vp * kPanel + vb * args.vbox * 128;
-    int nclean = 0;
+    const int ky = (int)rank * 2 * nv + lane * kstep;
+    const uint32_t kdst = dst + lane * args.kbox * 128, vdst = dst + vp * kPanel + vb * args.vbox * 128;
+    int k = 0, nclean = 0;   // uses so far; of them values cleaned here
     bool ok = true;
-    auto fetch = [&](const Seg& g, int kt) {
-      const int key = kt * kKeys + lane * args.vbox;
-      return lane < 4 * nv && key < g.kend ? __ldg(p.table + (size_t)g.seq * p.max_pages + key / p.page_size) : -2;
-    };
-    auto rows = [&](int kt, int page) {
-      if (page >= 0 && page < p.num_pages) return page * p.page_size + (kt * kKeys + lane * args.vbox) % p.page_size;
-      if (page != -2) *status = kErrPage;
-      return none;
-    };
-    // ring use u, if it is this warp's: its slot, once free
-    auto take = [&](int u) {
-      // a slot stays with one warp, which so knows that its last use was loaded
-      const int s = u % kSlots, k = u / kSlots;
-      if (s >> 1 != warp || !ok) return -1;
-      if (k > 0 && !(ok = warp_wait(&c->empty[s], (k - 1) & 1, w))) return -1;
-      return s;
-    };
-    auto load_k = [&](int u, int y, int panel) {
-      const int s = take(u);
-      if (s < 0) return;
+    auto free_slot = [&]() { return k == 0 || (ok = warp_wait(&c->empty[s], (k - 1) & 1, w)); };
+    auto load_k = [&](const Tile& t, int panel) {
+      const int y = lane < nk ? t.y[ky] : 0;
+      if (!free_slot()) return;
+      if (lane < nk) pair_tma3(kdst, &maps.k, y, panel, bar);
       if (lane == 0) {
-        expect_at(full0 + s * 8, kSlot);
-        c->loads[s] = u / kSlots + 1;
+        expect_at(bar, kSlot);
+        c->loads[s] = k + 1;
       }
-      const int yy = __shfl_sync(~0u, y, (int)rank * 2 * nv + min(lane * kstep, 2 * nv - 1));
-      if (lane < nk) pair_tma3(kdst + s * kSlot, &maps.k, yy, panel, full0 + s * 8);
+      ++k;
     };
-    // 64 keys from key0 on, 128 features; y0: lane of their first box
-    auto load_v = [&](int u, const Seg& g, int key0, int y, int y0, int panel) {
-      const int s = take(u);
-      if (s < 0) return;
-      const int yy = __shfl_sync(~0u, y, y0 + vb);
-      // keys past `least` that a box brings in
-      const int least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;
-      const int loaded = min(64, (max(0, g.kend - key0) + args.vbox - 1) / args.vbox * args.vbox);
-      if (loaded == 0 || least + 1 >= key0 + loaded) {
+    // 64 keys, 128 features: part i of the tile's values
+    auto load_v = [&](const Tile& t, int i) {
+      const int key0 = t.key0 + (i >> 1) * 64, panel = (int)rank * 4 + (i & 1) * 2 + vp;
+      const int y = vissues ? t.y[(i >> 1) * nv + vb] : 0;
+      // keys that a box brings in; those past `least` are masked for some row
+      const int loaded = min(64, (max(0, t.kend - key0) + args.vbox - 1) / args.vbox * args.vbox);
+      const bool clean = loaded > 0 && t.least + 1 < key0 + loaded;
+      const int first = max(0, t.least + 1 - key0), end = t.kend - key0;
+      if (!free_slot()) return;
+      if (!clean) {
+        if (vissues) pair_tma3(vdst, &maps.v, y, panel, bar);
         if (lane == 0) {
-          expect_at(full0 + s * 8, kSlot);
-          c->loads[s] = u / kSlots + 1;
+          expect_at(bar, kSlot);
+          c->loads[s] = k + 1;
         }
-        __syncwarp();
-        if (vissues) pair_tma3(vdst + s * kSlot, &maps.v, yy, panel + vp, full0 + s * 8);
+        ++k;
         return;
       }
       // Values of masked keys: rows no query row sees become zeros (they may
       // hold anything), and non-finite values of the others, which would
       // reach rows that do not see them as 0 x inf (a row that sees them has
       // a non-finite score from the same cache row).
-      if (lane == 0) mbar_expect_tx(&c->vloc[warp], kSlot);
+      if (lane == 0) mbar_expect_tx(&c->vloc[s], kSlot);
       __syncwarp();
-      if (vissues) pair_tma3(vdst + s * kSlot, &maps.v, yy, panel + vp, smem_u32(&c->vloc[warp]));
-      mbar_settle(&c->vloc[warp], nclean++ & 1, status);   // the copy is on its way, whatever else gave up
+      if (vissues) pair_tma3(vdst, &maps.v, y, panel, smem_u32(&c->vloc[s]));
+      mbar_settle(&c->vloc[s], nclean++ & 1, status);   // the copy is on its way, whatever else gave up
       __syncwarp();
-      for (int k = max(0, least + 1 - key0) + (lane >> 4); k < loaded; k += 2) {
-        const uint32_t at = ring + s * kSlot + ((lane >> 3) & 1) * kPanel + k * 128 + ((lane & 7) << 4);
+      for (int q = first + (lane >> 4); q < loaded; q += 2) {
+        const uint32_t at = dst + ((lane >> 3) & 1) * kPanel + q * 128 + ((lane & 7) << 4);
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (key0 + k < g.kend) {
+        if (q < end) {
           v = lds128(at);
           float e[8];
           unpack8<T>(v, e);
@@ -579,67 +615,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive_at(full0 + s * 8);
-        c->loads[s] = u / kSlots + 1;
+        arrive_at(bar);
+        c->loads[s] = k + 1;
       }
+      ++k;
     };
-    // one copy of the code for every tile: keys of the next, values of the last
-    Seg g, prev;
-    g.kt1 = 0;
-    int kt = 0, page = -2, prev_kt = 0, prev_y = 0, tile = 0, n = 0, qn = 0;
-    for (bool more = true; ok;) {
-      if (kt >= g.kt1) {   // a new piece
-        const int r = n % kSegs;
-        if (!warp_wait(&c->seg_full[r], (n / kSegs) & 1, w)) break;
-        g = c->seg[r];
+    int u = s, base = 0;   // the slot's next use; the first use of the block below
+    for (int t = -1; t < ntiles && ok; ++t) {
+      if (t + 1 < ntiles) {
+        const int i = (t + 1) % kTiles;
+        if (!(ok = warp_wait(&c->tile_full[i], ((t + 1) / kTiles) & 1, w))) break;
+#pragma unroll 1
+        for (; u < base + kKSlots && ok; u += kSlots) load_k(c->tile[i], u - base);
+        base += kKSlots;
+      }
+      if (t >= 0) {
+#pragma unroll 1
+        for (; u < base + kVSlots && ok; u += kSlots) load_v(c->tile[t % kTiles], u - base);
+        base += kVSlots;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->seg_empty[r]);
-        ++n;
-        more = g.kt1 != 0;
-        kt = g.kt0;
-        if (more) page = fetch(g, kt);
-        if (more && warp == 0) {
-          // the query rows, once the segment before has done its products
-          if (qn > 0 && !warp_wait(&c->qempty, (qn - 1) & 1, w)) break;
-          if (lane == 0) {
-            expect_at(qfull, (8 + ROPE) * kPanel);
-            c->q_issued = qn + 1;
-          }
-          __syncwarp();
-          if (lane < 8 + ROPE)
-            pair_tma(smem_u32(sm) + lane * kPanel, lane < 8 ? &maps.q : &maps.qr, (lane & 7) * 64, g.row0 + rank * 64,
-                     qfull);
-          ++qn;
-        }
+        if (lane == 0) mbar_arrive(&c->tile_empty[t % kTiles]);
       }
-      int y = none;
-      if (more) {
-        y = rows(kt, page);
-        if (kt + 1 < g.kt1) page = fetch(g, kt + 1);   // in flight during the waits
-        const int u = kpos(tile);
-#pragma unroll 1
-        for (int i = 0; i < kKSlots; ++i) load_k(u + i, y, i);
-      }
-      if (tile > 0) {
-        const int u = vpos(tile - 1);
-#pragma unroll 1
-        for (int i = 0; i < kVSlots; ++i)
-          load_v(u + i, prev, prev_kt * kKeys + (i >> 1) * 64, prev_y, (i >> 1) * nv, (int)rank * 4 + (i & 1) * 2);
-      }
-      if (!more) break;
-      prev = g;
-      prev_kt = kt++;
-      prev_y = y;
-      ++tile;
     }
-    // the slots' last releases and the last query release have arrived: none
-    // is on its way to a CTA that has ended
-    if (__all_sync(~0u, !*w.abort)) {
-      const int uses = tile * kPer;
-      for (int u = max(0, uses - kSlots); u < uses; ++u)
-        if (u % kSlots >> 1 == warp) warp_wait(&c->empty[u % kSlots], (u / kSlots) & 1, w);
-      if (qn > 0) warp_wait(&c->qempty, (qn - 1) & 1, w);
-    }
+    // the slot's last release has arrived: none is on its way to a CTA that
+    // has ended
+    if (ok && k > 0) warp_wait(&c->empty[s], (k - 1) & 1, w);
   } else if (work && leader && warp == 4) {
     // ---------------------------------------------------------------- MMAs
     // In the ring's order, S one tile ahead: S(0) S(1) PV(0) S(2) PV(1) ...
