@@ -401,8 +401,8 @@ typedef struct sfa_paged_params {
  * k (tokens, 512), k_rope (tokens, 64), q_rope (tokens, N1, 64).  With Dr = 0
  * the rope tensors and cos_sin are ignored.  No two tokens share a row unless
  * the block table names a page twice.  A token is left out when its sequence's
- * lengths are negative, exceed the block table or its position is negative
- * (SFA_DEVERR_SEQLENS), when its page lies outside the cache (SFA_DEVERR_PAGE)
+ * lengths are negative, exceed the tokens or the block table or its position
+ * is negative (SFA_DEVERR_SEQLENS), when its page lies outside the cache (SFA_DEVERR_PAGE)
  * or its position outside the table (SFA_DEVERR_POSITION); `error` (optional,
  * device int32) then receives the code, and is not written otherwise.
  * scale, sparse_mode and wait_limit_us are not used.

@@ -23,6 +23,11 @@ template <typename... Ts>
 bool all_aligned(Ts... ps) {
   return (... && aligned(ps));
 }
+// int32 and fp32 arrays read and written by element
+template <typename... Ts>
+bool words_aligned(Ts... ps) {
+  return (... && aligned(ps, 4));
+}
 
 sfa_status check_rows(const sfa_rows_params* p) {
   if (!p) return SFA_ERR_NULLPTR;
@@ -99,7 +104,8 @@ sfa_status sfa_norm_rope(const sfa_rows_params* p, const int32_t* positions, con
     return SFA_ERR_NULLPTR;
   if ((q_rope || k_rope) && (!positions || !cos_sin)) return SFA_ERR_NULLPTR;
   if ((q_rope || k_rope) && p->table_len < 1) return SFA_ERR_SHAPE;
-  if (!all_aligned(cos_sin, q, q_weight, q_rope, k, k_weight, k_rope, q_out, q_rope_out, k_out, k_rope_out))
+  if (!all_aligned(cos_sin, q, q_weight, q_rope, k, k_weight, k_rope, q_out, q_rope_out, k_out, k_rope_out) ||
+      !words_aligned(positions, q_rstd, k_rstd))
     return SFA_ERR_PARAM_INVALID;
   if (p->T1 == 0) return SFA_OK;
   RowsArgs a = rows_args(p, positions, cos_sin);
@@ -140,7 +146,8 @@ sfa_status sfa_norm_rope_grad(const sfa_rows_params* p, const int32_t* positions
   if (rope && (!positions || !cos_sin)) return SFA_ERR_NULLPTR;
   if ((d_q || d_k) && !workspace) return SFA_ERR_NULLPTR;
   if (rope && p->table_len < 1) return SFA_ERR_SHAPE;
-  if (!all_aligned(cos_sin, q, q_weight, k, k_weight, d_q, d_q_rope, d_k, d_k_rope, dq, dq_rope, dk, dk_rope))
+  if (!all_aligned(cos_sin, q, q_weight, k, k_weight, d_q, d_q_rope, d_k, d_k_rope, dq, dq_rope, dk, dk_rope) ||
+      !words_aligned(positions, q_rstd, k_rstd, dq_weight, dk_weight))
     return SFA_ERR_PARAM_INVALID;
   if ((d_q || d_k) && (workspace_bytes < need || !aligned(workspace, 256))) return SFA_ERR_PARAM_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -179,7 +186,9 @@ sfa_status sfa_cache_append(const sfa_paged_params* p, void* cache, const int32_
   if (rope && (!k_rope || !cos_sin || (q_rope && !q_rope_out))) return SFA_ERR_NULLPTR;
   if (rope && (table_len < 1 || table_len > INT32_MAX)) return SFA_ERR_SHAPE;
   if (!std::isfinite(eps) || eps < 0) return SFA_ERR_SHAPE;
-  if (!all_aligned(cache, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out)) return SFA_ERR_PARAM_INVALID;
+  if (!all_aligned(cache, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out) ||
+      !words_aligned(block_table, act_seq_q, act_seq_kv, error))
+    return SFA_ERR_PARAM_INVALID;
   a.pg.table = block_table;
   a.pg.act_q = act_seq_q;
   a.pg.act_kv = act_seq_kv;
@@ -227,7 +236,9 @@ sfa_status sfa_paged_fwd(const sfa_paged_params* p, const void* q, const void* q
   if (!q || !cache || !block_table || !act_seq_kv || !out || !softmax_max || !softmax_sum ||
       (a.pg.tnd && !act_seq_q) || (rope && !q_rope))
     return SFA_ERR_NULLPTR;
-  if (!all_aligned(q, rope ? q_rope : nullptr, cache, out)) return SFA_ERR_PARAM_INVALID;
+  if (!all_aligned(q, rope ? q_rope : nullptr, cache, out) ||
+      !words_aligned(block_table, act_seq_q, act_seq_kv, softmax_max, softmax_sum))
+    return SFA_ERR_PARAM_INVALID;
   a.pg.table = block_table;
   a.pg.act_q = act_seq_q;
   a.pg.act_kv = act_seq_kv;

@@ -213,14 +213,6 @@ __device__ __forceinline__ void pair_commit(uint32_t el, uint64_t* bar) {
       "h"((uint16_t)3), "r"(el)
       : "memory");
 }
-// ... of this CTA only.
-__device__ __forceinline__ void pair_commit_own(uint32_t el, uint64_t* bar) {
-  asm volatile(
-      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
-      "r"(el)
-      : "memory");
-}
 // A box into this CTA's shared memory; the bytes count on `bar`, a barrier of
 // either CTA (cluster address).
 __device__ __forceinline__ void pair_tma(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -324,7 +316,7 @@ __device__ void plan_work(const Paged& p, Ctl* c, int pair, int max_pairs) {
     total += c->scan64[i];
     toks_all += c->scan64[kThreads / 32 + i];
   }
-  const bool wrong = any || (p.tnd && toks_all > p.T);
+  const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)max_pairs * INT32_MAX;
   // shares of total / np, the first total % np pairs one more
   const int np = total < 1 ? 1 : total < max_pairs ? (int)total : max_pairs;
   const long long share = total >> 32 ? total / np : (unsigned)total / (unsigned)np;
@@ -723,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok && lane == 0) mbar_arrive(&c->seg_empty[r]);
     }
     // every product done, and the other CTA's last arrivals received
-    pair_commit_own(el, &c->settle);
+    pair_commit(el, &c->settle);
     mbar_settle(&c->settle, 0, status);
     __syncwarp();
     for (int t = max(0, ntiles - 2); t < ntiles && ok; ++t) ok = warp_wait(&c->sfree[t & 1], (t >> 1) & 1, w);
@@ -919,7 +911,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // ---------------------------------------------------------------- end
   __syncthreads();
-  if (tid == 0) store_at(map_to(smem_u32(&c->peer_abort), rank ^ 1), c->abort);
+  if (tid == 0) {
+    // the last of the MMA warp's arrivals has come here too
+    if (work && !leader) mbar_settle(&c->settle, 0, status);
+    store_at(map_to(smem_u32(&c->peer_abort), rank ^ 1), c->abort);
+  }
   cluster_sync();
   const bool gave_up = c->abort || c->peer_abort;   // the same in both CTAs
   if (gave_up && tid == 0) {

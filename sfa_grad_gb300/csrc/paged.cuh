@@ -56,6 +56,8 @@ __device__ __forceinline__ SeqTok find_token(const Paged& p, int t) {
       const int l = __ffs(hit) - 1;
       const int ql = __shfl_sync(~0u, q, l);
       const long long end = __shfl_sync(~0u, sum, l);
+      r.bad = before + end > p.T;   // more tokens than there are
+      if (r.bad) return r;
       return SeqTok{b0 + l, (int)(t - (before + end - ql)), ql, false};
     }
     before += __shfl_sync(~0u, sum, 31);

@@ -6,6 +6,8 @@ checks and marshalling only, like the rest of the binding.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import Optional
 
 import torch
@@ -30,6 +32,13 @@ class PagedParams(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("wait_limit_us", ctypes.c_int32)]
 
 
+# The calls pass their parameters packed: a Structure costs more to fill than
+# the whole of a small call's checks.
+_pack_rows = struct.Struct("@iiqqqd").pack
+_pack_paged = struct.Struct("@iiqqqqqqqqqdqii").pack
+assert struct.calcsize("@iiqqqd") == ctypes.sizeof(RowsParams)
+assert struct.calcsize("@iiqqqqqqqqqdqii") == ctypes.sizeof(PagedParams)
+
 _ready = None
 
 
@@ -38,7 +47,7 @@ def _lib():
     if _ready is None:
         L = lib()
         vp, sz, d, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_double, ctypes.c_int64
-        R, P = ctypes.POINTER(RowsParams), ctypes.POINTER(PagedParams)
+        R = P = vp
         L.sfa_norm_rope.argtypes = [R] + [vp] * 15
         L.sfa_norm_rope_grad_workspace_size.argtypes = [R, ctypes.POINTER(sz)]
         L.sfa_norm_rope_grad.argtypes = [R] + [vp] * 18 + [vp, sz, vp]
@@ -57,26 +66,40 @@ def _need(name: str, t: Optional[torch.Tensor], shape, dtype, device):
     """Checks a tensor and returns its address."""
     if t is None:
         raise ValueError(f"{name} is required")
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensors must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: tensors must be contiguous")
 
 
-def _launch(device, stream, call, what):
-    """Runs call(stream handle) with `device` current."""
+def _on_stream(fn):
+    """Makes `stream` the current one for the call, so that what the call
+    allocates itself (outputs, workspace) belongs to that stream."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return call
+
+
+def _call(device, stream, fn, what, *args):
+    """fn(*args, stream handle) with `device` current."""
     if device.type != "cuda":
         raise ValueError("tensors must live on a CUDA device")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the call runs on {device}")
     if device.index == torch.cuda.current_device():
-        rc = call(torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
-            rc = call(_stream(stream))
+            rc = fn(*args, _stream(None))
     if rc:
         _check(rc, what)
 
@@ -110,10 +133,11 @@ def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved):
             raise ValueError("cos_sin is required with positions")
     if cos_sin is not None:
         cs = _need("cos_sin", cos_sin, (cos_sin.shape[0], 64), torch.float32, dev)
-    p = RowsParams(DTYPES[dt], 1 if interleaved else 0, tokens, heads, 0 if cos_sin is None else cos_sin.shape[0], eps)
-    return p, lead, heads, dt, dev, pos, cs, at
+    fields = (DTYPES[dt], 1 if interleaved else 0, tokens, heads, 0 if cos_sin is None else cos_sin.shape[0], eps)
+    return fields, lead, heads, dt, dev, pos, cs, at
 
 
+@_on_stream
 def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None, q_weight=None, q_rope=None, eps=1e-6,
               interleaved=True, outputs=None, stream=None):
     """sfa_norm_rope on torch CUDA tensors: normalises k (..., 1, 512) and q
@@ -137,11 +161,11 @@ def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None,
              for name, t, x in zip(("q", "q_rope", "k", "k_rope"), outputs, (q, q_rope, k, k_rope))]
         o += [None if x is None or t is None else _need(f"outputs: {name}", t, lead + (h,), torch.float32, dev)
               for name, t, x, h in (("q_rstd", outputs[4], q, heads), ("k_rstd", outputs[5], k, 1))]
-    _launch(dev, stream, lambda st: _lib().sfa_norm_rope(ctypes.byref(p), pos, cs, qa, qw, qra, ka, kw, kra, *o, st),
-            "sfa_norm_rope")
+    _call(dev, stream, _lib().sfa_norm_rope, "sfa_norm_rope", _pack_rows(*p), pos, cs, qa, qw, qra, ka, kw, kra, *o)
     return outputs
 
 
+@_on_stream
 def norm_rope_grad(positions, cos_sin, *, k=None, k_weight=None, k_rstd=None, dk=None, dk_rope=None, q=None,
                    q_weight=None, q_rstd=None, dq=None, dq_rope=None, interleaved=True, workspace=None, stream=None):
     """sfa_norm_rope_grad: gradients of norm_rope's inputs from those of its
@@ -157,20 +181,19 @@ def norm_rope_grad(positions, cos_sin, *, k=None, k_weight=None, k_rstd=None, dk
             _need(name, x, d.shape, dt, dev), _need(f"{name}_weight", w, (512,), dt, dev),
             _need(f"{name}_rstd", r, lead + (h,), torch.float32, dev))
     out = [None if d is None else torch.empty_like(d) for d in (dq, dq_rope, dk, dk_rope)]
-    new = torch.empty if p.T1 else torch.zeros       # no token: the weights' gradients are empty sums
+    new = torch.empty if p[2] else torch.zeros       # no token: the weights' gradients are empty sums
     out += [None if d is None else new(512, dtype=torch.float32, device=dev) for d in (dq, dk)]
-    if p.T1 == 0:
+    if p[2] == 0:
         return tuple(out)
     ws, nbytes = None, 0
     if dq is not None or dk is not None:
         if workspace is None or workspace.device != dev:
-            workspace = _workspace(norm_rope_grad_workspace_size(p), dev, workspace)
+            workspace = _workspace(norm_rope_grad_workspace_size(RowsParams(*p)), dev, workspace)
         ws, nbytes = _need("workspace", workspace, workspace.shape, workspace.dtype, dev), \
             workspace.numel() * workspace.element_size()
     o = [None if t is None else t.data_ptr() for t in out]
-    _launch(dev, stream, lambda st: _lib().sfa_norm_rope_grad(ctypes.byref(p), pos, cs, *saved["q"], *saved["k"], dqa,
-                                                              dqra, dka, dkra, *o, ws, nbytes, st),
-            "sfa_norm_rope_grad")
+    _call(dev, stream, _lib().sfa_norm_rope_grad, "sfa_norm_rope_grad", _pack_rows(*p), pos, cs, *saved["q"],
+          *saved["k"], dqa, dqra, dka, dkra, *o, ws, nbytes)
     return tuple(out)
 
 
@@ -186,24 +209,34 @@ def make_paged_params(cache, block_table, act_seq_kv, *, tokens, heads, layout="
                       scale=1.0, sparse_mode=3, interleaved=True, wait_limit_us=0) -> PagedParams:
     """Parameters of the paged calls, with checks of the cache and of the index
     tensors.  `tokens`: rows of q (B * S1 for BSND, with `seq` = S1)."""
+    return PagedParams(*_paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale,
+                               sparse_mode, interleaved, wait_limit_us)[0])
+
+
+def _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale, sparse_mode, interleaved,
+           wait_limit_us):
+    """The fields of PagedParams, and the addresses of cache, block_table,
+    act_seq_q and act_seq_kv."""
     if cache.dtype not in DTYPES:
         raise ValueError("cache must be bfloat16 or float16")
     if cache.dim() != 3 or cache.shape[2] not in (512, 576):
         raise ValueError("cache: expected (num_pages, page_size, 576) or (num_pages, page_size, 512)")
     if block_table.dim() != 2:
         raise ValueError("block_table: expected (B, max_pages)")
-    b, dev = block_table.shape[0], cache.device
-    _need("cache", cache, cache.shape, cache.dtype, dev)
-    _need("block_table", block_table, block_table.shape, torch.int32, dev)
-    _need("act_seq_kv", act_seq_kv, (b,), torch.int32, dev)
+    dev = cache.device
+    pages, page, width = cache.shape
+    b, per = block_table.shape
+    at = (_need("cache", cache, cache.shape, cache.dtype, dev),
+          _need("block_table", block_table, block_table.shape, torch.int32, dev))
+    kva = _need("act_seq_kv", act_seq_kv, (b,), torch.int32, dev)
     lay = LAYOUTS[layout.upper()]
+    qla = None
     if act_seq_q is not None or lay == 1:
-        _need("act_seq_q", act_seq_q, (b,), torch.int32, dev)
+        qla = _need("act_seq_q", act_seq_q, (b,), torch.int32, dev)
     if lay == 0 and tokens != b * seq:
         raise ValueError(f"BSND rows of {tokens} tokens do not match {b} sequences of {seq}")
-    return PagedParams(lay, DTYPES[cache.dtype], b, 0 if lay else seq, tokens if lay else 0, heads, 512,
-                       cache.shape[2] - 512, cache.shape[0], cache.shape[1], block_table.shape[1], scale, sparse_mode,
-                       1 if interleaved else 0, wait_limit_us)
+    return (lay, DTYPES[cache.dtype], b, 0 if lay else seq, tokens if lay else 0, heads, 512, width - 512, pages, page,
+            per, scale, sparse_mode, 1 if interleaved else 0, wait_limit_us), at + (qla, kva)
 
 
 def _leading(name, t, layout):
@@ -216,6 +249,7 @@ def _leading(name, t, layout):
     return lead, tokens, lead[1] if n == 2 else None
 
 
+@_on_stream
 def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *, k_weight=None, eps=1e-6,
                  interleaved=True, q_rope=None, q_rope_out=None, layout="BSND", act_seq_q=None, error=None,
                  stream=None):
@@ -228,14 +262,14 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
     SFA_DEVERR_* code.  Returns (cache, q_rope_out)."""
     lead, tokens, seq = _leading("k", k, layout)
     heads = 1 if q_rope is None else q_rope.shape[-2]
-    p = make_paged_params(cache, block_table, act_seq_kv, tokens=tokens, heads=heads, layout=layout, seq=seq,
-                          act_seq_q=act_seq_q, interleaved=interleaved)
+    p, (ca, bta, aq, akv) = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, 1.0, 3,
+                                   interleaved, 0)
     dt, dev = cache.dtype, cache.device
     ka = _need("k", k, lead + (1, 512), dt, dev)
     kw = None if k_weight is None else _need("k_weight", k_weight, (512,), dt, dev)
     kra = cs = qra = qroa = None
     table_len = 0
-    if p.Dr == 64:
+    if cache.shape[2] == 576:
         kra = _need("k_rope", k_rope, lead + (1, 64), dt, dev)
         if cos_sin is None:
             raise ValueError("cos_sin is required")
@@ -249,10 +283,8 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
     elif k_rope is not None or q_rope is not None:
         raise ValueError("rope rows given for a cache without them")
     err = None if error is None else _need("error", error, (1,), torch.int32, dev)
-    aq = None if act_seq_q is None else act_seq_q.data_ptr()
-    _launch(dev, stream, lambda st: _lib().sfa_cache_append(ctypes.byref(p), cache.data_ptr(), block_table.data_ptr(),
-                                                            aq, act_seq_kv.data_ptr(), ka, kra, kw, eps, cs, table_len,
-                                                            qra, qroa, err, st), "sfa_cache_append")
+    _call(dev, stream, _lib().sfa_cache_append, "sfa_cache_append", _pack_paged(*p), ca, bta, aq, akv, ka, kra, kw, eps,
+          cs, table_len, qra, qroa, err)
     return cache, q_rope_out
 
 
@@ -262,6 +294,7 @@ def paged_workspace_size(p: PagedParams) -> int:
     return n.value
 
 
+@_on_stream
 def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="BSND", act_seq_q=None, sparse_mode=3,
               out=None, softmax_max=None, softmax_sum=None, workspace=None, stream=None, wait_limit_us=0):
     """sfa_paged_fwd: attention of the new tokens' q (B, S1, N1, 512) or (T1,
@@ -272,31 +305,28 @@ def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="
     workspace's error word."""
     lead, tokens, seq = _leading("q", q, layout)
     heads = q.shape[-2]
-    p = make_paged_params(cache, block_table, act_seq_kv, tokens=tokens, heads=heads, layout=layout, seq=seq,
-                          act_seq_q=act_seq_q, scale=scale, sparse_mode=sparse_mode, wait_limit_us=wait_limit_us)
+    p, (ca, bta, aq, akv) = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale,
+                                   sparse_mode, True, wait_limit_us)
     dt, dev = cache.dtype, cache.device
     qa = _need("q", q, lead + (heads, 512), dt, dev)
     qra = None
-    if p.Dr == 64:
+    if cache.shape[2] == 576:
         qra = _need("q_rope", q_rope, lead + (heads, 64), dt, dev)
     elif q_rope is not None:
         raise ValueError("q_rope given for a cache without rope rows")
     st_shape = (lead[0], 1, lead[1], heads) if seq is not None else (1, tokens, heads)
     if out is None:
         out = torch.empty_like(q)
+    oa = _need("out", out, q.shape, dt, dev)
     if softmax_max is None:
         softmax_max = torch.empty(st_shape, dtype=torch.float32, device=dev)
     if softmax_sum is None:
-        softmax_sum = torch.empty(st_shape, dtype=torch.float32, device=dev)
-    oa = _need("out", out, q.shape, dt, dev)
+        softmax_sum = torch.empty_like(softmax_max)
     ma = _need("softmax_max", softmax_max, st_shape, torch.float32, dev)
     sa = _need("softmax_sum", softmax_sum, st_shape, torch.float32, dev)
     if workspace is None or workspace.device != dev:
-        workspace = _workspace(paged_workspace_size(p), dev, workspace)
+        workspace = _workspace(paged_workspace_size(PagedParams(*p)), dev, workspace)
     ws = _need("workspace", workspace, workspace.shape, workspace.dtype, dev)
-    aq = None if act_seq_q is None else act_seq_q.data_ptr()
-    _launch(dev, stream, lambda s: _lib().sfa_paged_fwd(ctypes.byref(p), qa, qra, cache.data_ptr(),
-                                                        block_table.data_ptr(), aq, act_seq_kv.data_ptr(), oa, ma, sa,
-                                                        ws, workspace.numel() * workspace.element_size(), s),
-            "sfa_paged_fwd")
+    _call(dev, stream, _lib().sfa_paged_fwd, "sfa_paged_fwd", _pack_paged(*p), qa, qra, ca, bta, aq, akv, oa, ma, sa, ws,
+          workspace.numel() * workspace.element_size())
     return out, softmax_max, softmax_sum
