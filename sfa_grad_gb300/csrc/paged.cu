@@ -21,8 +21,7 @@
 // Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
 // MMAs (only in the pair's first CTA), 6 the walk over the work with the page
 // table and the query rows, 8..15 softmax and epilogue.
-#include "kernels.h"
-#include "rows.cuh"
+#include "paged_work.cuh"
 
 namespace sfa {
 namespace {
@@ -41,47 +40,10 @@ constexpr uint32_t kOffRing = kOffP + 4 * kPanel;
 constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
 constexpr uint32_t kColS = 256;             // tensor memory: O, then two S tiles of 128 columns
 constexpr int kSegs = 8;                    // work descriptors in flight
-constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
-constexpr int kMaxPairs = kMaxSms / 2;
-// How scores are scaled.  The sign is taken out first, so that a larger score
-// is a larger weight, and a scale of zero becomes one that leaves every finite
-// score zero and a masked one -inf.
-struct Scale {
-  bool negative;
-  float scale, log2;   // |scale|, times log2(e)
-};
-// The tensor core adds each step of 16 products to a score in fp32 rounding
-// towards zero: about 0.36 x 2^-23 of the partial sum a step, 36 steps with
-// partial sums half the score on the mean.  Measured, scores are short by
-// 9 (bf16) and 12 (fp16) x 2^-24 of themselves; the scale makes that up.
-template <typename T>
-__device__ __forceinline__ Scale score_scale(float scale) {
-  constexpr float unbias = 1.0f + (Elt<T>::is_f16 ? 12 : 9) * 5.9604645e-8f;
-  const float s = fabsf(scale) * unbias;
-  return {scale < 0.f, s, fmaxf(s * kLog2e, 1e-30f)};
-}
-
-// One piece of work: key tiles kt0 .. kt1 - 1 of a row tile.
-struct Seg {
-  int row0, nrows;        // rows of q, row0 the first
-  int i0;                 // first row's index in its sequence (token * heads + head)
-  int kt0, kt1;           // kt1 = 0: end of the work
-  int kend;               // keys any row sees
-  int base;               // mode 3: last key of the sequence's first new token; mode 0: of every token
-  int slot;               // -1: whole row tile; else where the piece's result goes
-};
-
 // What the loads of a key tile need.
 struct Tile {
   int y[kKeys / 16];      // cache row of each box of vbox keys
   int key0, kend, least;  // first key; keys any row sees; last key the first row sees
-};
-
-// A piece's place in the workspace, for the merge.
-struct Piece {
-  int valid, row0, nrows;
-  int first, last;        // begins / ends its row tile
-  int pad[3];
 };
 
 struct Ctl {
@@ -97,9 +59,7 @@ struct Ctl {
   Tile tile[kTiles];
   float xbuf[2][4][64];
   long long scan64[2 * kThreads / 32];
-  long long start_off;    // units into the first sequence
-  int start_seq, start_row;
-  int bad, ntiles;        // ntiles: this pair's share
+  Share share;
   uint32_t tmem;
   int abort, peer_abort;
   // what this CTA's loaders have issued, for the end after a wait that gave up
@@ -144,44 +104,11 @@ __device__ __forceinline__ int load_from(uint32_t cluster_addr) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
-// Bounded waits of this kernel: as common.cuh's, with the limit in SM clocks
-// (a read of the global timer costs more than most waits here last).
-struct Limit {
-  volatile int* abort;
-  int* gerr;
-  long long clocks;
-};
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Limit& w) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_test(a, parity)) return true;
-  const long long t0 = clock64();
-  while (!mbar_test(a, parity)) {
-    if (*w.abort) return false;
-    if (clock64() - t0 > w.clocks) {
-      *w.abort = 1;
-      atomicExch(w.gerr, kErrTimeout);
-      return false;
-    }
-  }
-  return true;
-}
-// Wait by a whole warp: one answer for all lanes, and the lanes together again
-// before what follows (tcgen05.ld and .st want a converged warp).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Limit& w) {
-  const bool ok = wait_bar(bar, parity, w);
-  return __all_sync(~0u, ok);
-}
-
 // ------------------------------------------------------------------ tensor cores, both SMs of the pair
 // The MMA warp runs as a whole and one elected lane issues: descriptors then
 // stay in uniform registers.  Four MMAs of N = 256 from a single-lane branch
 // measured 650 clk (their descriptors move to uniform registers one by one),
 // from a converged warp 257, the tensor core's own time.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r;
-}
 // Steps 0..2, and 3, of a contraction over 64 elements; SA, SB: a step in
 // encoded descriptor units.
 template <uint32_t SA, uint32_t SB>
@@ -229,146 +156,7 @@ __device__ __forceinline__ void pair_tma3(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// ------------------------------------------------------------------ the work
-// Row tile j of a sequence: keys its last row sees, and its key tiles (at
-// least one: a tile without keys still writes its rows).
-struct SeqWork {
-  int qlen, kvlen, rows, tiles;
-};
-__device__ __forceinline__ SeqWork seq_work(const Paged& p, int b) {
-  SeqWork s;
-  s.qlen = p.act_q ? __ldg(p.act_q + b) : p.S1;
-  s.kvlen = __ldg(p.act_kv + b);
-  s.rows = s.qlen * p.G;
-  s.tiles = (s.rows + kRows - 1) / kRows;
-  return s;
-}
-__device__ __forceinline__ int tile_keys(const Paged& p, const SeqWork& s, int j) {
-  if (p.mode == 0) return s.kvlen;
-  const int tok = min((j + 1) * kRows - 1, s.rows - 1) / p.G;
-  return max(0, s.kvlen - s.qlen + tok + 1);
-}
-__device__ __forceinline__ int tile_units(const Paged& p, const SeqWork& s, int j) {
-  return max(1, (tile_keys(p, s, j) + kKeys - 1) / kKeys);
-}
-// Key tiles of row tiles 0 .. n-1, n < tiles (mode 3).  Tile j ends at token
-// (128 j + 127) / G, so its units are max(1, (j + e) / d) rounded down with d =
-// 2 G and e = (127 + G (base + 256)) / 128 rounded down: ones while j + e <
-// 2 d, then a sum over i / d.
-__device__ __forceinline__ long long units_before(const Paged& p, const SeqWork& s, int n) {
-  if (n <= 0) return 0;
-  if (p.mode == 0) return (long long)n * max(1, (s.kvlen + kKeys - 1) / kKeys);
-  const int d = kKeys / kRows * p.G;
-  const long long x = kRows - 1 + (long long)p.G * (s.kvlen - s.qlen + kKeys);
-  const long long e = x >> 7;   // / kRows, rounded down
-  const long long ones = min((long long)n, max(0LL, 2LL * d - e));
-  auto sum = [&](long long m) {   // sum of i / d over i < m
-    const long long q = (long long)((unsigned)m / (unsigned)d), r = m - q * d;
-    return d * (q * (q - 1) / 2) + q * r;
-  };
-  return ones + (ones < n ? sum(n + e) - sum(ones + e) : 0);
-}
-__device__ __forceinline__ long long seq_units(const Paged& p, const SeqWork& s) {
-  return s.tiles ? units_before(p, s, s.tiles - 1) + tile_units(p, s, s.tiles - 1) : 0;
-}
-
-// Block-wide: checks the lengths, sums the work, and finds where this pair's
-// share begins (in Ctl after the next block barrier).
-__device__ void plan_work(const Paged& p, Ctl* c, int pair, int max_pairs) {
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  long long units = 0, toks = 0;
-  bool bad = false;
-  for (int b = b0; b < b1; ++b) {
-    const SeqWork s = seq_work(p, b);
-    const bool no = s.qlen < 0 || s.kvlen < 0 || s.qlen > (p.tnd ? p.T : p.S1) ||
-                    s.kvlen > (long long)p.max_pages * p.page_size;
-    bad |= no;
-    if (!no) units += seq_units(p, s), toks += s.qlen;
-  }
-  // inclusive scans over the block's threads
-  long long u = units, t = toks;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long du = __shfl_up_sync(~0u, u, o), dt = __shfl_up_sync(~0u, t, o);
-    if (lane >= o) u += du, t += dt;
-  }
-  if (lane == 31) c->scan64[w] = u, c->scan64[kThreads / 32 + w] = t;
-  const bool any = __syncthreads_or(bad);
-  long long total = 0, toks_all = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < w) u += c->scan64[i], t += c->scan64[kThreads / 32 + i];
-    total += c->scan64[i];
-    toks_all += c->scan64[kThreads / 32 + i];
-  }
-  const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)max_pairs * INT32_MAX;
-  // shares of total / np, the first total % np pairs one more
-  const int np = total < 1 ? 1 : total < max_pairs ? (int)total : max_pairs;
-  const long long share = total >> 32 ? total / np : (unsigned)total / (unsigned)np;
-  const int rest = (int)(total - share * np);
-  const long long u0 = share * pair + min(pair, rest);
-  const int n = wrong || pair >= np ? 0 : (int)(share + (pair < rest));
-  if (tid == 0) {
-    c->bad = wrong;
-    c->ntiles = n;
-  }
-  if (n > 0 && u0 >= u - units && u0 < u) {
-    long long at = u - units, row = t - toks;
-    for (int b = b0; b < b1; ++b) {
-      const SeqWork s = seq_work(p, b);
-      const long long k = seq_units(p, s);
-      if (u0 < at + k) {
-        c->start_seq = b;
-        c->start_off = u0 - at;
-        c->start_row = (int)row;
-        break;
-      }
-      at += k;
-      row += s.qlen;
-    }
-  }
-}
-
-// The first piece's row tile: the last j with units_before(j) <= off; all
-// lanes of a warp search together.
-__device__ __forceinline__ int find_tile(const Paged& p, const SeqWork& s, long long off) {
-  int lo = 0, hi = s.tiles;   // units_before(lo) <= off < units_before(hi)
-  const int lane = threadIdx.x & 31;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 32) / 33;
-    const int j = lo + (lane + 1) * step;
-    const unsigned ok = __ballot_sync(~0u, j < hi && units_before(p, s, j) <= off);
-    const int n = __popc(ok);   // a prefix of the lanes
-    lo += n * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
-struct Args {
-  PagedArgs a;
-  int max_pairs;
-  int kbox, vbox;          // rows of a box of keys (16 .. 128) and of values (16 .. 64)
-  int* status;             // one word a CTA
-  Piece* piece;
-  float4* stats;           // (slot, row) x {max, the max P is relative to, sum, -}
-  float* part;             // (slot, row, 512)
-};
+using W = Work<kRows, kKeys, kThreads>;
 
 struct Maps2 {
   CUtensorMap q, qr;   // boxes of 64 columns x 64 rows
@@ -442,19 +230,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  plan_work(p, c, pair, args.max_pairs);   // with block barriers
+  W::plan(p, &c->share, c->scan64, pair, args.workers);   // with block barriers
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = c->tmem;
   const Limit w{&c->abort, status, (long long)(args.a.wait_ns * 21 / 10)};   // SM clock at most 2.1 GHz
-  const int ntiles = c->ntiles;
+  const int ntiles = c->share.ntiles;
   const bool work = ntiles > 0;
   // the ring holds, slot after slot, K(0) K(1) V(0) K(2) V(1) ... K(N-1) V(N-2) V(N-1)
   const uint32_t ring = smem_u32(sm + kOffRing), lead = 0;
 
-  if (c->bad && tid == 0) *status = kErrSeqLens;
+  if (c->share.bad && tid == 0) *status = kErrSeqLens;
 
   if (work && warp == 6) {
     // ---------------------------------------------------------------- the walk
@@ -463,11 +251,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int none = p.num_pages * p.page_size;     // a row outside the maps: zeros
     const int boxes = kKeys / args.vbox;
     const uint32_t qfull = map_to(smem_u32(&c->qfull), lead);
-    int b = c->start_seq, left = ntiles, tile = 0;
-    SeqWork s = seq_work(p, b);
-    int j = find_tile(p, s, c->start_off);
-    int kt = (int)(c->start_off - units_before(p, s, j));
-    int row = p.tnd ? c->start_row * p.G : b * p.S1 * p.G;   // first row of the sequence
+    int b = c->share.start_seq, left = ntiles, tile = 0;
+    SeqWork s = W::seq_work(p, b);
+    int j = W::find_tile(p, s, c->share.start_off);
+    int kt = (int)(c->share.start_off - W::units_before(p, s, j));
+    int row = p.tnd ? c->share.start_row * p.G : b * p.S1 * p.G;   // first row of the sequence
     bool ok = true;
     for (int n = 0; ok; ++n) {
       Seg g;
@@ -475,16 +263,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (left > 0) {
         while (j >= s.tiles) {
           row += (p.tnd ? s.qlen : p.S1) * p.G;
-          s = seq_work(p, ++b);
+          s = W::seq_work(p, ++b);
           j = 0;
         }
-        const int units = tile_units(p, s, j);
+        const int units = W::tile_units(p, s, j);
         g.row0 = row + j * kRows;
         g.i0 = j * kRows;
         g.nrows = min(kRows, s.rows - g.i0);
         g.kt0 = kt;
         g.kt1 = min(units, kt + left);
-        g.kend = tile_keys(p, s, j);
+        g.kend = W::tile_keys(p, s, j);
         g.base = p.mode == 3 ? s.kvlen - s.qlen : s.kvlen - 1;
         g.slot = g.kt0 == 0 && g.kt1 == units ? -1 : n == 0 ? 2 * pair : 2 * pair + 1;
         left -= g.kt1 - g.kt0;
@@ -937,165 +725,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// ------------------------------------------------------------------ merge
-// Pieces of row tiles, added in order.  The pair whose last piece begins a row
-// tile owns it.  A tile of few pieces takes a warp a row, one of many (few
-// rows over a long cache) a block a row, its warps a share of the pieces each.
-// Block 0 also sums up the error words.
-constexpr int kMergeThreads = 512;
-constexpr int kManyPieces = 16;
-
-template <typename T>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Args args) {
-  constexpr int kW = kMergeThreads / 32;
-  __shared__ int few_before[kMaxPairs + 1], many_before[kMaxPairs + 1], pieces[kMaxPairs], slot0[kMaxPairs];
-  __shared__ Piece pc[2 * kMaxPairs];
-  __shared__ float part_sum[kW];
-  __shared__ float4 part[kW][128];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, np = args.max_pairs;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int e = tid < 2 * np ? args.status[tid] : 0;
-  if (tid < 2 * np) pc[tid] = args.piece[tid];
-  const int t1 = __syncthreads_or(e == kErrTimeout), t2 = __syncthreads_or(e == kErrSeqLens),
-            t3 = __syncthreads_or(e == kErrPage);
-  if (blockIdx.x == 0 && tid == 0)
-    *reinterpret_cast<int*>(args.a.ws) = t1 ? kErrTimeout : t2 ? kErrSeqLens : t3 ? kErrPage : 0;
-  if (tid < np) {
-    const int s = pc[2 * tid + 1].valid ? 2 * tid + 1 : 2 * tid;
-    int n = 0;
-    if (pc[s].valid && pc[s].first) {
-      // this piece, then every following pair's first, up to the tile's end
-      // (a call that gave up a wait leaves the chain without its end)
-      n = 1;
-      for (int q = s; !pc[q].last && tid + n < np && pc[2 * (tid + n)].valid; ++n) q = 2 * (tid + n);
-    }
-    slot0[tid] = s;
-    pieces[tid] = n;
-  }
-  __syncthreads();
-  if (warp < 2) {   // prefix sums of the rows of tiles of few and of many pieces
-    int* before = warp ? many_before : few_before;
-    int sum = 0;
-    for (int i0 = 0; i0 < np; i0 += 32) {
-      const int i = i0 + lane;
-      int v = i < np && pieces[i] > 0 && (pieces[i] > kManyPieces) == (warp == 1) ? pc[slot0[i]].nrows : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(~0u, v, o);
-        if (lane >= o) v += u;
-      }
-      if (i < np) before[i + 1] = sum + v;
-      sum += __shfl_sync(~0u, v, 31);
-    }
-    if (lane == 0) before[0] = 0;
-  }
-  __syncthreads();
-  const Scale sc = score_scale<T>(args.a.scale);
-  auto owner = [&](const int* before, int task) {   // before[lo] <= task < before[lo + 1]
-    int lo = 0, hi = np;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (before[mid] <= task) lo = mid; else hi = mid;
-    }
-    return lo;
-  };
-  // One warp's share of a row: pieces first, first + step, ... of n, relative
-  // to the max m of all of them.  Lane l holds columns 4 l + 128 i.
-  auto gather = [&](int pair, int r, int n, int first, int step, float m, float4* o) {
-    float l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = first; i < n; i += step) {
-      const int s = i == 0 ? slot0[pair] : 2 * (pair + i);
-      const float4 st = args.stats[s * kRows + r];
-      const float4* p = reinterpret_cast<const float4*>(args.part + ((size_t)s * kRows + r) * 512) + lane;
-      const float4 v[4] = {p[0], p[32], p[64], p[96]};
-      if (st.x == -INFINITY && st.z == 0.f) continue;
-      const float f = ex2((st.y - m) * sc.log2);
-      l += st.z * f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o[k].x += v[k].x * f; o[k].y += v[k].y * f; o[k].z += v[k].z * f; o[k].w += v[k].w * f;
-      }
-    }
-    return l;
-  };
-  auto top = [&](int pair, int r, int n) {
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, args.stats[(i == 0 ? slot0[pair] : 2 * (pair + i)) * kRows + r].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    return m;
-  };
-  auto finish = [&](int pair, int r, float m, float l, const float4* o) {
-    const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-    const size_t row = (size_t)pc[slot0[pair]].row0 + r;
-    uint2* dst = reinterpret_cast<uint2*>((T*)args.a.out + row * 512) + lane;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      dst[32 * k] = make_uint2(Elt<T>::pack(o[k].x * inv, o[k].y * inv), Elt<T>::pack(o[k].z * inv, o[k].w * inv));
-    if (lane == 0) {
-      args.a.smax[row] = m == -INFINITY ? m : m * sc.scale;
-      args.a.ssum[row] = l;
-    }
-  };
-  for (int task = blockIdx.x; task < many_before[np]; task += gridDim.x) {
-    const int pair = owner(many_before, task), r = task - many_before[pair], n = pieces[pair];
-    const float m = top(pair, r, n);
-    float4 o[4];
-    const float l = gather(pair, r, n, warp, kW, m, o);
-    __syncthreads();   // the row before has been read
-#pragma unroll
-    for (int k = 0; k < 4; ++k) part[warp][lane + 32 * k] = o[k];
-    if (lane == 0) part_sum[warp] = l;
-    __syncthreads();
-    if (warp == 0) {
-      float sum = 0.f;
-      for (int w = 0; w < kW; ++w) sum += part_sum[w];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float4 a = part[0][lane + 32 * k];
-        for (int w = 1; w < kW; ++w) {
-          const float4 v = part[w][lane + 32 * k];
-          a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-        }
-        o[k] = a;
-      }
-      finish(pair, r, m, sum, o);
-    }
-  }
-  for (int task = warp * gridDim.x + blockIdx.x; task < few_before[np]; task += kW * gridDim.x) {
-    const int pair = owner(few_before, task), r = task - few_before[pair], n = pieces[pair];
-    const float m = top(pair, r, n);
-    float4 o[4];
-    const float l = gather(pair, r, n, 0, 1, m, o);
-    finish(pair, r, m, l, o);
-  }
-}
-
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr size_t kOffStatus = 256;
 const size_t kOffPiece = kOffStatus + up256(kMaxSms * sizeof(int));
-const size_t kOffStats = kOffPiece + up256(2 * kMaxPairs * sizeof(Piece));
-const size_t kOffPart = kOffStats + up256(2 * kMaxPairs * kRows * sizeof(float4));
+// two pieces a worker: pairs with pieces of 128 rows, or CTAs with pieces of 32
+const size_t kOffStats = kOffPiece + up256(2 * kMaxSms * sizeof(Piece));
+const size_t kOffPart = kOffStats + up256(kMaxSms * kRows * sizeof(float4));
 
 }  // namespace
 
-size_t paged_workspace(const Paged&) { return kOffPart + (size_t)2 * kMaxPairs * kRows * 512 * sizeof(float); }
+size_t paged_workspace(const Paged&) { return kOffPart + (size_t)kMaxSms * kRows * 512 * sizeof(float); }
+
+// Few query rows a sequence go to paged_few.cu: their time is the cache's
+// bytes, which this file's kernel takes twice (keys, then values).  32 rows of
+// 128 sequences of 2048 .. 8192 keys took 199 us here and 148 there, 32 of 64
+// sequences of 1024 .. 4096 74 and 60.  Not where a few tiles an SM are all
+// the tables can hold: it takes longer to begin and to end (one sequence of
+// 1000 keys 22.7 and 24.7 us, 128 of 30 .. 300 31 and 35; even from 10 tiles
+// an SM on).
+static bool few_rows(const Paged& p, int nsm) {
+  const long long rows = (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G;
+  return rows <= 32 && (long long)p.B * p.max_pages * p.page_size >= 640LL * nsm;
+}
 
 template <typename T>
 cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   const Paged& p = a.pg;
   Args g;
   g.a = a;
-  g.max_pairs = nsm / 2;
+  g.workers = nsm / 2;
+  g.ctas = 2 * g.workers;
   g.kbox = p.page_size % 128 == 0 ? 128 : p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
   g.vbox = g.kbox < 64 ? g.kbox : 64;
   g.status = reinterpret_cast<int*>(a.ws + kOffStatus);
   g.piece = reinterpret_cast<Piece*>(a.ws + kOffPiece);
   g.stats = reinterpret_cast<float4*>(a.ws + kOffStats);
   g.part = reinterpret_cast<float*>(a.ws + kOffPart);
+  if (few_rows(p, nsm)) {
+    g.workers = g.ctas = nsm;
+    return launch_paged_few<T>(g, st);
+  }
   Maps2 m;
   const bool f16 = Elt<T>::is_f16, rope = p.row == 576;
   const uint64_t rows = (uint64_t)p.T * p.G, cached = (uint64_t)p.num_pages * p.page_size;
@@ -1107,19 +776,10 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   auto kern = rope ? paged_kernel<T, true> : paged_kernel<T, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<2 * g.max_pairs, kThreads, kSmem, st>>>(m, g);
+  kern<<<g.ctas, kThreads, kSmem, st>>>(m, g);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * nsm);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T>, g);
+  return launch_paged_merge<T>(g, kRows, st);
 }
 
 template cudaError_t launch_paged<__nv_bfloat16>(const PagedArgs&, int, cudaStream_t);

@@ -1,0 +1,241 @@
+// What the kernels of the paged attention share: the work of a call and its
+// even split over workers (a CTA, or a pair of them), the bounded waits, the
+// scaling of scores, and the pieces that the merge adds up.
+#pragma once
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace sfa {
+
+constexpr float kRaise = 8.0f;              // log2 growth of a row's max that rescales O
+// How scores are scaled.  The sign is taken out first, so that a larger score
+// is a larger weight, and a scale of zero becomes one that leaves every finite
+// score zero and a masked one -inf.
+struct Scale {
+  bool negative;
+  float scale, log2;   // |scale|, times log2(e)
+};
+// The tensor core adds each step of 16 products to a score in fp32 rounding
+// towards zero: about 0.36 x 2^-23 of the partial sum a step, 36 steps with
+// partial sums half the score on the mean.  Measured, scores are short by
+// 9 (bf16) and 12 (fp16) x 2^-24 of themselves; the scale makes that up.
+template <typename T>
+__device__ __forceinline__ Scale score_scale(float scale) {
+  constexpr float unbias = 1.0f + (Elt<T>::is_f16 ? 12 : 9) * 5.9604645e-8f;
+  const float s = fabsf(scale) * unbias;
+  return {scale < 0.f, s, fmaxf(s * kLog2e, 1e-30f)};
+}
+
+// One piece of work: key tiles kt0 .. kt1 - 1 of a row tile.
+struct Seg {
+  int row0, nrows;        // rows of q, row0 the first
+  int i0;                 // first row's index in its sequence (token * heads + head)
+  int kt0, kt1;           // kt1 = 0: end of the work
+  int kend;               // keys any row sees
+  int base;               // mode 3: last key of the sequence's first new token; mode 0: of every token
+  int slot;               // -1: whole row tile; else where the piece's result goes
+};
+
+// A piece's place in the workspace, for the merge.
+struct Piece {
+  int valid, row0, nrows;
+  int first, last;        // begins / ends its row tile
+  int pad[3];
+};
+
+// Where a worker's share of the work begins, and its size in key tiles.
+struct Share {
+  long long start_off;    // units into the first sequence
+  int start_seq, start_row;
+  int bad, ntiles;
+};
+
+// Bounded waits of these kernels: as common.cuh's, with the limit in SM clocks
+// (a read of the global timer costs more than most waits here last).
+struct Limit {
+  volatile int* abort;
+  int* gerr;
+  long long clocks;
+};
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Limit& w) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_test(a, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_test(a, parity)) {
+    if (*w.abort) return false;
+    if (clock64() - t0 > w.clocks) {
+      *w.abort = 1;
+      atomicExch(w.gerr, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+// Wait by a whole warp: one answer for all lanes, and the lanes together again
+// before what follows (tcgen05.ld and .st want a converged warp).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Limit& w) {
+  const bool ok = wait_bar(bar, parity, w);
+  return __all_sync(~0u, ok);
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ the work
+struct SeqWork {
+  int qlen, kvlen, rows, tiles;
+};
+// The work in row tiles of kRows and key tiles of kKeys.
+template <int kRows, int kKeys, int kThreads>
+struct Work {
+  static_assert(kRows == 32 || kRows == 128, "a shift");
+  static_assert(kKeys % kRows == 0, "whole units of d");
+  // Row tile j of a sequence: keys its last row sees, and its key tiles (at
+  // least one: a tile without keys still writes its rows).
+  static __device__ __forceinline__ SeqWork seq_work(const Paged& p, int b) {
+    SeqWork s;
+    s.qlen = p.act_q ? __ldg(p.act_q + b) : p.S1;
+    s.kvlen = __ldg(p.act_kv + b);
+    s.rows = s.qlen * p.G;
+    s.tiles = (s.rows + kRows - 1) / kRows;
+    return s;
+  }
+  static __device__ __forceinline__ int tile_keys(const Paged& p, const SeqWork& s, int j) {
+    if (p.mode == 0) return s.kvlen;
+    const int tok = min((j + 1) * kRows - 1, s.rows - 1) / p.G;
+    return max(0, s.kvlen - s.qlen + tok + 1);
+  }
+  static __device__ __forceinline__ int tile_units(const Paged& p, const SeqWork& s, int j) {
+    return max(1, (tile_keys(p, s, j) + kKeys - 1) / kKeys);
+  }
+  // Key tiles of row tiles 0 .. n-1, n < tiles (mode 3).  Tile j ends at token
+  // (128 j + 127) / G, so its units are max(1, (j + e) / d) rounded down with d =
+  // 2 G and e = (127 + G (base + 256)) / 128 rounded down: ones while j + e <
+  // 2 d, then a sum over i / d.
+  static __device__ __forceinline__ long long units_before(const Paged& p, const SeqWork& s, int n) {
+    if (n <= 0) return 0;
+    if (p.mode == 0) return (long long)n * max(1, (s.kvlen + kKeys - 1) / kKeys);
+    const int d = kKeys / kRows * p.G;
+    const long long x = kRows - 1 + (long long)p.G * (s.kvlen - s.qlen + kKeys);
+    const long long e = x >> (kRows == 128 ? 7 : 5);   // / kRows, rounded down
+    const long long ones = min((long long)n, max(0LL, 2LL * d - e));
+    auto sum = [&](long long m) {   // sum of i / d over i < m
+      const long long q = (long long)((unsigned)m / (unsigned)d), r = m - q * d;
+      return d * (q * (q - 1) / 2) + q * r;
+    };
+    return ones + (ones < n ? sum(n + e) - sum(ones + e) : 0);
+  }
+  static __device__ __forceinline__ long long seq_units(const Paged& p, const SeqWork& s) {
+    return s.tiles ? units_before(p, s, s.tiles - 1) + tile_units(p, s, s.tiles - 1) : 0;
+  }
+
+  // Block-wide: checks the lengths, sums the work, and finds where this worker's
+  // share begins (in Ctl after the next block barrier).
+  static __device__ void plan(const Paged& p, Share* c, long long* scan64, int worker, int workers) {
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long units = 0, toks = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+      const SeqWork s = seq_work(p, b);
+      const bool no = s.qlen < 0 || s.kvlen < 0 || s.qlen > (p.tnd ? p.T : p.S1) ||
+                      s.kvlen > (long long)p.max_pages * p.page_size;
+      bad |= no;
+      if (!no) units += seq_units(p, s), toks += s.qlen;
+    }
+    // inclusive scans over the block's threads
+    long long u = units, t = toks;
+  #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long du = __shfl_up_sync(~0u, u, o), dt = __shfl_up_sync(~0u, t, o);
+      if (lane >= o) u += du, t += dt;
+    }
+    if (lane == 31) scan64[w] = u, scan64[kThreads / 32 + w] = t;
+    const bool any = __syncthreads_or(bad);
+    long long total = 0, toks_all = 0;
+  #pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < w) u += scan64[i], t += scan64[kThreads / 32 + i];
+      total += scan64[i];
+      toks_all += scan64[kThreads / 32 + i];
+    }
+    const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)workers * INT32_MAX;
+    // shares of total / np, the first total % np workers one more
+    const int np = total < 1 ? 1 : total < workers ? (int)total : workers;
+    const long long share = total >> 32 ? total / np : (unsigned)total / (unsigned)np;
+    const int rest = (int)(total - share * np);
+    const long long u0 = share * worker + min(worker, rest);
+    const int n = wrong || worker >= np ? 0 : (int)(share + (worker < rest));
+    if (tid == 0) {
+      c->bad = wrong;
+      c->ntiles = n;
+    }
+    if (n > 0 && u0 >= u - units && u0 < u) {
+      long long at = u - units, row = t - toks;
+      for (int b = b0; b < b1; ++b) {
+        const SeqWork s = seq_work(p, b);
+        const long long k = seq_units(p, s);
+        if (u0 < at + k) {
+          c->start_seq = b;
+          c->start_off = u0 - at;
+          c->start_row = (int)row;
+          break;
+        }
+        at += k;
+        row += s.qlen;
+      }
+    }
+  }
+
+  // The first piece's row tile: the last j with units_before(j) <= off; all
+  // lanes of a warp search together.
+  static __device__ __forceinline__ int find_tile(const Paged& p, const SeqWork& s, long long off) {
+    int lo = 0, hi = s.tiles;   // units_before(lo) <= off < units_before(hi)
+    const int lane = threadIdx.x & 31;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 32) / 33;
+      const int j = lo + (lane + 1) * step;
+      const unsigned ok = __ballot_sync(~0u, j < hi && units_before(p, s, j) <= off);
+      const int n = __popc(ok);   // a prefix of the lanes
+      lo += n * step;
+      hi = min(hi, lo + step);
+    }
+    return lo;
+  }
+};
+
+struct Args {
+  PagedArgs a;
+  int workers, ctas;       // that share the work; CTAs of the grid
+  int kbox, vbox;          // rows of a box of the cache (16 .. 128 and 16 .. 64)
+  int* status;             // one word a CTA
+  Piece* piece;
+  float4* stats;           // (slot, row) x {max, the max P is relative to, sum, -}
+  float* part;             // (slot, row, 512); slots 2 w and 2 w + 1 are worker w's
+};
+
+// Adds up the pieces of row tiles of `rows` rows (32 or 128).
+template <typename T>
+cudaError_t launch_paged_merge(const Args& g, int rows, cudaStream_t st);
+// The kernel of row tiles of 32 rows, one CTA each, and its merge.
+template <typename T>
+cudaError_t launch_paged_few(const Args& g, cudaStream_t st);
+
+}  // namespace sfa
