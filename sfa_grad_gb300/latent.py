@@ -61,20 +61,30 @@ def _lib():
 
 
 # A call on few rows takes the GPU a few microseconds, so the checks below are
-# written to cost little: one comparison a property, messages only on failure.
-def _need(name: str, t: Optional[torch.Tensor], shape, dtype, device):
+# written to cost little: one comparison a property, messages only on failure,
+# devices as their indices (-1: the CPU), and empty_strided for what is not
+# like an input (half of what torch.empty costs).
+def _need(name: str, t: Optional[torch.Tensor], shape, dtype, index):
     """Checks a tensor and returns its address."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{index}" if index >= 0 else "cpu"))
     raise ValueError(f"{name}: tensors must be contiguous")
+
+
+def _floats(shape, like):
+    strides, n = [], 1
+    for k in reversed(shape):
+        strides.append(n)
+        n *= k
+    return torch.empty_strided(shape, strides[::-1], dtype=torch.float32, device=like.device)
 
 
 def _on_stream(fn):
@@ -89,16 +99,16 @@ def _on_stream(fn):
     return call
 
 
-def _call(device, stream, fn, what, *args):
-    """fn(*args, stream handle) with `device` current."""
-    if device.type != "cuda":
+def _call(index, stream, fn, what, *args):
+    """fn(*args, stream handle) with the tensors' device current."""
+    if index < 0:
         raise ValueError("tensors must live on a CUDA device")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the call runs on {device}")
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the call runs on cuda:{index}")
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, _stream(None))
     if rc:
         _check(rc, what)
@@ -111,20 +121,22 @@ def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved):
     first = k if k is not None else q if q is not None else k_rope if k_rope is not None else q_rope
     if first is None:
         raise ValueError("at least one of q, q_rope, k, k_rope is required")
-    dt, dev = first.dtype, first.device
+    dt, dev = first.dtype, first.get_device()
     if dt not in DTYPES:
         raise ValueError("rows must be bfloat16 or float16")
     if first.dim() < 2:
         raise ValueError("rows need a head dimension: (..., heads, 512) or (..., heads, 64)")
     lead = first.shape[:-2]
     heads = q.shape[-2] if q is not None else q_rope.shape[-2] if q_rope is not None else 1
-    at = [None if t is None else _need(name, t, lead + (h, w), dt, dev)
-          for name, t, h, w in (("q", q, heads, 512), ("q_rope", q_rope, heads, 64), ("k", k, 1, 512),
-                                ("k_rope", k_rope, 1, 64))]
+    at = (None if q is None else _need("q", q, lead + (heads, 512), dt, dev),
+          None if q_rope is None else _need("q_rope", q_rope, lead + (heads, 64), dt, dev),
+          None if k is None else _need("k", k, lead + (1, 512), dt, dev),
+          None if k_rope is None else _need("k_rope", k_rope, lead + (1, 64), dt, dev))
     tokens = lead.numel()
     if (positions is None or cos_sin is None) and (q_rope is not None or k_rope is not None):
         raise ValueError("positions and cos_sin are required with q_rope or k_rope")
     pos = cs = None
+    table_len = 0
     if positions is not None:
         if positions.numel() != tokens:
             raise ValueError(f"positions: {positions.numel()} elements, expected {tokens}")
@@ -132,9 +144,9 @@ def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved):
         if cos_sin is None:
             raise ValueError("cos_sin is required with positions")
     if cos_sin is not None:
-        cs = _need("cos_sin", cos_sin, (cos_sin.shape[0], 64), torch.float32, dev)
-    fields = (DTYPES[dt], 1 if interleaved else 0, tokens, heads, 0 if cos_sin is None else cos_sin.shape[0], eps)
-    return fields, lead, heads, dt, dev, pos, cs, at
+        table_len = cos_sin.shape[0]
+        cs = _need("cos_sin", cos_sin, (table_len, 64), torch.float32, dev)
+    return (DTYPES[dt], 1 if interleaved else 0, tokens, heads, table_len, eps), lead, heads, dt, dev, pos, cs, at
 
 
 @_on_stream
@@ -153,8 +165,8 @@ def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None,
     if outputs is None:
         outputs = (None if q is None else torch.empty_like(q), None if q_rope is None else torch.empty_like(q_rope),
                    None if k is None else torch.empty_like(k), None if k_rope is None else torch.empty_like(k_rope),
-                   None if q is None else torch.empty(lead + (heads,), dtype=torch.float32, device=dev),
-                   None if k is None else torch.empty(lead + (1,), dtype=torch.float32, device=dev))
+                   None if q is None else _floats(lead + (heads,), q),
+                   None if k is None else _floats(lead + (1,), k))
         o = [None if t is None else t.data_ptr() for t in outputs]
     else:
         o = [None if x is None else _need(f"outputs: {name}", t, x.shape, dt, dev)
@@ -181,14 +193,17 @@ def norm_rope_grad(positions, cos_sin, *, k=None, k_weight=None, k_rstd=None, dk
             _need(name, x, d.shape, dt, dev), _need(f"{name}_weight", w, (512,), dt, dev),
             _need(f"{name}_rstd", r, lead + (h,), torch.float32, dev))
     out = [None if d is None else torch.empty_like(d) for d in (dq, dq_rope, dk, dk_rope)]
-    new = torch.empty if p[2] else torch.zeros       # no token: the weights' gradients are empty sums
-    out += [None if d is None else new(512, dtype=torch.float32, device=dev) for d in (dq, dk)]
-    if p[2] == 0:
+    out += [None if d is None else _floats((512,), d) for d in (dq, dk)]
+    if p[2] == 0:      # no token: the weights' gradients are empty sums
+        for t in out[4:]:
+            if t is not None:
+                t.zero_()
         return tuple(out)
     ws, nbytes = None, 0
     if dq is not None or dk is not None:
-        if workspace is None or workspace.device != dev:
-            workspace = _workspace(norm_rope_grad_workspace_size(RowsParams(*p)), dev, workspace)
+        if workspace is None or workspace.get_device() != dev:
+            workspace = _workspace(norm_rope_grad_workspace_size(RowsParams(*p)), (dk if dq is None else dq).device,
+                                   workspace)
         ws, nbytes = _need("workspace", workspace, workspace.shape, workspace.dtype, dev), \
             workspace.numel() * workspace.element_size()
     o = [None if t is None else t.data_ptr() for t in out]
@@ -223,7 +238,7 @@ def _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q
         raise ValueError("cache: expected (num_pages, page_size, 576) or (num_pages, page_size, 512)")
     if block_table.dim() != 2:
         raise ValueError("block_table: expected (B, max_pages)")
-    dev = cache.device
+    dev = cache.get_device()
     pages, page, width = cache.shape
     b, per = block_table.shape
     at = (_need("cache", cache, cache.shape, cache.dtype, dev),
@@ -264,7 +279,7 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
     heads = 1 if q_rope is None else q_rope.shape[-2]
     p, (ca, bta, aq, akv) = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, 1.0, 3,
                                    interleaved, 0)
-    dt, dev = cache.dtype, cache.device
+    dt, dev = cache.dtype, cache.get_device()
     ka = _need("k", k, lead + (1, 512), dt, dev)
     kw = None if k_weight is None else _need("k_weight", k_weight, (512,), dt, dev)
     kra = cs = qra = qroa = None
@@ -273,8 +288,8 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
         kra = _need("k_rope", k_rope, lead + (1, 64), dt, dev)
         if cos_sin is None:
             raise ValueError("cos_sin is required")
-        cs = _need("cos_sin", cos_sin, (cos_sin.shape[0], 64), torch.float32, dev)
         table_len = cos_sin.shape[0]
+        cs = _need("cos_sin", cos_sin, (table_len, 64), torch.float32, dev)
         if q_rope is not None:
             qra = _need("q_rope", q_rope, lead + (heads, 64), dt, dev)
             if q_rope_out is None:
@@ -307,7 +322,7 @@ def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="
     heads = q.shape[-2]
     p, (ca, bta, aq, akv) = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale,
                                    sparse_mode, True, wait_limit_us)
-    dt, dev = cache.dtype, cache.device
+    dt, dev = cache.dtype, cache.get_device()
     qa = _need("q", q, lead + (heads, 512), dt, dev)
     qra = None
     if cache.shape[2] == 576:
@@ -319,13 +334,13 @@ def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="
         out = torch.empty_like(q)
     oa = _need("out", out, q.shape, dt, dev)
     if softmax_max is None:
-        softmax_max = torch.empty(st_shape, dtype=torch.float32, device=dev)
+        softmax_max = _floats(st_shape, q)
     if softmax_sum is None:
         softmax_sum = torch.empty_like(softmax_max)
     ma = _need("softmax_max", softmax_max, st_shape, torch.float32, dev)
     sa = _need("softmax_sum", softmax_sum, st_shape, torch.float32, dev)
-    if workspace is None or workspace.device != dev:
-        workspace = _workspace(paged_workspace_size(PagedParams(*p)), dev, workspace)
+    if workspace is None or workspace.get_device() != dev:
+        workspace = _workspace(paged_workspace_size(PagedParams(*p)), cache.device, workspace)
     ws = _need("workspace", workspace, workspace.shape, workspace.dtype, dev)
     _call(dev, stream, _lib().sfa_paged_fwd, "sfa_paged_fwd", _pack_paged(*p), qa, qra, ca, bta, aq, akv, oa, ma, sa, ws,
           workspace.numel() * workspace.element_size())
