@@ -728,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr size_t kOffStatus = 256;
 const size_t kOffPiece = kOffStatus + up256(kMaxSms * sizeof(int));
-// two pieces a worker: pairs with pieces of 128 rows, or CTAs with pieces of 32
+// two pieces a worker: pairs with pieces of 128 rows, or CTAs with pieces of at most 64
 const size_t kOffStats = kOffPiece + up256(2 * kMaxSms * sizeof(Piece));
 const size_t kOffPart = kOffStats + up256(kMaxSms * kRows * sizeof(float4));
 
@@ -737,15 +737,18 @@ const size_t kOffPart = kOffStats + up256(kMaxSms * kRows * sizeof(float4));
 size_t paged_workspace(const Paged&) { return kOffPart + (size_t)kMaxSms * kRows * 512 * sizeof(float); }
 
 // Few query rows a sequence go to paged_few.cu: their time is the cache's
-// bytes, which this file's kernel takes twice (keys, then values).  32 rows of
-// 128 sequences of 2048 .. 8192 keys took 199 us here and 148 there, 32 of 64
-// sequences of 1024 .. 4096 74 and 60.  Not where a few tiles an SM are all
-// the tables can hold: it takes longer to begin and to end (one sequence of
-// 1000 keys 22.7 and 24.7 us, 128 of 30 .. 300 31 and 35; even from 10 tiles
-// an SM on).
-static bool few_rows(const Paged& p, int nsm) {
+// bytes, which this file's kernel takes twice (keys, then values).  128
+// sequences of 2048 .. 8192 keys took 199 us here and 142 there with 32 rows,
+// 200 and 162 with 64; with 128 rows 207 and, cut in two, 296.  Not where the
+// tables cannot hold a tile of 64 keys an SM, or ten with more than 32 rows,
+// for it takes longer to begin and to end: with 16 rows one sequence of 1000
+// keys 23 and 27 us, 128 of 30 .. 300 30.8 and 29.6, 4 of 4000 31 and 27; with
+// 64 rows one of 1000 25 and 31, 16 of 3000 33 and 37, 32 of 3000 57 and 49.
+static int few_rows(const Paged& p, int nsm) {
   const long long rows = (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G;
-  return rows <= 32 && (long long)p.B * p.max_pages * p.page_size >= 640LL * nsm;
+  const long long keys = (long long)p.B * p.max_pages * p.page_size;
+  if (rows <= 32) return keys >= 64LL * nsm ? 32 : 0;
+  return rows <= 64 && keys >= 640LL * nsm ? 64 : 0;
 }
 
 template <typename T>
@@ -761,9 +764,9 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   g.piece = reinterpret_cast<Piece*>(a.ws + kOffPiece);
   g.stats = reinterpret_cast<float4*>(a.ws + kOffStats);
   g.part = reinterpret_cast<float*>(a.ws + kOffPart);
-  if (few_rows(p, nsm)) {
+  if (const int few = few_rows(p, nsm)) {
     g.workers = g.ctas = nsm;
-    return launch_paged_few<T>(g, st);
+    return launch_paged_few<T>(g, few, st);
   }
   Maps2 m;
   const bool f16 = Elt<T>::is_f16, rope = p.row == 576;

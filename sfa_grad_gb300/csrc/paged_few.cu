@@ -1,24 +1,31 @@
 // Attention over the paged cache for few query rows a sequence: row tiles of
-// 32 (token, head) rows, one CTA each (paged.cu takes tiles of 128 with pairs
-// of CTAs and decides which calls come here).
+// R = 32 or 64 (token, head) rows, one CTA each (paged.cu takes tiles of 128
+// with pairs of CTAs and decides which calls come here).
 //
 // With few rows the cache's bytes decide, so a tile of 64 keys is loaded once:
 // its panels (64 keys x 64 features, 128-byte swizzle) are the K-major operand
 // of S^T = K Q^T and, two at a time, the MN-major one of O^T = V^T P^T.  Keys
 // and features lie on M and the rows on N, so both products cost what the rows
-// that are there cost: 36 MMAs of 25 clk and 16 of 40 a tile.
+// that are there cost: 36 MMAs and 16, of 25 and 41 clk each at 32 rows, of 33
+// and 49 at 64.
 //
-// S^T has a key a lane: a thread keeps its own maximum and sum of every row
-// and P stays relative to a row's stale reference, so the rows' maxima are
-// brought together only when a score exceeds its reference by 2^8, and at the
-// end.
+// A warp reads the scores of 16 keys as matrix fragments, so that all lanes
+// have work (M = 64 leaves half the lanes of tensor memory empty).  A thread
+// keeps its own maximum and sum of every row it meets and P stays relative to
+// a row's stale reference: the rows' maxima are brought together only when a
+// score exceeds its reference by 2^8, and at the end.
 //
-// The ring holds ten slots of two panels, four a tile, so up to 2.5 tiles are
-// on their way or worked on.  Each product has a warp of its own: one warp that
-// looked at both products' barriers in turn spent 650 clk a slot where its
-// eight MMAs take 200, and the loads waited for it (128 sequences x 16 heads of
-// 2048 .. 16384 keys: 302 us, now 246, the loads alone 226; 5.7 TB/s of the
-// cache's bytes).  Work is split and merged as in paged.cu.
+// The ring holds ten slots of two panels (eight at 64 rows), four a tile, so
+// up to 2.5 tiles are on their way or worked on.  Each product has a warp of
+// its own: one warp that looked at both products' barriers in turn spent 650
+// clk a slot where its eight MMAs take 200, and the loads waited for it.
+//
+// Measured: 128 sequences x 16 heads of 2048 .. 16384 keys 239 us, 5.9 TB/s of
+// the cache's bytes (302 with the rows on M, the loads alone 226); 128 x 64
+// heads of 2048 .. 8192 keys 161 us, 4.7 TB/s: with eight slots the loads wait
+// for the products, a tile takes 3900 clk.
+//
+// Work is split and merged as in paged.cu.
 //
 // Warps: 0..7 softmax, rescaling, epilogue, 8 the scores' MMAs, 15 the values',
 // 9 the walk with the page table and the query rows, 10..13 the loads of a
@@ -28,27 +35,31 @@
 namespace sfa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kSoft = 8;
-constexpr int kRows = 32, kKeys = 64;
-constexpr int kCols = 16;                   // rows of a softmax thread
+constexpr int kKeys = 64;
+constexpr int kSoft = 8;                    // softmax warps, the first ones
+constexpr int kThreads = 32 * (kSoft + 8);
 constexpr int kSegs = 4;                    // work descriptors in flight
 constexpr int kTiles = 8;                   // tiles whose cache rows are known in advance
+constexpr int kMaxSlots = 10;
 constexpr uint32_t kPanel = 8192;           // 64 rows of 128 bytes
 constexpr uint32_t kSlot = 2 * kPanel;
 constexpr uint32_t kColS = 256;             // tensor memory: O^T, 64 columns a block of 128 features, then two S^T
 
-constexpr int kSlots = 10;
-constexpr int kHalves = kRows / kCols;      // softmax warps of a key
-constexpr uint32_t kQPanel = kRows * 128;
-constexpr uint32_t kOffP = 9 * kQPanel;     // P^T: 64 keys x 64 rows
-constexpr uint32_t kOffRope = kOffP + kPanel;
-constexpr uint32_t kOffRing = kOffRope + 2 * kPanel;
-constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
-using W = Work<kRows, kKeys, kThreads>;
+// What follows from the rows of a row tile.
+template <int R>
+struct Few {
+  static constexpr int kWide = R / 2;                  // rows of a softmax warp
+  static constexpr int kSlots = R == 32 ? 10 : 8;
+  static constexpr uint32_t kQPanel = R * 128;
+  static constexpr uint32_t kOffP = 9 * kQPanel;       // P^T: 64 keys x 64 rows
+  static constexpr uint32_t kOffRope = kOffP + kPanel;
+  static constexpr uint32_t kOffRing = kOffRope + 2 * kPanel;
+  static constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
+  using W = Work<R, kKeys, kThreads>;
+};
 
 struct Ctl {
-  uint64_t full[kSlots], empty[kSlots], rfull[2], rempty[2];
+  uint64_t full[kMaxSlots], empty[kMaxSlots], rfull[2], rempty[2];
   uint64_t qfull, qempty, sfull[2], sfree[2], pready, pfree, ofree;
   uint64_t xch, fch, settle[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -59,12 +70,14 @@ struct Ctl {
   int abort;
   Seg seg[kSegs];
   int y[kTiles][4];                         // cache row of each box of a tile
-  int loads[kSlots], rloads[2];                 // uses of a slot that have been issued
-  float rbuf[kRows], fbuf[kRows];                 // a row's reference (times log2) and its factor for O
+  int loads[kMaxSlots], rloads[2];                 // uses of a slot that have been issued
+  alignas(16) float rbuf[64];
+  float fbuf[64];                 // a row's reference (times log2) and its factor for O
 };
-constexpr uint32_t kSmem = kOffCtl + sizeof(Ctl) + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory");
-static_assert(kSmem > kOneCtaSmem, "one CTA an SM: it allocates all of tensor memory");
+template <int R>
+constexpr uint32_t kSmem = Few<R>::kOffCtl + sizeof(Ctl) + 1024;
+static_assert(kSmem<32> <= 227 * 1024 && kSmem<64> <= 227 * 1024, "shared memory");
+static_assert(kSmem<32> > kOneCtaSmem && kSmem<64> > kOneCtaSmem, "one CTA an SM: it allocates all of tensor memory");
 
 // The four steps of a contraction over 64 elements, by the elected lane of a
 // converged warp; SA, SB: a step in encoded descriptor units.
@@ -87,17 +100,45 @@ __device__ __forceinline__ void commit(uint32_t el, uint64_t* bar) {
       "r"(el)
       : "memory");
 }
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+// 16 lanes x 8 N columns of tensor memory as matrix fragments: v[4 j + 2 h + e]
+// is lane (thread / 4) + 8 h, column 8 j + 2 (thread % 4) + e.
+template <int N>
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
+  static_assert(N == 2 || N == 4, "");
+  uint32_t r[4 * N];
+  if constexpr (N == 2)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 struct MapsFew {
-  CUtensorMap q, qr;   // boxes of 64 columns x 32 rows
+  CUtensorMap q, qr;   // boxes of 64 columns x R rows
   CUtensorMap c2, c1;  // the cache, boxes of vbox rows of two panels (vbox = 64 only) and of one
 };
 
-template <typename T, bool ROPE>
-__global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_constant__ MapsFew maps, const Args args) {
+template <typename T, bool ROPE, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_few_kernel(const __grid_constant__ MapsFew maps, const Args args) {
+  using F = Few<R>;
+  using W = typename F::W;
+  constexpr int kSlots = F::kSlots;
+  constexpr uint32_t kQPanel = F::kQPanel, kOffP = F::kOffP, kOffRope = F::kOffRope, kOffRing = F::kOffRing;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  Ctl* c = reinterpret_cast<Ctl*>(sm + kOffCtl);
+  Ctl* c = reinterpret_cast<Ctl*>(sm + F::kOffCtl);
   const Paged& p = args.a.pg;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   constexpr int kPanels = ROPE ? 9 : 8;
@@ -131,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
     mbar_fence_init();
   } else if (warp == 1) {
     if (lane < kSegs) mbar_init(&c->seg_full[lane], 1), mbar_init(&c->seg_empty[lane], kSoft + 2);
+    c->rbuf[lane] = c->rbuf[lane + 32] = -INFINITY;
     if (lane < kTiles) mbar_init(&c->tile_full[lane], 1), mbar_init(&c->tile_empty[lane], 4 + ROPE);
     if (lane < kSlots) {
       mbar_init(&c->full[lane], 1);
@@ -142,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
     const CUtensorMap* m = lane == 0 ? &maps.q : lane == 1 ? &maps.qr : lane == 2 ? &maps.c2 : &maps.c1;
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   }
-  if (warp == 9) tmem_alloc(&c->tmem, 512);
+  if (warp == kSoft + 1) tmem_alloc(&c->tmem, 512);
   // (the scan's sums lie in the ring, which nothing has been loaded into yet)
   W::plan(p, &c->share, reinterpret_cast<long long*>(sm + kOffRing), cta, args.workers);
   fence_async_smem();
@@ -157,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
 
   if (c->share.bad && tid == 0) *status = kErrSeqLens;
 
-  if (work && warp == 9) {
+  if (work && warp == kSoft + 1) {
     // ---------------------------------------------------------------- the walk
     const int none = p.num_pages * p.page_size;     // a row outside the map: zeros
     const int boxes = kKeys / args.vbox;
@@ -177,9 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
           j = 0;
         }
         const int units = W::tile_units(p, s, j);
-        g.row0 = row + j * kRows;
-        g.i0 = j * kRows;
-        g.nrows = min(kRows, s.rows - g.i0);
+        g.row0 = row + j * R;
+        g.i0 = j * R;
+        g.nrows = min(R, s.rows - g.i0);
         g.kt0 = kt;
         g.kt1 = min(units, kt + left);
         g.kend = W::tile_keys(p, s, j);
@@ -229,11 +271,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
     }
     // rows on their way, where another warp gave up
     if (issued > 0) mbar_settle(&c->qfull, (issued - 1) & 1, status);
-  } else if (work && warp >= 10 && warp < 14 + ROPE) {
+  } else if (work && warp >= kSoft + 2 && warp < kSoft + 6 + ROPE) {
     // ---------------------------------------------------------------- TMA loads
     const int boxes = kKeys / args.vbox;
     const int pl = boxes == 1 ? 0 : lane / boxes, pb = boxes == 1 ? 0 : lane % boxes;   // panel, box of a lane
-    const int k = warp - 10;   // slot of the tile, 4: rope
+    const int k = warp - (kSoft + 2);   // slot of the tile, 4: rope
     const bool is_rope = k == 4;
     for (int t = 0; t < ntiles; ++t) {
       const int i = t % kTiles, u = 4 * t + k;
@@ -256,10 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
         tma_3d(dst + pl * kPanel + pb * args.vbox * 128, &maps.c1, 0, y, 2 * k + pl, full);
       }
     }
-  } else if (work && warp == 8) {
+  } else if (work && warp == kSoft) {
     // ---------------------------------------------------------------- scores
     const uint32_t el = elect_one();
-    constexpr uint32_t ids = idesc_f16(kKeys, kRows, Elt<T>::is_f16, false, false);
+    constexpr uint32_t ids = idesc_f16(kKeys, R, Elt<T>::is_f16, false, false);
     const uint64_t dq = sdesc_kmajor(smem_u32(sm), 0), dk = sdesc_kmajor(ring, 0), dr = sdesc_kmajor(rope, 0);
     int s = 0, ph = 0, segs = 0, left = 0;   // ring slot and its phase; pieces; tiles of the piece to come
     bool ok = true;
@@ -296,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
     }
     commit(el, &c->settle[0]);
     mbar_settle(&c->settle[0], 0, status);
-  } else if (work && warp == 15) {
+  } else if (work && warp == kSoft + 7) {
     // ---------------------------------------------------------------- products with the values
     // (a warp of their own: neither product waits for the other's slots)
     const uint32_t el = elect_one();
@@ -328,17 +370,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
     }
     commit(el, &c->settle[1]);
     mbar_settle(&c->settle[1], 0, status);
-  } else if (work && warp < 8) {
+  } else if (work && warp < kSoft) {
     // ---------------------------------------------------------------- softmax, epilogue
-    // Lane l < 16 of warps q and q + 4: key 16 q + l of a tile (M = 64 puts 16
-    // keys in each warp's quarter of tensor memory), rows c0 .. c0 + kCols - 1;
-    // every lane: feature 32 q + l of two blocks of O^T.  Lane l of a warp
-    // with q = 0 brings row c0 + l together.
-    const int wq = warp & 3, cg = warp >> 2, c0 = cg * kCols;
-    const bool act = cg < kHalves, owner = act && wq == 0 && lane < kCols;
-    const int key = wq * 16 + (lane & 15);
+    // Warps q and q + 4: keys 16 q .. 16 q + 15 of a tile (M = 64 puts 16 keys
+    // in each warp's quarter of tensor memory), rows c0 .. c0 + kWide - 1.  A
+    // thread has keys key and key + 8 and, of every eight rows, two:
+    // row(i) = c0 + 8 (i / 2) + 2 (lane % 4) + i % 2.  Every lane: feature 32 q +
+    // lane of two blocks of O^T.  Lane l of a warp with q = 0 brings row c0 + l
+    // together.
+    constexpr int kWide = F::kWide, kHas = kWide / 4;   // rows of a warp, of a thread
+    const int wq = warp & 3, cg = warp >> 2, c0 = cg * kWide, r0 = c0 + 2 * (lane & 3);
+    const bool owner = wq == 0 && lane < kWide;
+    const int key = wq * 16 + (lane >> 2);
     const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t prow = smem_u32(sm + kOffP) + key * 128;
+    const uint32_t pkey = smem_u32(sm + kOffP) + key * 128 + (lane & 3) * 4;   // P's row of key; key + 8: 1024 on
     float* scratch = reinterpret_cast<float*>(sm + kOffP);   // P's place, when no product reads it
     const Scale sc = score_scale<T>(args.a.scale);
     int tile = 0, nx = 0, nf = 0;
@@ -358,22 +403,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
       if (lane == 0) mbar_arrive(&c->fch);
       return warp_wait(&c->fch, nf++ & 1, w);
     };
-    // a value of each row over a warp's 16 keys, into the scratch: each step
-    // halves the rows a lane keeps, until lane l has row c0 + l
+    // a value of each row over a warp's keys, into the scratch: each step
+    // halves the rows a lane keeps
     auto gather = [&](const float* v, bool sum, int at) {
-      float u[kCols];
+      float u[kHas];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) u[i] = v[i];
+      for (int i = 0; i < kHas; ++i) u[i] = v[i];
+      int i = 0;
 #pragma unroll
-      for (int o = 8; o; o >>= 1) {
+      for (int o = 16, n = kHas / 2; o >= 4; o >>= 1, n >>= 1) {
         const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-          const float e = __shfl_xor_sync(~0u, up ? u[i] : u[i + o], o), k = up ? u[i + o] : u[i];
-          u[i] = sum ? k + e : fmaxf(k, e);
+        if (n == 0) {   // one row left: both lanes keep it
+          const float e = __shfl_xor_sync(~0u, u[0], o);
+          u[0] = sum ? u[0] + e : fmaxf(u[0], e);
+          continue;
         }
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+          const float e = __shfl_xor_sync(~0u, up ? u[k] : u[k + n], o), x = up ? u[k + n] : u[k];
+          u[k] = sum ? x + e : fmaxf(x, e);
+        }
+        if (up) i += n;
       }
-      if (lane < 16) scratch[at * 256 + wq * 64 + c0 + lane] = u[0];
+      if (kHas == 8 || !(lane & 4)) scratch[at * 256 + wq * 64 + r0 + 8 * (i >> 1) + (i & 1)] = u[0];
     };
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -385,40 +437,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
       if (g.kt1 == 0) break;
       const int least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;   // last key the tile's first row sees
       const int cols = (g.nrows + 15) / 16 * 16;
-      // of this thread's key, by row: the max of its scores, the row's
-      // reference times log2, the sum of its weights
-      float m[kCols], ref[kCols], l[kCols];
+      // of this thread's keys, by row: the max of their scores, the sum of
+      // their weights
+      float m[kHas], l[kHas];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) m[i] = ref[i] = -INFINITY, l[i] = 0.f;
+      for (int i = 0; i < kHas; ++i) m[i] = -INFINITY, l[i] = 0.f;
       float mtop = -INFINITY, mref = -INFINITY;   // an owner's row: its max, its reference
       for (int kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
         const int buf = tile & 1;
         if (!(ok = warp_wait(&c->sfull[buf], (tile >> 1) & 1, w))) break;
         tc_fence_after();
         const bool edge = (kt + 1) * kKeys > least + 1;
-        float x[kCols];
+        float x[2 * kHas];   // [4 j + 2 h + e]: key + 8 h, row(2 j + e)
+        tmem_ld_frag<kWide / 8>(tq + kColS + buf * 64 + c0, x);
+        if (sc.negative) {
+#pragma unroll
+          for (int i = 0; i < 2 * kHas; ++i) x[i] = -x[i];
+        }
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 2 * kHas; ++i) {
+            const int j = kt * kKeys + key + 4 * (i & 2), r = r0 + 8 * (i >> 2) + (i & 1);
+            if (j >= g.kend || j > (p.mode == 3 ? g.base + (g.i0 + r) / p.G : g.base)) x[i] = -INFINITY;
+          }
+        }
         bool rises = false;
-        if (act) {
-          tmem_ld16(tq + kColS + buf * 64 + c0, x);
-          if (sc.negative) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) x[i] = -x[i];
-          }
-          if (edge) {
-            const int j = kt * kKeys + key;
-#pragma unroll
-            for (int i = 0; i < kCols; ++i)
-              if (j >= g.kend || j > (p.mode == 3 ? g.base + (g.i0 + c0 + i) / p.G : g.base)) x[i] = -INFINITY;
-          }
-          if (lane >= 16) {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) x[i] = -INFINITY;
-          }
-#pragma unroll
-          for (int i = 0; i < kCols; ++i) {
-            m[i] = fmaxf(m[i], x[i]);
-            rises |= fmaf(x[i], sc.log2, -ref[i]) > kRaise;
-          }
+        for (int j = 0; j < kHas / 2; ++j) {
+          const float2 ref = *reinterpret_cast<const float2*>(c->rbuf + r0 + 8 * j);
+          const float t0 = fmaxf(x[4 * j], x[4 * j + 2]), t1 = fmaxf(x[4 * j + 1], x[4 * j + 3]);
+          m[2 * j] = fmaxf(m[2 * j], t0);
+          m[2 * j + 1] = fmaxf(m[2 * j + 1], t1);
+          rises |= fmaf(t0, sc.log2, -ref.x) > kRaise || fmaf(t1, sc.log2, -ref.y) > kRaise;
         }
         tc_fence_before();
         rises = __any_sync(~0u, rises);
@@ -428,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
         // P and O belong to the products of the tile before until they end
         if (any) {
           if (tile > 0 && !(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
-          if (act) gather(m, false, 0);
+          gather(m, false, 0);
           if (!(ok = sync())) break;
           if (owner) {
             // a stale reference keeps P below 2^8, which both types hold as
@@ -444,19 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
             c->fbuf[c0 + lane] = f;
           }
           if (!(ok = sync())) break;
-          if (act) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-              ref[i] = c->rbuf[c0 + i];
-              l[i] *= c->fbuf[c0 + i];
-            }
-          }
+          for (int i = 0; i < kHas; ++i) l[i] *= c->fbuf[r0 + 8 * (i >> 1) + (i & 1)];
           if (kt > g.kt0) {
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < 2 * cols; q += 16) {
-              const int col = q < cols ? q : q - cols;
-              const uint32_t at = tq + (2 * cg + (q >= cols)) * 64 + col;
+              const int blk = q >= cols, col = q - (blk ? cols : 0);
+              const uint32_t at = tq + (2 * cg + blk) * 64 + col;
               float o[16];
               tmem_ld16(at, o);
 #pragma unroll
@@ -465,16 +510,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
             }
           }
         }
-        uint32_t pk[kCols / 2];
-        if (act) {
+        uint32_t pk[kHas];   // [2 j + h]
 #pragma unroll
-          for (int i = 0; i < kCols / 2; ++i) {
-            const float r0 = ref[2 * i] == -INFINITY ? 0.f : ref[2 * i];
-            const float r1 = ref[2 * i + 1] == -INFINITY ? 0.f : ref[2 * i + 1];
-            const float a = ex2(fmaf(x[2 * i], sc.log2, -r0)), b = ex2(fmaf(x[2 * i + 1], sc.log2, -r1));
-            l[2 * i] += a;
-            l[2 * i + 1] += b;
-            pk[i] = Elt<T>::pack(a, b);
+        for (int j = 0; j < kHas / 2; ++j) {
+          const float2 ref = *reinterpret_cast<const float2*>(c->rbuf + r0 + 8 * j);
+          const float a = ref.x == -INFINITY ? 0.f : ref.x, b = ref.y == -INFINITY ? 0.f : ref.y;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float u = ex2(fmaf(x[4 * j + 2 * h], sc.log2, -a)), v = ex2(fmaf(x[4 * j + 2 * h + 1], sc.log2, -b));
+            l[2 * j] += u;
+            l[2 * j + 1] += v;
+            pk[2 * j + h] = Elt<T>::pack(u, v);
           }
         }
         if (!any && tile > 0 && !(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
@@ -500,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
             sts128(base + q * 128, v);
           }
         }
-        if (act && lane < 16) {
 #pragma unroll
-          for (int i = 0; i < kCols / 8; ++i)
-            sts128(prow + (((c0 / 8 + i) ^ (key & 7)) << 4),
-                   make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]));
+        for (int j = 0; j < kHas / 2; ++j) {
+          const uint32_t at = pkey + (((c0 / 8 + j) ^ (key & 7)) << 4);
+          sts32(at, pk[2 * j]);
+          sts32(at + 1024, pk[2 * j + 1]);
         }
         fence_async_smem();
         tc_fence_before();
@@ -513,10 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
       }
       if (!ok) break;
       if (!(ok = warp_wait(&c->pfree, (tile - 1) & 1, w))) break;
-      if (act) {
-        gather(m, false, 0);
-        gather(l, true, 1);
-      }
+      gather(m, false, 0);
+      gather(l, true, 1);
       if (!(ok = sync())) break;
       const bool whole = g.slot < 0;
       float lsum = 0.f;
@@ -525,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
         mtop = fmaxf(fmaxf(s[0], s[64]), fmaxf(s[128], s[192]));
         lsum = (s[256] + s[320]) + (s[384] + s[448]);
         c->fbuf[c0 + lane] = lsum > 0.f || lsum != lsum ? 1.0f / lsum : 0.f;
+        c->rbuf[c0 + lane] = -INFINITY;   // for the next piece
       }
       if (!(ok = sync())) break;
       tc_fence_after();
@@ -541,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
           for (int i = 0; i < 16; ++i)
             if (col + i < g.nrows) dst[i * 512] = Elt<T>::from_f(o[i] * c->fbuf[col + i]);
         } else {
-          float* dst = args.part + ((size_t)g.slot * kRows + col) * 512 + feat + blk * 128;
+          float* dst = args.part + ((size_t)g.slot * R + col) * 512 + feat + blk * 128;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (col + i < g.nrows) dst[i * 512] = o[i];
@@ -553,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
           args.a.smax[row] = mtop == -INFINITY ? mtop : mtop * sc.scale;
           args.a.ssum[row] = lsum > 0.f ? lsum * ex2((mref - mtop) * sc.log2) : lsum;
         } else {
-          args.stats[g.slot * kRows + c0 + lane] = make_float4(mtop, mref, lsum, 0.f);
+          args.stats[g.slot * R + c0 + lane] = make_float4(mtop, mref, lsum, 0.f);
         }
       }
       tc_fence_before();
@@ -570,32 +615,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_few_kernel(const __grid_con
     const int s = tid < kSlots ? tid : tid - kSlots, n = tid < kSlots ? c->loads[s] : c->rloads[s];
     if (n > 0) mbar_settle(tid < kSlots ? &c->full[s] : &c->rfull[s], (n - 1) & 1, status);
   }
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kSoft + 1) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
 
-template <typename T>
-cudaError_t launch_paged_few(const Args& g, cudaStream_t st) {
+template <typename T, int R>
+static cudaError_t launch_few(const Args& g, cudaStream_t st) {
   const Paged& p = g.a.pg;
   MapsFew m;
   const bool f16 = Elt<T>::is_f16, rope = p.row == 576;
   const uint64_t rows = (uint64_t)p.T * p.G, cached = (uint64_t)p.num_pages * p.page_size;
-  if (!encode_map2d(&m.q, f16, g.a.q, 512, rows, kRows) ||
-      !encode_map2d(&m.qr, f16, rope ? g.a.qr : g.a.q, rope ? 64 : 512, rows, kRows) ||
+  if (!encode_map2d(&m.q, f16, g.a.q, 512, rows, R) ||
+      !encode_map2d(&m.qr, f16, rope ? g.a.qr : g.a.q, rope ? 64 : 512, rows, R) ||
       !encode_map_panels(&m.c2, f16, g.a.cache, p.row, cached, g.vbox, g.vbox == 64 ? 2 : 1) ||
       !encode_map_panels(&m.c1, f16, g.a.cache, p.row, cached, g.vbox, 1))
     return cudaErrorInvalidValue;
-  auto kern = rope ? paged_few_kernel<T, true> : paged_few_kernel<T, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  auto kern = rope ? paged_few_kernel<T, true, R> : paged_few_kernel<T, false, R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
   if (e != cudaSuccess) return e;
-  kern<<<g.ctas, kThreads, kSmem, st>>>(m, g);
+  kern<<<g.ctas, kThreads, kSmem<R>, st>>>(m, g);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_paged_merge<T>(g, kRows, st);
+  return launch_paged_merge<T>(g, R, st);
 }
 
-template cudaError_t launch_paged_few<__nv_bfloat16>(const Args&, cudaStream_t);
-template cudaError_t launch_paged_few<__half>(const Args&, cudaStream_t);
+template <typename T>
+cudaError_t launch_paged_few(const Args& g, int rows, cudaStream_t st) {
+  return rows == 32 ? launch_few<T, 32>(g, st) : launch_few<T, 64>(g, st);
+}
+
+template cudaError_t launch_paged_few<__nv_bfloat16>(const Args&, int, cudaStream_t);
+template cudaError_t launch_paged_few<__half>(const Args&, int, cudaStream_t);
 
 }  // namespace sfa

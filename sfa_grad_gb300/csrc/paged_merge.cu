@@ -154,8 +154,9 @@ cudaError_t launch_paged_merge(const Args& g, int rows, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return rows == 32 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 32>, g)
-                    : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 128>, g);
+  return rows == 32   ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 32>, g)
+         : rows == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 64>, g)
+                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, 128>, g);
 }
 
 template cudaError_t launch_paged_merge<__nv_bfloat16>(const Args&, int, cudaStream_t);

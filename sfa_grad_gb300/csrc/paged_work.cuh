@@ -104,7 +104,7 @@ struct SeqWork {
 // The work in row tiles of kRows and key tiles of kKeys.
 template <int kRows, int kKeys, int kThreads>
 struct Work {
-  static_assert(kRows == 32 || kRows == 128, "a shift");
+  static_assert(kRows == 32 || kRows == 64 || kRows == 128, "a shift");
   static_assert(kKeys % kRows == 0, "whole units of d");
   // Row tile j of a sequence: keys its last row sees, and its key tiles (at
   // least one: a tile without keys still writes its rows).
@@ -133,7 +133,7 @@ struct Work {
     if (p.mode == 0) return (long long)n * max(1, (s.kvlen + kKeys - 1) / kKeys);
     const int d = kKeys / kRows * p.G;
     const long long x = kRows - 1 + (long long)p.G * (s.kvlen - s.qlen + kKeys);
-    const long long e = x >> (kRows == 128 ? 7 : 5);   // / kRows, rounded down
+    const long long e = x >> (kRows == 128 ? 7 : kRows == 64 ? 6 : 5);   // / kRows, rounded down
     const long long ones = min((long long)n, max(0LL, 2LL * d - e));
     auto sum = [&](long long m) {   // sum of i / d over i < m
       const long long q = (long long)((unsigned)m / (unsigned)d), r = m - q * d;
@@ -231,11 +231,11 @@ struct Args {
   float* part;             // (slot, row, 512); slots 2 w and 2 w + 1 are worker w's
 };
 
-// Adds up the pieces of row tiles of `rows` rows (32 or 128).
+// Adds up the pieces of row tiles of `rows` rows (32, 64 or 128).
 template <typename T>
 cudaError_t launch_paged_merge(const Args& g, int rows, cudaStream_t st);
-// The kernel of row tiles of 32 rows, one CTA each, and its merge.
+// The kernel of row tiles of 32 or 64 rows, one CTA each, and its merge.
 template <typename T>
-cudaError_t launch_paged_few(const Args& g, cudaStream_t st);
+cudaError_t launch_paged_few(const Args& g, int rows, cudaStream_t st);
 
 }  // namespace sfa

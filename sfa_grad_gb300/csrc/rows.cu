@@ -8,7 +8,11 @@
 // Bound by HBM: every row is read once and written once, in 16-byte pieces, a
 // row of 512 by one warp that keeps it in registers between the sum and the
 // scaling.  One launch covers all four tensors: ranges of blocks take the key
-// rows, the query rows and the rotated rows.
+// rows, the query rows and the rotated rows.  Measured (a plain copy reaches
+// 6.8 TB/s): 4096 tokens, keys normed, 128 query heads rotated, bf16: 24.6 us,
+// 5.9 TB/s; their gradients 32.4 us, 4.6 TB/s, with the second launch that adds
+// up the weight's; 16381 tokens x 16 normed heads, fp16, gradients: 166 us, 5.6
+// TB/s.
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -16,8 +20,13 @@ namespace sfa {
 namespace {
 
 constexpr int kWarps = 8;       // warps of a block
-constexpr int kGradBlocks = 3;  // blocks of the gradient's rows of 512 an SM
-constexpr int kPieces = 8;      // 16-byte pieces a lane rotates at once (32 rows of 64 a warp)
+// Blocks of the gradient's rows of 512 an SM.  Two leave the keys of 4096
+// tokens waiting (the gradients of that step 43 us instead of 37), four take
+// registers away from the row in flight (16381 x 16 heads 240 instead of 166).
+constexpr int kGradBlocks = 3;
+// 16-byte pieces a lane rotates at once (32 rows of 64 a warp): the gradients
+// of 4096 x 128 heads took 41 us with two, 37 with four, 32 with eight.
+constexpr int kPieces = 8;
 
 __device__ __forceinline__ bool padded(const RowsArgs& a, int t) {
   if (!a.pos) return false;

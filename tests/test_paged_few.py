@@ -1,5 +1,5 @@
 """Attention over the paged cache for few query rows a sequence (row tiles of
-32): calls whose sequences have at most 32 (token, head) rows on the mean and
+32 or 64): calls whose sequences have at most 64 (token, head) rows on the mean and
 whose block tables can hold a long cache."""
 import pytest
 import torch
@@ -30,6 +30,13 @@ CASES = {
     "borders": ([1] * 11, [1, 62, 63, 64, 65, 127, 128, 129, 255, 256, 257], 16, "bf16", 64, True, 3, "TND", None, 3),
     "heads_32": ([1] * 5, [700, 64, 1, 130, 2000], 32, "bf16", 128, True, 3, "BSND", 1, 0),
     "heads_17": ([1, 0, 1, 1], [400, 90, 33, 70], 17, "fp16", 48, True, 3, "TND", None, 2),
+    "heads_33": ([1] * 6, [700, 64, 1, 130, 2000, 63], 33, "fp16", 128, True, 3, "BSND", 1, 0),
+    "heads_64": ([1] * 5 + [0], [900, 65, 1, 128, 3000, 70], 64, "bf16", 64, True, 3, "TND", None, 1),
+    "drafts_60": ([3, 2, 1, 0], [500, 2, 64, 67], 20, "bf16", 32, True, 3, "BSND", 3, 0),
+    "no_mask_64": ([1, 2], [200, 40], 32, "fp16", 48, True, 0, "TND", None, 0),
+    "no_rope_64": ([1, 1, 1], [500, 129, 3], 50, "bf16", 64, False, 3, "TND", None, 0),
+    "long_64": ([1], [30000], 64, "bf16", 64, True, 3, "BSND", 1, 0),
+    "uneven_64": ([40] + [1] * 30, [300] + list(range(1, 31)), 24, "fp16", 16, True, 3, "TND", None, 0),
     "drafts": ([3, 2, 1, 4], [500, 2, 64, 67], 8, "bf16", 32, True, 3, "BSND", 4, 0),
     "more_new_than_cached": ([4, 4], [3, 70], 5, "fp16", 16, True, 3, "BSND", 4, 0),
     # a few tokens on the mean, many of one sequence: several row tiles of it
@@ -56,13 +63,14 @@ def test_few(name):
     _check(x, _call(x, mode=mode, layout=layout, **_buffers(x)), qlens, kvlens, mode=mode, layout=layout)
 
 
+@pytest.mark.parametrize("name", ["long_3", "heads_64"])
 @pytest.mark.parametrize("scale", [0.7, -SCALE, 0.0])
-def test_few_scales(scale):
-    x, qlens, kvlens, mode, layout = _inputs("long_3")
+def test_few_scales(scale, name):
+    x, qlens, kvlens, mode, layout = _inputs(name)
     _check(x, _call(x, scale, mode, layout, **_buffers(x)), qlens, kvlens, scale, mode, layout)
 
 
-@pytest.mark.parametrize("heads,dtype", [(16, "bf16"), (32, "fp16")])
+@pytest.mark.parametrize("heads,dtype", [(16, "bf16"), (32, "fp16"), (64, "bf16")])
 def test_few_rising_scores(heads, dtype):
     """Scores that rise along the keys, so that O is rescaled tile after tile."""
     qlens, kvlens = [1, 1], [2500, 90]
@@ -76,10 +84,11 @@ def test_few_rising_scores(heads, dtype):
     _check(x, _call(x, 0.3, **_buffers(x)), qlens, kvlens, 0.3)
 
 
-def test_few_nan_ahead():
+@pytest.mark.parametrize("heads", [16, 32])
+def test_few_nan_ahead(heads):
     """Non-finite rows of the cache reach only the tokens that see them."""
     qlens, kvlens = [3, 1], [130, 70]
-    x = _wide(paged_inputs(qlens, kvlens, 16, "bf16"))
+    x = _wide(paged_inputs(qlens, kvlens, heads, "bf16"))
     clean = _call(x, **_buffers(x))[0]
     flat = x["cache"].flatten(0, 1)
     for at, v in ((128, float("inf")), (129, float("nan"))):      # seen by tokens 1 and 2, and by token 2
@@ -137,7 +146,7 @@ def test_few_bad_lengths(what):
     assert sfa.read_device_error(ws) == 0
 
 
-@pytest.mark.parametrize("name", ["long", "many"])
+@pytest.mark.parametrize("name", ["long", "many", "long_64"])
 def test_few_wait_timeout_then_recovery(name):
     """As the other kernels': a limit of a microsecond ends the call early or
     every wait was shorter, and the next call on the workspace is right."""
@@ -153,12 +162,14 @@ def test_few_wait_timeout_then_recovery(name):
     _check(x, got, qlens, kvlens, mode=mode, layout=layout)
 
 
-def test_few_and_many_rows_agree():
+@pytest.mark.parametrize("heads", [32, 64])
+def test_few_and_many_rows_agree(heads):
     """The same sequences through both kernels (by the table's width): equal
     up to the two orders of summation."""
-    x = paged_inputs([1] * 6, [900, 64, 65, 3000, 1, 500], 32, "bf16")
+    kvlens = [500, 64, 65, 900, 1, 300]
+    x = paged_inputs([1] * 6, kvlens, heads, "bf16")
     a = _call(x, **_buffers(x))
     b = _call(_wide(x), **_buffers(x))
-    _check(x, a, [1] * 6, [900, 64, 65, 3000, 1, 500])
-    _check(x, b, [1] * 6, [900, 64, 65, 3000, 1, 500])
+    _check(x, a, [1] * 6, kvlens)
+    _check(x, b, [1] * 6, kvlens)
     assert not all(torch.equal(u, v) for u, v in zip(a, b))     # two kernels indeed
