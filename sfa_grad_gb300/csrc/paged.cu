@@ -59,7 +59,7 @@ struct Ctl {
   Seg seg[kSegs];
   Tile tile[kTiles];
   float xbuf[2][4][64];
-  long long scan64[2 * kThreads / 32];
+  long long scan64[3 * kThreads / 32];
   Share share;
   uint32_t tmem;
   int abort, peer_abort;
@@ -157,7 +157,8 @@ __device__ __forceinline__ void pair_tma3(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-using W = Work<kRows, kKeys, kThreads>;
+// (a row tile's beginning and end take about as long as a key tile and a half)
+using W = Work<kRows, kKeys, kThreads, 1>;
 
 struct Maps2 {
   CUtensorMap q, qr;   // boxes of 64 columns x 64 rows
@@ -254,11 +255,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int none = p.num_pages * p.page_size;     // a row outside the maps: zeros
     const int boxes = kKeys / args.vbox;
     const uint32_t qfull = map_to(smem_u32(&c->qfull), lead);
-    int b = c->share.start_seq, left = ntiles, tile = 0;
+    int b = c->share.seq, left = ntiles, tile = 0;
     SeqWork s = W::seq_work(p, b);
-    int j = W::find_tile(p, s, c->share.start_off);
-    int kt = (int)(c->share.start_off - W::units_before(p, s, j));
-    int row = p.tnd ? c->share.start_row * p.G : b * p.S1 * p.G;   // first row of the sequence
+    int j = c->share.tile, kt = c->share.kt, row = c->share.row;   // row: the sequence's first
     bool ok = true;
     for (int n = 0; ok; ++n) {
       Seg g;

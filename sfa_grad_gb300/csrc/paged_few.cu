@@ -55,7 +55,7 @@ struct Few {
   static constexpr uint32_t kOffRope = kOffP + kPanel;
   static constexpr uint32_t kOffRing = kOffRope + 2 * kPanel;
   static constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
-  using W = Work<R, kKeys, kThreads>;
+  using W = Work<R, kKeys, kThreads, 2>;
 };
 
 struct Ctl {
@@ -203,11 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- the walk
     const int none = p.num_pages * p.page_size;     // a row outside the map: zeros
     const int boxes = kKeys / args.vbox;
-    int b = c->share.start_seq, left = ntiles, tile = 0, issued = 0;
+    int b = c->share.seq, left = ntiles, tile = 0, issued = 0;
     SeqWork s = W::seq_work(p, b);
-    int j = W::find_tile(p, s, c->share.start_off);
-    int kt = (int)(c->share.start_off - W::units_before(p, s, j));
-    int row = p.tnd ? c->share.start_row * p.G : b * p.S1 * p.G;   // first row of the sequence
+    int j = c->share.tile, kt = c->share.kt, row = c->share.row;   // row: the sequence's first
     bool ok = true;
     for (int n = 0; ok; ++n) {
       Seg g;

@@ -43,11 +43,13 @@ struct Piece {
   int pad[3];
 };
 
-// Where a worker's share of the work begins, and its size in key tiles.
+// A worker's share of the work: where it begins, and its size in key tiles.
 struct Share {
-  long long start_off;    // units into the first sequence
-  int start_seq, start_row;
+  int seq, row, tile, kt;      // sequence, its first row, row tile of it, key tile of that
   int bad, ntiles;
+  // the two ends: sequence, offset into its cost, key tiles before it
+  int end_seq[2];
+  long long end_off[2], end_before[2], end_units[2];
 };
 
 // Bounded waits of these kernels: as common.cuh's, with the limit in SM clocks
@@ -102,7 +104,7 @@ struct SeqWork {
   int qlen, kvlen, rows, tiles;
 };
 // The work in row tiles of kRows and key tiles of kKeys.
-template <int kRows, int kKeys, int kThreads>
+template <int kRows, int kKeys, int kThreads, int kOwn>
 struct Work {
   static_assert(kRows == 32 || kRows == 64 || kRows == 128, "a shift");
   static_assert(kKeys % kRows == 0, "whole units of d");
@@ -145,74 +147,112 @@ struct Work {
     return s.tiles ? units_before(p, s, s.tiles - 1) + tile_units(p, s, s.tiles - 1) : 0;
   }
 
-  // Block-wide: checks the lengths, sums the work, and finds where this worker's
-  // share begins (in Ctl after the next block barrier).
-  static __device__ void plan(const Paged& p, Share* c, long long* scan64, int worker, int workers) {
+  // Row tiles cost their key tiles and kOwn more, their beginning and end (none
+  // where the workers get a key tile each at most): the cost before row tile n.
+  static __device__ __forceinline__ long long cost_before(const Paged& p, const SeqWork& s, int n, int own) {
+    return units_before(p, s, n) + (long long)own * n;
+  }
+
+  // Block-wide: checks the lengths, adds up the work and splits its cost evenly
+  // and in order; this worker's share is in `c` after the next block barrier.
+  // scan: 3 * kThreads / 32 elements.
+  static __device__ void plan(const Paged& p, Share* c, long long* scan, int worker, int workers) {
+    constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long units = 0, toks = 0;
+    int tiles = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
       const SeqWork s = seq_work(p, b);
       const bool no = s.qlen < 0 || s.kvlen < 0 || s.qlen > (p.tnd ? p.T : p.S1) ||
                       s.kvlen > (long long)p.max_pages * p.page_size;
       bad |= no;
-      if (!no) units += seq_units(p, s), toks += s.qlen;
+      if (!no) units += seq_units(p, s), tiles += s.tiles, toks += s.qlen;
     }
     // inclusive scans over the block's threads
     long long u = units, t = toks;
-  #pragma unroll
+    int g = tiles;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long du = __shfl_up_sync(~0u, u, o), dt = __shfl_up_sync(~0u, t, o);
-      if (lane >= o) u += du, t += dt;
+      const int dg = __shfl_up_sync(~0u, g, o);
+      if (lane >= o) u += du, t += dt, g += dg;
     }
-    if (lane == 31) scan64[w] = u, scan64[kThreads / 32 + w] = t;
+    if (lane == 31) scan[w] = u, scan[kWarps + w] = t, scan[2 * kWarps + w] = g;
     const bool any = __syncthreads_or(bad);
-    long long total = 0, toks_all = 0;
-  #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < w) u += scan64[i], t += scan64[kThreads / 32 + i];
-      total += scan64[i];
-      toks_all += scan64[kThreads / 32 + i];
+    long long total = 0, toks_all = 0, tiles_all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < w) u += scan[i], t += scan[kWarps + i], g += (int)scan[2 * kWarps + i];
+      total += scan[i];
+      toks_all += scan[kWarps + i];
+      tiles_all += scan[2 * kWarps + i];
     }
-    const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)workers * INT32_MAX;
-    // shares of total / np, the first total % np workers one more
+    const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)workers * (INT32_MAX / 2);
     const int np = total < 1 ? 1 : total < workers ? (int)total : workers;
-    const long long share = total >> 32 ? total / np : (unsigned)total / (unsigned)np;
-    const int rest = (int)(total - share * np);
-    const long long u0 = share * worker + min(worker, rest);
-    const int n = wrong || worker >= np ? 0 : (int)(share + (worker < rest));
+    const int own = total > workers ? kOwn : 0;
+    // shares of cost / np, the first cost % np workers one more
+    const long long cost = total + own * tiles_all;
+    const long long share = cost >> 32 ? cost / np : (unsigned)cost / (unsigned)np;
+    const int rest = (int)(cost - share * np);
+    const bool mine = !wrong && total > 0 && worker < np;
+    const long long first = share * worker + min(worker, rest), last = first + share + (worker < rest);
+    const long long from = u - units + (long long)own * (g - tiles), to = u + (long long)own * g;
     if (tid == 0) {
       c->bad = wrong;
-      c->ntiles = n;
+      c->ntiles = 0;
+      if (last == cost) c->end_seq[1] = -1, c->end_units[1] = total;
     }
-    if (n > 0 && u0 >= u - units && u0 < u) {
-      long long at = u - units, row = t - toks;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long at = e ? last : first;
+      if (!mine || at < from || at >= to) continue;
+      long long before = u - units, row = t - toks, cum = from;
       for (int b = b0; b < b1; ++b) {
         const SeqWork s = seq_work(p, b);
-        const long long k = seq_units(p, s);
-        if (u0 < at + k) {
-          c->start_seq = b;
-          c->start_off = u0 - at;
-          c->start_row = (int)row;
+        const long long k = seq_units(p, s), all = k + (long long)own * s.tiles;
+        if (at < cum + all) {
+          c->end_seq[e] = b;
+          c->end_off[e] = at - cum;
+          c->end_before[e] = before;
+          if (e == 0) c->row = (int)(p.tnd ? row : (long long)b * p.S1) * p.G;
           break;
         }
-        at += k;
+        cum += all;
+        before += k;
         row += s.qlen;
       }
     }
+    __syncthreads();
+    if (mine && w < 2) {
+      // warp e: the row tile and key tile of end e
+      const int b = c->end_seq[w];
+      if (b >= 0) {
+        const SeqWork s = seq_work(p, b);
+        const long long off = c->end_off[w];
+        const int j = find_tile(p, s, off, own);
+        const int kt = (int)max(0LL, off - cost_before(p, s, j, own) - own);
+        if (lane == 0) {
+          c->end_units[w] = c->end_before[w] + units_before(p, s, j) + kt;
+          if (w == 0) c->seq = b, c->tile = j, c->kt = kt;
+        }
+      }
+    }
+    __syncthreads();
+    if (mine && tid == 0) c->ntiles = (int)(c->end_units[1] - c->end_units[0]);
   }
 
-  // The first piece's row tile: the last j with units_before(j) <= off; all
-  // lanes of a warp search together.
-  static __device__ __forceinline__ int find_tile(const Paged& p, const SeqWork& s, long long off) {
-    int lo = 0, hi = s.tiles;   // units_before(lo) <= off < units_before(hi)
+  // The row tile at an offset into a sequence's cost: the last j with
+  // cost_before(j) <= off; all lanes of a warp search together.
+  static __device__ __forceinline__ int find_tile(const Paged& p, const SeqWork& s, long long off, int own) {
+    int lo = 0, hi = s.tiles;   // cost_before(lo) <= off < cost_before(hi)
     const int lane = threadIdx.x & 31;
     while (hi - lo > 1) {
       const int step = (hi - lo + 32) / 33;
       const int j = lo + (lane + 1) * step;
-      const unsigned ok = __ballot_sync(~0u, j < hi && units_before(p, s, j) <= off);
+      const unsigned ok = __ballot_sync(~0u, j < hi && cost_before(p, s, j, own) <= off);
       const int n = __popc(ok);   // a prefix of the lanes
       lo += n * step;
       hi = min(hi, lo + step);
