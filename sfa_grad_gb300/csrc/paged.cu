@@ -12,11 +12,19 @@
 // SM stages only half of every B operand: the keys of its half of the tile for
 // S = Q K^T, its half of the features for O += P V.
 //
-// Work: every row tile counts its key tiles; the pairs split the total
-// evenly and in order, so a pair takes some whole row tiles and at most one
-// piece of a tile at each end.  Pieces leave (m, l, O) in fp32 and a second
-// kernel merges them in order: few rows over a long cache spread over all
-// SMs, and the result does not depend on timing.
+// Work: every row tile counts its key tiles, and one more for its beginning and
+// end; the pairs split the total evenly and in order, so a pair takes some
+// whole row tiles and at most one piece of a tile at each end.  (Without the
+// one more, a chunk of 532 tokens x 128 heads over 768 keys took 159 us, now
+// 109: the first pairs got twice the row tiles of the last.)  Pieces leave
+// (m, l, O) in fp32 and a second kernel merges them in order: few rows over a
+// long cache spread over all SMs, and the result does not depend on timing.
+//
+// Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1405 to
+// 1455 us (1640 to 1580 TFLOP/s; the tensor pipe is busy 71 % of the cycles,
+// the rest is switches between the two products and late slots); 64 sequences
+// x 128 heads, one token each, 262,000 keys, 103 us: there bound by the bytes
+// into shared memory, which keys and values pass separately.
 //
 // Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
 // MMAs (only in the pair's first CTA), 6 the walk over the work with the page
@@ -243,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool work = ntiles > 0;
   // the ring holds, slot after slot, K(0) K(1) V(0) K(2) V(1) ... K(N-1) V(N-2) V(N-1);
   // at the end of a piece V(t) comes before K(t+1), whose S waits for other
-  // query rows (a chunk of 512 tokens x 128 heads over 2000 keys: @@)
+  // query rows (64 sequences x 128 heads, one token each: 112 -> 105 us)
   const uint32_t ring = smem_u32(sm + kOffRing), lead = 0;
 
   if (c->share.bad && tid == 0) *status = kErrSeqLens;
