@@ -671,33 +671,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       char* dst = whole ? (char*)args.a.out + ((size_t)(g.row0 + row0) * 512 + col) * sizeof(T)
                         : (char*)(args.part + ((size_t)g.slot * kRows + row0) * 512 + col);
       const int stride = 512 * (whole ? (int)sizeof(T) : 4);
-      for (int q = 0; q < 128;) {
-        uint4 v[8];   // 128 bytes of the thread's row
+      const int fill = whole ? 3 : 1;   // 16 columns are 32 or 64 of a row's 128 staged bytes
+      const int piece = lane & 7;
+      // (rolled: this code runs once a piece, and fetching it took longer than
+      // running it; unrolled, 6300 clk instead of @@)
+#pragma unroll 1
+      for (int q = 0; q < 8; ++q) {
+        float o[16];
+        tmem_ld16(tq + cg * 128 + q * 16, o);
+        const uint32_t line = stage + lane * 128;
         if (whole) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float o[32];
-            tmem_ld32(tq + cg * 128 + q + half * 32, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= inv;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[half * 4 + i] = pack8<T>(o + 8 * i);
-          }
-          q += 64;
+          for (int i = 0; i < 16; ++i) o[i] *= inv;
+          const int at = 2 * (q & 3);
+          sts128(line + ((at ^ (lane & 7)) << 4), pack8<T>(o));
+          sts128(line + (((at + 1) ^ (lane & 7)) << 4), pack8<T>(o + 8));
         } else {
-          float o[32];
-          tmem_ld32(tq + cg * 128 + q, o);
+          const int at = 4 * (q & 1);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            v[i] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                              __float_as_uint(o[4 * i + 3]));
-          q += 32;
+          for (int i = 0; i < 4; ++i)
+            sts128(line + (((at + i) ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                              __float_as_uint(o[4 * i + 3])));
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sts128(stage + lane * 128 + ((i ^ (lane & 7)) << 4), v[i]);
+        if ((q & fill) != fill) continue;
         __syncwarp();
-        const int piece = lane & 7;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < 8; ++i) {
           const int k = i * 4 + (lane >> 3);
           const uint4 u = lds128(stage + k * 128 + ((piece ^ (k & 7)) << 4));
