@@ -15,15 +15,15 @@
 // Work: every row tile counts its key tiles, and one more for its beginning and
 // end; the pairs split the total evenly and in order, so a pair takes some
 // whole row tiles and at most one piece of a tile at each end.  (Without the
-// one more, a chunk of 532 tokens x 128 heads over 768 keys took 159 us, now
-// 109: the first pairs got twice the row tiles of the last.)  Pieces leave
+// one more, a chunk of 532 tokens x 128 heads over 768 keys took 159 us, with
+// it 109: the first pairs got twice the row tiles of the last.)  Pieces leave
 // (m, l, O) in fp32 and a second kernel merges them in order: few rows over a
 // long cache spread over all SMs, and the result does not depend on timing.
 //
 // Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1405 to
 // 1455 us (1640 to 1580 TFLOP/s; the tensor pipe is busy 71 % of the cycles,
 // the rest is switches between the two products and late slots); 64 sequences
-// x 128 heads, one token each, 262,000 keys, 103 us: there bound by the bytes
+// x 128 heads, one token each, 262,000 keys, 101 us: there bound by the bytes
 // into shared memory, which keys and values pass separately.
 //
 // Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
@@ -673,8 +673,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int stride = 512 * (whole ? (int)sizeof(T) : 4);
       const int fill = whole ? 3 : 1;   // 16 columns are 32 or 64 of a row's 128 staged bytes
       const int piece = lane & 7;
-      // (rolled: this code runs once a piece, and fetching it took longer than
-      // running it; unrolled, 6300 clk instead of @@)
+      // (rolled: this code runs once a piece, and fetching it takes longer than
+      // running it; unrolled, 6300 clk instead of 4800)
 #pragma unroll 1
       for (int q = 0; q < 8; ++q) {
         float o[16];
