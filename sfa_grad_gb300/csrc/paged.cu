@@ -20,10 +20,10 @@
 // (m, l, O) in fp32 and a second kernel merges them in order: few rows over a
 // long cache spread over all SMs, and the result does not depend on timing.
 //
-// Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1405 to
-// 1455 us (1640 to 1580 TFLOP/s; the tensor pipe is busy 71 % of the cycles,
-// the rest is switches between the two products and late slots); 64 sequences
-// x 128 heads, one token each, 262,000 keys, 101 us: there bound by the bytes
+// Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1385
+// us (1660 TFLOP/s; the tensor pipe is busy 71 % of the cycles, the rest is
+// switches between the two products and late slots); 64 sequences
+// x 128 heads, one token each, 262,000 keys, 99 us: there bound by the bytes
 // into shared memory, which keys and values pass separately.
 //
 // Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
@@ -52,7 +52,6 @@ constexpr int kSegs = 8;                    // work descriptors in flight
 struct Tile {
   int y[kKeys / 16];      // cache row of each box of vbox keys
   int key0, kend, least;  // first key; keys any row sees; last key the first row sees
-  int ends;               // the piece's last tile
 };
 
 struct Ctl {
@@ -249,9 +248,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const Limit w{&c->abort, status, (long long)(args.a.wait_ns * 21 / 10)};   // SM clock at most 2.1 GHz
   const int ntiles = c->share.ntiles;
   const bool work = ntiles > 0;
-  // the ring holds, slot after slot, K(0) K(1) V(0) K(2) V(1) ... K(N-1) V(N-2) V(N-1);
-  // at the end of a piece V(t) comes before K(t+1), whose S waits for other
-  // query rows (64 sequences x 128 heads, one token each: 112 -> 105 us)
+  // the ring holds, slot after slot, K(0) K(1) V(0) K(2) V(1) ... K(N-1) V(N-2) V(N-1),
+  // over the ends of pieces too: V(t) before K(t+1) there cost every tile more in
+  // code than it gained (512 tokens x 128 heads over 16384 keys 1425 us, so 1385)
   const uint32_t ring = smem_u32(sm + kOffRing), lead = 0;
 
   if (c->share.bad && tid == 0) *status = kErrSeqLens;
@@ -318,7 +317,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           c->tile[i].key0 = t * kKeys;
           c->tile[i].kend = g.kend;
           c->tile[i].least = p.mode == 3 ? g.base + g.i0 / p.G : g.base;
-          c->tile[i].ends = t + 1 == g.kt1;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->tile_full[i]);
@@ -413,23 +411,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     int u = s, base = 0;   // the slot's next use; the first use of the block below
     for (int t = -1; t < ntiles && ok; ++t) {
-      const bool ends = t >= 0 && c->tile[t % kTiles].ends;
+      if (t + 1 < ntiles) {
+        const int i = (t + 1) % kTiles;
+        if (!(ok = warp_wait(&c->tile_full[i], ((t + 1) / kTiles) & 1, w))) break;
 #pragma unroll 1
-      for (int step = 0; step < 2 && ok; ++step) {
-        if ((step == 0) != ends) {
-          if (t + 1 == ntiles) continue;
-          const int i = (t + 1) % kTiles;
-          if (!(ok = warp_wait(&c->tile_full[i], ((t + 1) / kTiles) & 1, w))) break;
+        for (; u < base + kKSlots && ok; u += kSlots) load_k(c->tile[i], u - base);
+        base += kKSlots;
+      }
+      if (t >= 0) {
 #pragma unroll 1
-          for (; u < base + kKSlots && ok; u += kSlots) load_k(c->tile[i], u - base);
-          base += kKSlots;
-        } else if (t >= 0) {
-#pragma unroll 1
-          for (; u < base + kVSlots && ok; u += kSlots) load_v(c->tile[t % kTiles], u - base);
-          base += kVSlots;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c->tile_empty[t % kTiles]);
-        }
+        for (; u < base + kVSlots && ok; u += kSlots) load_v(c->tile[t % kTiles], u - base);
+        base += kVSlots;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->tile_empty[t % kTiles]);
       }
     }
     // the slot's last release has arrived: none is on its way to a CTA that
@@ -437,8 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (ok && k > 0) warp_wait(&c->empty[s], (k - 1) & 1, w);
   } else if (work && leader && warp == 4) {
     // ---------------------------------------------------------------- MMAs
-    // In the ring's order, S one tile ahead within a piece: S(0) S(1) PV(0) S(2)
-    // PV(1) ...
+    // In the ring's order, S one tile ahead: S(0) S(1) PV(0) S(2) PV(1) ...
     // One warp takes every slot in turn: two, one for each product, could
     // meet a slot's barrier a whole phase early and mistake it for a phase
     // late.  The next slot's barrier is looked at before a slot's last MMA,
@@ -510,15 +503,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     for (int t = -1; t < ntiles && ok; ++t) {
       const int len = pv_left == 0 ? pv_next : 0;   // of the piece that tile t begins
-      const bool ends = t >= 0 && (len ? len : pv_left) == 1;
-#pragma unroll 1
-      for (int step = 0; step < 2 && ok; ++step) {
-        if ((step == 0) != ends) {
-          if (t + 1 < ntiles) products_s(t + 1);
-        } else if (t >= 0) {
-          products_v(t, len);
-        }
-      }
+      if (t + 1 < ntiles) products_s(t + 1);
+      if (t >= 0 && ok) products_v(t, len);
     }
     if (ok) {   // the end mark
       const int r = segs % kSegs;
