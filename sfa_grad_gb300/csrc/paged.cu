@@ -20,10 +20,10 @@
 // (m, l, O) in fp32 and a second kernel merges them in order: few rows over a
 // long cache spread over all SMs, and the result does not depend on timing.
 //
-// Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1385
-// us (1660 TFLOP/s; the tensor pipe is busy 71 % of the cycles, the rest is
+// Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1357
+// us (1695 TFLOP/s; the tensor pipe is busy 71 % of the cycles, the rest is
 // switches between the two products and late slots); 64 sequences
-// x 128 heads, one token each, 262,000 keys, 99 us: there bound by the bytes
+// x 128 heads, one token each, 262,000 keys, 98 us: there bound by the bytes
 // into shared memory, which keys and values pass separately.
 //
 // Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
@@ -431,7 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (ok && k > 0) warp_wait(&c->empty[s], (k - 1) & 1, w);
   } else if (work && leader && warp == 4) {
     // ---------------------------------------------------------------- MMAs
-    // In the ring's order, S one tile ahead: S(0) S(1) PV(0) S(2) PV(1) ...
+    // In the ring's order, S one tile ahead: S(0) S(1) PV(0) S(2) PV(1) ...  The
+    // loops over slots are unrolled by 3 and 4: by 1 they cost 6 % each in loop
+    // code between the MMAs, by 9 and 8 24 % in fetching it.
     // One warp takes every slot in turn: two, one for each product, could
     // meet a slot's barrier a whole phase early and mistake it for a phase
     // late.  The next slot's barrier is looked at before a slot's last MMA,
@@ -487,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!(ok = warp_wait(&c->pready, t & 1, w))) return;
       tc_fence_after();   // ... and reads and rescaling of O
-#pragma unroll 2
+#pragma unroll 4
       for (int i = 0; i < kVSlots; ++i) {
         const int s = slot();
         if (!ok) return;

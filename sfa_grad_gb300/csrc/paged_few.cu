@@ -20,9 +20,9 @@
 // its own: one warp that looked at both products' barriers in turn spent 650
 // clk a slot where its eight MMAs take 200, and the loads waited for it.
 //
-// Measured: 128 sequences x 16 heads of 2048 .. 16384 keys 239 us, 5.9 TB/s of
-// the cache's bytes (302 with the rows on M, the loads alone 226); 128 x 64
-// heads of 2048 .. 8192 keys 161 us, 4.7 TB/s: with eight slots the loads wait
+// Measured: 128 sequences x 16 heads of 2048 .. 16384 keys 228 us, 6.2 TB/s of
+// the cache's bytes (302 with the rows on M); 128 x 64 heads of 2048 .. 8192
+// keys 158 us, 4.8 TB/s: with eight slots the loads wait
 // for the products, a tile takes 3900 clk.
 //
 // Work is split and merged as in paged.cu.
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t >= 2 && !(ok = warp_wait(&c->sfree[buf], (t / 2 - 1) & 1, w))) break;
       tc_fence_after();   // the softmax warps' reads of this S buffer
       const uint32_t d = tmem + kColS + buf * 64;
-#pragma unroll 1
+#pragma unroll 2
       for (int i = 0; i < 4; ++i) {
         if (!(ok = warp_wait(&c->full[s], ph, w))) break;
         const uint64_t a = dk + desc_off(s * kSlot), b = dq + desc_off(2 * i * kQPanel);
