@@ -23,10 +23,12 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Args a
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int e = tid < args.ctas ? args.status[tid] : 0;
   if (tid < 2 * np) pc[tid] = args.piece[tid];
-  const int t1 = __syncthreads_or(e == kErrTimeout), t2 = __syncthreads_or(e == kErrSeqLens),
-            t3 = __syncthreads_or(e == kErrPage);
-  if (blockIdx.x == 0 && tid == 0)
-    *reinterpret_cast<int*>(args.a.ws) = t1 ? kErrTimeout : t2 ? kErrSeqLens : t3 ? kErrPage : 0;
+  if (blockIdx.x == 0) {
+    const int t1 = __syncthreads_or(e == kErrTimeout), t2 = __syncthreads_or(e == kErrSeqLens),
+              t3 = __syncthreads_or(e == kErrPage);
+    if (tid == 0) *reinterpret_cast<int*>(args.a.ws) = t1 ? kErrTimeout : t2 ? kErrSeqLens : t3 ? kErrPage : 0;
+  }
+  __syncthreads();
   if (tid < np) {
     const int s = pc[2 * tid + 1].valid ? 2 * tid + 1 : 2 * tid;
     int n = 0;
@@ -111,25 +113,28 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Args a
     const int worker = owner(many_before, task), r = task - many_before[worker], n = pieces[worker];
     const float m = top(worker, r, n);
     float4 o[4];
-    const float l = gather(worker, r, n, warp, kW, m, o);
+    const float share = gather(worker, r, n, warp, kW, m, o);
     __syncthreads();   // the row before has been read
 #pragma unroll
     for (int k = 0; k < 4; ++k) part[warp][lane + 32 * k] = o[k];
-    if (lane == 0) part_sum[warp] = l;
+    if (lane == 0) part_sum[warp] = share;
     __syncthreads();
-    if (warp == 0) {
-      float sum = 0.f;
-      for (int w = 0; w < kW; ++w) sum += part_sum[w];
+    if (tid < 256) {   // two columns a thread, the warps in ascending order
+      float l = 0.f;
+      float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float4 a = part[0][lane + 32 * k];
-        for (int w = 1; w < kW; ++w) {
-          const float4 v = part[w][lane + 32 * k];
-          a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-        }
-        o[k] = a;
+      for (int w = 0; w < kW; ++w) {
+        const float2 v = reinterpret_cast<const float2*>(part[w])[tid];
+        l += part_sum[w];
+        a.x += v.x; a.y += v.y;
       }
-      finish(worker, r, m, sum, o);
+      const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+      const size_t row = (size_t)pc[slot0[worker]].row0 + r;
+      reinterpret_cast<uint32_t*>((T*)args.a.out + row * 512)[tid] = Elt<T>::pack(a.x * inv, a.y * inv);
+      if (tid == 0) {
+        args.a.smax[row] = m == -INFINITY ? m : m * sc.scale;
+        args.a.ssum[row] = l;
+      }
     }
   }
   for (int task = warp * gridDim.x + blockIdx.x; task < few_before[np]; task += kW * gridDim.x) {
