@@ -21,7 +21,7 @@
 // long cache spread over all SMs, and the result does not depend on timing.
 //
 // Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1357
-// us (1695 TFLOP/s; the tensor pipe is busy 71 % of the cycles, the rest is
+// us (1695 TFLOP/s; the tensor pipe is busy 74 % of the cycles, the rest is
 // switches between the two products and late slots); 64 sequences
 // x 128 heads, one token each, 262,000 keys, 98 us: there bound by the bytes
 // into shared memory, which keys and values pass separately.
