@@ -70,9 +70,9 @@ struct Ctl {
   int abort;
   Seg seg[kSegs];
   int y[kTiles][4];                         // cache row of each box of a tile
-  int loads[kMaxSlots], rloads[2];                 // uses of a slot that have been issued
-  alignas(16) float rbuf[64];
-  float fbuf[64];                 // a row's reference (times log2) and its factor for O
+  int loads[kMaxSlots], rloads[2];          // uses of a slot that have been issued
+  alignas(16) float rbuf[64];               // a row's reference, times log2
+  float fbuf[64];                           // ... and its factor for O
 };
 template <int R>
 constexpr uint32_t kSmem = Few<R>::kOffCtl + sizeof(Ctl) + 1024;
