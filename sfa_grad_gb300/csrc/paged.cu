@@ -298,16 +298,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (g.kt1 == 0) break;
       const int* table = p.table + (size_t)b * p.max_pages;
-      auto fetch = [&](int t) {
-        const int key = t * kKeys + lane * args.vbox;
-        return lane < boxes && key < g.kend ? __ldg(table + key / p.page_size) : -2;
-      };
+      // (an entry may hold any value, so none marks a box that is not needed)
+      auto needed = [&](int t) { return lane < boxes && t * kKeys + lane * args.vbox < g.kend; };
+      auto fetch = [&](int t) { return needed(t) ? __ldg(table + (t * kKeys + lane * args.vbox) / p.page_size) : -1; };
       int page = fetch(g.kt0);
       for (int t = g.kt0; t < g.kt1; ++t, ++tile) {
         int y = none;
         if (page >= 0 && page < p.num_pages)
           y = page * p.page_size + (t * kKeys + lane * args.vbox) % p.page_size;
-        else if (page != -2)
+        else if (needed(t))
           *status = kErrPage;
         if (t + 1 < g.kt1) page = fetch(t + 1);   // in flight during the waits
         const int i = tile % kTiles;
