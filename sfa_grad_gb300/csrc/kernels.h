@@ -165,6 +165,7 @@ struct PagedArgs {
   void* out;
   float *smax, *ssum;
   float scale;
+  int brief;             // the wait limit is short against a suspension
   unsigned long long wait_ns;
   uint8_t* ws;
 };

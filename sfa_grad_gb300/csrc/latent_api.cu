@@ -250,6 +250,7 @@ sfa_status sfa_paged_fwd(const sfa_paged_params* p, const void* q, const void* q
   a.ssum = softmax_sum;
   a.scale = (float)p->scale;
   a.wait_ns = p->wait_limit_us > 0 ? (unsigned long long)p->wait_limit_us * 1000ull : kWaitNsDefault;
+  a.brief = a.wait_ns < 40000;   // four suspensions of at most 10 us
   a.ws = static_cast<uint8_t*>(workspace);
   int nsm = device_sm_count();
   if (nsm > kMaxSms) nsm = kMaxSms;

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c->tmem;
-  const Limit w{&c->abort, status, (long long)(args.a.wait_ns * 21 / 10)};   // SM clock at most 2.1 GHz
+  const Limit w = wait_limit(&c->abort, status, args.a);
   const int ntiles = c->share.ntiles;
   const bool work = ntiles > 0;
   const uint32_t ring = smem_u32(sm + kOffRing), rope = smem_u32(sm + kOffRope);

@@ -53,17 +53,26 @@ struct Share {
 };
 
 // Bounded waits of these kernels: as common.cuh's, with the limit in SM clocks
-// (a read of the global timer costs more than most waits here last).
+// (a read of the global timer costs more than most waits here last).  The
+// first look at a barrier does not suspend, so that the limit counts from the
+// beginning, and where the limit is short none does: a suspension, 10 us at
+// most, would outlast it (waits of 1 to 4 us did not notice a limit of 1, with
+// a hint of 0.25 us for the suspension neither).  512 tokens x 128 heads over
+// 16384 keys take 1369 us so, and 1361 with a first look that suspends.
 struct Limit {
   volatile int* abort;
   int* gerr;
   long long clocks;
+  int brief;               // no suspensions
 };
+__device__ __forceinline__ Limit wait_limit(int* abort, int* status, const PagedArgs& a) {
+  return {abort, status, (long long)(a.wait_ns * 21 / 10), a.brief};   // SM clock at most 2.1 GHz
+}
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Limit& w) {
   const uint32_t a = smem_u32(bar);
-  if (mbar_test(a, parity)) return true;
+  if (mbar_poll(a, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_test(a, parity)) {
+  while (!(w.brief ? mbar_poll(a, parity) : mbar_test(a, parity))) {
     if (*w.abort) return false;
     if (clock64() - t0 > w.clocks) {
       *w.abort = 1;

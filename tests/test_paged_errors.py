@@ -1,5 +1,7 @@
 """What the attention over a paged cache reports: table entries outside the
 cache, waits that run out, and both in one call."""
+import time
+
 import pytest
 import torch
 
@@ -37,3 +39,43 @@ def test_bad_page_is_reported_and_reads_as_zeros(few, page):
     assert sfa.read_device_error(ws) == 3
     assert all(torch.equal(a, b) for a, b in zip(got, zeros))
     assert torch.equal(got[0][1:], want[1:])
+
+
+# ------------------------------------------------------------------ waits that run out
+# A limit of a microsecond on cold caches.  The first key tile's scores need
+# the table's entry, the rows' way into shared memory and 32 MMAs at least,
+# each after the other: several microseconds, which some warp waits for.  So
+# the limit runs out in every call, and the next call on the workspace is right.
+WAITS = {
+    # qlens, kvlens, heads, few
+    "whole_tiles": ([60, 3], [2000, 700], 128, False),
+    "pieces": ([1], [30000], 128, False),
+    "one_tile": ([9] * 5, [9] * 5, 64, False),
+    "few_pieces": ([1], [30000], 16, True),
+    "few_whole": ([1] * 200, [1 + (i * 37) % 300 for i in range(200)], 16, True),
+    "few_64": ([1], [30000], 64, True),
+}
+
+
+@pytest.mark.parametrize("name", list(WAITS))
+def test_short_limit_runs_out(name):
+    qlens, kvlens, heads, few = WAITS[name]
+    x = paged_inputs(qlens, kvlens, heads, "bf16")
+    if few:
+        x = _wide(x)
+    ws, cold = _workspace(), torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    _call(x, workspace=ws)      # the library is loaded
+    codes = []
+    for _ in range(4):
+        cold.fill_(1)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        _call(x, workspace=ws, wait_limit_us=1)
+        torch.cuda.synchronize()
+        # the wind-down waits only for work already issued: far below its own 2 s limit
+        assert time.perf_counter() - t0 < 1.0
+        codes.append(sfa.read_device_error(ws))
+    assert codes == [1] * 4
+    got = _call(x, workspace=ws, **_buffers(x))
+    assert sfa.read_device_error(ws) == 0
+    _check(x, got, qlens, kvlens)
