@@ -307,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (page >= 0 && page < p.num_pages)
           y = page * p.page_size + (t * kKeys + lane * args.vbox) % p.page_size;
         else if (needed(t))
-          *status = kErrPage;
+          atomicCAS(status, 0, kErrPage);   // a timeout stays
         if (t + 1 < g.kt1) page = fetch(t + 1);   // in flight during the waits
         const int i = tile % kTiles;
         if (tile >= kTiles && !(ok = warp_wait(&c->tile_empty[i], (tile / kTiles - 1) & 1, w))) break;

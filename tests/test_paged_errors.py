@@ -79,3 +79,24 @@ def test_short_limit_runs_out(name):
     got = _call(x, workspace=ws, **_buffers(x))
     assert sfa.read_device_error(ws) == 0
     _check(x, got, qlens, kvlens)
+
+
+# ------------------------------------------------------------------ both
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("kvlen", [40, 180_000])
+def test_timeout_is_not_lost_to_a_bad_page(few, kvlen):
+    """A call that gave up says so, whatever pages it meets before and after:
+    its outputs are not complete.  One worker's single key tile, and many for
+    every worker, all of whose pages are bad."""
+    x = paged_inputs([1], [40], 16 if few else 128, "bf16", page=16)
+    x["block_table"] = torch.full((1, 200_000 // 16), -1, dtype=torch.int32, device="cuda")
+    x["act_seq_kv"].fill_(kvlen)
+    ws, cold = _workspace(), torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    _call(x, workspace=ws)
+    assert sfa.read_device_error(ws) == 3
+    codes = []
+    for _ in range(20):
+        cold.fill_(1)
+        _call(x, workspace=ws, wait_limit_us=1)
+        codes.append(sfa.read_device_error(ws))
+    assert codes == [1] * 20
