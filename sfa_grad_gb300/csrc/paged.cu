@@ -529,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t prow = smem_u32(sm + kOffP) + (2 * h + cg) * kPanel + r * 128;
     const uint32_t pready = map_to(smem_u32(&c->pready), lead), ofree = map_to(smem_u32(&c->ofree), lead);
     const uint32_t sfree0 = map_to(smem_u32(&c->sfree[0]), lead);
-    const Scale sc = score_scale<T>(args.a.scale);
+    const Scale sc = score_scale(args.a.scale);
     int tile = 0, nx = 0;
     // one value of each of the row's four threads
     auto exchange = [&](float v, float* o) {

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t pkey = smem_u32(sm + kOffP) + key * 128 + (lane & 3) * 4;   // P's row of key; key + 8: 1024 on
     float* scratch = reinterpret_cast<float*>(sm + kOffP);   // P's place, when no product reads it
-    const Scale sc = score_scale<T>(args.a.scale);
+    const Scale sc = score_scale(args.a.scale);
     int tile = 0, nx = 0, nf = 0;
     // all softmax warps: has any of them a flag
     auto exchange = [&](bool flag, bool* any) {

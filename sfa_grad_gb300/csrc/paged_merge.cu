@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Args a
     if (lane == 0) before[0] = 0;
   }
   __syncthreads();
-  const Scale sc = score_scale<T>(args.a.scale);
+  const Scale sc = score_scale(args.a.scale);
   auto owner = [&](const int* before, int task) {   // before[lo] <= task < before[lo + 1]
     int lo = 0, hi = np;
     while (hi - lo > 1) {

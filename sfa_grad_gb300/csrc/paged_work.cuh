@@ -15,14 +15,13 @@ struct Scale {
   bool negative;
   float scale, log2;   // |scale|, times log2(e)
 };
-// The tensor core adds each step of 16 products to a score in fp32 rounding
-// towards zero: about 0.36 x 2^-23 of the partial sum a step, 36 steps with
-// partial sums half the score on the mean.  Measured, scores are short by
-// 9 (bf16) and 12 (fp16) x 2^-24 of themselves; the scale makes that up.
-template <typename T>
+// (The tensor core adds each step of 16 products to a score in fp32, rounding
+// towards zero.  Scores that fp32 holds exactly lose nothing by that; measured,
+// others come out short by 1 to 16 (bf16) and 4 to 54 (fp16) x 2^-24 of
+// themselves, normal rows by 9 and 11, rows of one sign by the most.  No factor
+// makes that up: it would have to know the rows.)
 __device__ __forceinline__ Scale score_scale(float scale) {
-  constexpr float unbias = 1.0f + (Elt<T>::is_f16 ? 12 : 9) * 5.9604645e-8f;
-  const float s = fabsf(scale) * unbias;
+  const float s = fabsf(scale);
   return {scale < 0.f, s, fmaxf(s * kLog2e, 1e-30f)};
 }
 
