@@ -181,10 +181,11 @@ def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None,
 def norm_rope_grad(positions, cos_sin, *, k=None, k_weight=None, k_rstd=None, dk=None, dk_rope=None, q=None,
                    q_weight=None, q_rstd=None, dq=None, dq_rope=None, interleaved=True, workspace=None, stream=None):
     """sfa_norm_rope_grad: gradients of norm_rope's inputs from those of its
-    outputs (dq, dq_rope, dk, dk_rope, for instance sfa_grad's).  k, k_weight
-    and k_rstd (q, ...) are norm_rope's inputs and its saved rstd.  Returns
-    (dq, dq_rope, dk, dk_rope, dq_weight, dk_weight); the weights' gradients
-    are fp32, summed in a fixed order."""
+    outputs (dq, dq_rope, dk, dk_rope, for instance sfa_grad's; where the row
+    is key and value, dk is the sum of its dK and dV).  k, k_weight and k_rstd
+    (q, ...) are norm_rope's inputs and its saved rstd.  Returns (dq, dq_rope,
+    dk, dk_rope, dq_weight, dk_weight); the weights' gradients are fp32, summed
+    in a fixed order."""
     p, lead, heads, dt, dev, pos, cs, (dqa, dqra, dka, dkra) = _rows(dq, dq_rope, dk, dk_rope, positions, cos_sin, 0.0,
                                                                      interleaved)
     saved = {}
