@@ -327,7 +327,7 @@ typedef struct sfa_rows_params {
   int32_t interleaved;  /* 0 or 1: which elements form a rotated pair */
   int64_t T1, N1;       /* tokens; query heads, 1..128 */
   int64_t table_len;    /* rows of cos_sin */
-  double eps;           /* finite, >= 0 */
+  double eps;           /* finite in fp32, >= 0 */
 } sfa_rows_params;
 
 /*
@@ -389,7 +389,7 @@ typedef struct sfa_paged_params {
   int64_t B, S1, T1;                      /* S1: BSND; T1: TND */
   int64_t N1, D, Dr;                      /* 1..128; 512; 64 or 0 */
   int64_t num_pages, page_size, max_pages; /* page_size: a multiple of 16, 16..1024 */
-  double scale;
+  double scale;                           /* finite in fp32, also times log2(e) */
   int64_t sparse_mode;                    /* 0 (all kvlen keys) or 3 (keys up to the token's position) */
   int32_t interleaved;                    /* sfa_cache_append */
   int32_t wait_limit_us;                  /* sfa_paged_fwd; as in sfa_params */

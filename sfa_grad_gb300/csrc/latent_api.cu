@@ -18,6 +18,9 @@ sfa_status fail(cudaError_t e, const char* what) {
   return SFA_ERR_RUNTIME;
 }
 
+// The kernels hold the scale, its product with log2(e) and eps in fp32.
+bool fits(double x) { return std::isfinite(static_cast<float>(x)); }
+
 bool aligned(const void* p, size_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 template <typename... Ts>
 bool all_aligned(Ts... ps) {
@@ -36,7 +39,7 @@ sfa_status check_rows(const sfa_rows_params* p) {
   if (p->N1 < 1 || p->N1 > 128 || p->T1 < 0 || p->T1 > INT32_MAX / 2 || p->T1 * p->N1 > INT32_MAX / 2)
     return SFA_ERR_SHAPE;
   if (p->table_len < 0 || p->table_len > INT32_MAX) return SFA_ERR_SHAPE;
-  if (!std::isfinite(p->eps) || p->eps < 0) return SFA_ERR_SHAPE;
+  if (!fits(p->eps) || p->eps < 0) return SFA_ERR_SHAPE;
   return SFA_OK;
 }
 
@@ -65,7 +68,7 @@ sfa_status check_paged(const sfa_paged_params* p, Paged* out) {
   if (p->num_pages < 1 || p->num_pages > INT32_MAX / 2 / p->page_size) return SFA_ERR_SHAPE;
   if (p->max_pages < 1 || p->max_pages > INT32_MAX / 2 / p->page_size) return SFA_ERR_SHAPE;
   if (p->sparse_mode != 0 && p->sparse_mode != 3) return SFA_ERR_SHAPE;
-  if (!std::isfinite(p->scale)) return SFA_ERR_SHAPE;
+  if (!fits(p->scale * 1.4426950408889634)) return SFA_ERR_SHAPE;
   const bool tnd = p->layout == SFA_LAYOUT_TND;
   const int64_t n = tnd ? p->T1 : p->S1;
   if (n < 0 || n > INT32_MAX / 2) return SFA_ERR_SHAPE;
@@ -185,7 +188,7 @@ sfa_status sfa_cache_append(const sfa_paged_params* p, void* cache, const int32_
   if (!cache || !block_table || !act_seq_kv || !k || (a.pg.tnd && !act_seq_q)) return SFA_ERR_NULLPTR;
   if (rope && (!k_rope || !cos_sin || (q_rope && !q_rope_out))) return SFA_ERR_NULLPTR;
   if (rope && (table_len < 1 || table_len > INT32_MAX)) return SFA_ERR_SHAPE;
-  if (!std::isfinite(eps) || eps < 0) return SFA_ERR_SHAPE;
+  if (!fits(eps) || eps < 0) return SFA_ERR_SHAPE;
   if (!all_aligned(cache, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out) ||
       !words_aligned(block_table, act_seq_q, act_seq_kv, error))
     return SFA_ERR_PARAM_INVALID;
