@@ -22,7 +22,7 @@ struct Scale {
 // makes that up: it would have to know the rows.)
 __device__ __forceinline__ Scale score_scale(float scale) {
   const float s = fabsf(scale);
-  return {scale < 0.f, s, fmaxf(s * kLog2e, 1e-30f)};
+  return {scale < 0.f, s, fmaxf(s * kLog2e, 1.4e-45f)};   // at least fp32's smallest value
 }
 
 // One piece of work: key tiles kt0 .. kt1 - 1 of a row tile.

@@ -7,7 +7,7 @@ import torch
 import sfa_grad_gb300 as sfa
 from latent_util import paged_inputs
 from sfa_grad_gb300.latent import PagedParams, RowsParams, _lib
-from test_paged import _buffers, _call
+from test_paged import _buffers, _call, _check
 from test_paged_few import _wide
 
 
@@ -31,3 +31,16 @@ def test_values_beyond_fp32_are_refused():
     p = PagedParams(1, 0, 2, 0, 3, 4, 512, 64, 8, 64, 2, 1.0, 3, 1, 0)
     args = [f, f, f, f, f, f, f, 1e300, f, 9, None, None, None, None]
     assert _lib().sfa_cache_append(ctypes.byref(p), *args) == sfa.SFA_ERR_SHAPE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("few,heads", [(False, 128), (True, 16)])
+@pytest.mark.parametrize("size,scale", [(1e15, 0.0), (1e15, -0.0), (1e16, 1e-32 / 24), (1e17, -1e-34 / 24), (1e-16, 1e32 / 24)])
+def test_rows_far_from_one(few, heads, size, scale):
+    """Elements far from one with the scale that fits them, and with none: a
+    scale of zero weighs every key alike, whatever its score."""
+    qlens, kvlens = [1, 2], [300, 65]
+    x = paged_inputs(qlens, kvlens, heads, "bf16", q_scale=size, k_scale=size)
+    if few:
+        x = _wide(x)
+    _check(x, _call(x, scale, **_buffers(x)), qlens, kvlens, scale)
