@@ -20,9 +20,10 @@
 // (m, l, O) in fp32 and a second kernel merges them in order: few rows over a
 // long cache spread over all SMs, and the result does not depend on timing.
 //
-// Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1357
-// us (1695 TFLOP/s; the tensor pipe is busy 74 % of the cycles, the rest is
-// switches between the two products and late slots); 64 sequences
+// Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1380 us
+// (1667 TFLOP/s; back to back the power limit makes it 1500 to 1525; the tensor
+// pipe is busy 74 % of the cycles, the rest is switches between the two
+// products and late slots); 64 sequences
 // x 128 heads, one token each, 262,000 keys, 98 us: there bound by the bytes
 // into shared memory, which keys and values pass separately.
 //
@@ -250,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool work = ntiles > 0;
   // the ring holds, slot after slot, K(0) K(1) V(0) K(2) V(1) ... K(N-1) V(N-2) V(N-1),
   // over the ends of pieces too: V(t) before K(t+1) there cost every tile more in
-  // code than it gained (512 tokens x 128 heads over 16384 keys 1425 us, so 1385)
+  // code than it gained (512 tokens x 128 heads over 16384 keys took 3 % longer)
   const uint32_t ring = smem_u32(sm + kOffRing), lead = 0;
 
   if (c->share.bad && tid == 0) *status = kErrSeqLens;
@@ -745,8 +746,8 @@ const size_t kOffPart = kOffStats + up256(kMaxSms * kRows * sizeof(float4));
 
 size_t paged_workspace(const Paged&) { return kOffPart + (size_t)kMaxSms * kRows * 512 * sizeof(float); }
 
-// Few query rows a sequence go to paged_few.cu: their time is the cache's
-// bytes, which this file's kernel takes twice (keys, then values).  128
+// Few query rows a sequence, on the mean, go to paged_few.cu: their time is the
+// cache's bytes, which this file's kernel takes twice (keys, then values).  128
 // sequences of 2048 .. 8192 keys took 199 us here and 142 there with 32 rows,
 // 200 and 162 with 64; with 128 rows 207 and, cut in two, 296.  Not where the
 // tables cannot hold a tile of 64 keys an SM, or ten with more than 32 rows,

@@ -20,7 +20,7 @@
 // its own: one warp that looked at both products' barriers in turn spent 650
 // clk a slot where its eight MMAs take 200, and the loads waited for it.
 //
-// Measured: 128 sequences x 16 heads of 2048 .. 16384 keys 228 us, 6.2 TB/s of
+// Measured: 128 sequences x 16 heads of 2048 .. 16384 keys 233 us, 6.1 TB/s of
 // the cache's bytes (302 with the rows on M); 128 x 64 heads of 2048 .. 8192
 // keys 158 us, 4.8 TB/s: with eight slots the loads wait
 // for the products, a tile takes 3900 clk.
