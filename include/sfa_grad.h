@@ -356,8 +356,9 @@ sfa_status sfa_norm_rope(const sfa_rows_params* p, const int32_t* positions, con
  * the same bits).  q, q_weight, q_rstd (k, ...) are the forward's and needed
  * with d_q (d_k).  Where the normed key row is the value too (paged_fwd, or
  * sfa_grad with k == v), d_k is the sum of sfa_grad's dK and dV.  Padding tokens
- * get zero rows and add nothing to the weights' gradients.  `workspace`: at least the size below, 256-byte aligned,
- * scratch; two calls that may overlap need one each.
+ * get zero rows and add nothing to the weights' gradients.  `workspace`: at
+ * least the size below, 256-byte aligned, scratch; two calls that may overlap
+ * need one each.
  */
 sfa_status sfa_norm_rope_grad_workspace_size(const sfa_rows_params* p, size_t* bytes);
 sfa_status sfa_norm_rope_grad(const sfa_rows_params* p, const int32_t* positions, const float* cos_sin, const void* q,

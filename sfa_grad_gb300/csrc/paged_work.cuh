@@ -16,8 +16,8 @@ struct Scale {
   float scale, log2;   // |scale|, times log2(e)
 };
 // (The tensor core adds each step of 16 products to a score in fp32, rounding
-// towards zero.  Scores that fp32 holds exactly lose nothing by that; measured,
-// others come out short by 1 to 16 (bf16) and 4 to 54 (fp16) x 2^-24 of
+// towards zero.  Scores whose partial sums fp32 holds exactly lose nothing by
+// that; measured, others come out short by 1 to 16 (bf16) and 4 to 54 (fp16) x 2^-24 of
 // themselves, normal rows by 9 and 11, rows of one sign by the most.  No factor
 // makes that up: it would have to know the rows.)
 __device__ __forceinline__ Scale score_scale(float scale) {
