@@ -73,7 +73,8 @@ typedef enum { SFA_LAYOUT_BSND = 0, SFA_LAYOUT_TND = 1 } sfa_layout;
 #define SFA_DEVERR_SEQLENS 2  /* TND lengths negative or not summing to T1/T2: every key was masked; the
                                  paged calls: lengths that do not fit the tokens or the block table */
 #define SFA_DEVERR_PAGE 3     /* the paged calls: a block table entry outside the cache */
-#define SFA_DEVERR_POSITION 4 /* sfa_cache_append: a token's position outside the rotation table */
+#define SFA_DEVERR_POSITION 4 /* the appends: a token's position outside the rotation table */
+#define SFA_DEVERR_POOL 5     /* sfa_page_plan: a step needs more pages than are free, or the free pages do not fit the cache */
 
 /*
  * Problem description (replaces the page's aclTensor shape metadata and the
@@ -369,6 +370,29 @@ sfa_status sfa_norm_rope_grad(const sfa_rows_params* p, const int32_t* positions
                               void* stream);
 
 /*
+ * Rotation by positions of several axes (time, height, width of an image or
+ * video): positions int32 (n_axes, T1), n_axes 1..4, and axes[i] < n_axes (32
+ * bytes of host memory, read during the call) names the axis whose position
+ * turns pair i: c = cos_sin[positions[axes[i]][t]][i], s likewise.  A token
+ * with a position outside the table on any axis is padding.  Otherwise as
+ * sfa_norm_rope and sfa_norm_rope_grad (positions and cos_sin are needed where
+ * n_axes > 1); the workspace is the latter's.
+ * Further errors: SFA_ERR_NULLPTR (axes), SFA_ERR_PARAM_INVALID (n_axes, an
+ * axis out of range).
+ */
+sfa_status sfa_norm_rope_axes(const sfa_rows_params* p, int32_t n_axes, const uint8_t* axes, const int32_t* positions,
+                              const float* cos_sin, const void* q, const void* q_weight, const void* q_rope,
+                              const void* k, const void* k_weight, const void* k_rope, void* q_out, void* q_rope_out,
+                              void* k_out, void* k_rope_out, float* q_rstd, float* k_rstd, void* stream);
+sfa_status sfa_norm_rope_axes_grad(const sfa_rows_params* p, int32_t n_axes, const uint8_t* axes,
+                                   const int32_t* positions, const float* cos_sin, const void* q,
+                                   const void* q_weight, const float* q_rstd, const void* k, const void* k_weight,
+                                   const float* k_rstd, const void* d_q, const void* d_q_rope, const void* d_k,
+                                   const void* d_k_rope, void* dq, void* dq_rope, void* dk, void* dk_rope,
+                                   float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
  * A paged cache of latent rows: num_pages pages of page_size tokens of 512 +
  * Dr elements (the latent part, then the rotated part), contiguous.  Token j
  * of sequence b is row j % page_size of page block_table[b][j / page_size];
@@ -435,6 +459,113 @@ sfa_status sfa_paged_fwd(const sfa_paged_params* p, const void* q, const void* q
                          const int32_t* block_table, const int32_t* act_seq_q, const int32_t* act_seq_kv, void* out,
                          float* softmax_max, float* softmax_sum, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/* ------------------------------------------------------------------ rows of 4 bits
+ *
+ * The same cache with its latent part in 4 bits: a row is 288 + 2 Dr bytes,
+ *   256 bytes of codes: element 2j in the low half of byte j, 2j + 1 in the
+ *       high half; a sign bit, then 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *   32 scales, one for 16 elements, in 8 bits (e4m3: 4 exponent bits, 3 of
+ *       fraction);
+ *   the rotated part in dtype.
+ * An element is code * scale * cache_scale, where cache_scale is a power of
+ * two from 2^-14 to 2^4, the same for every call on a cache; such products are
+ * exact in both types, and that is what the attention reads.  cache_scale puts
+ * the rows into the scales' range: a block's largest value should lie between
+ * 0.1 and 2688 of it (below, scales lose bits and then whole blocks; above,
+ * values are cut off).  Pages and 16-byte alignment as for the rows of 16 bits.
+ */
+
+/*
+ * sfa_cache_append to such a cache.  y = k * rstd * k_weight (or k) goes into
+ * it without a rounding to dtype before: a block's scale is max |y| / (6
+ * cache_scale) and a code y / (scale * cache_scale), each rounded to the
+ * nearest, ties to even, as exact arithmetic on k does it (a row close to a
+ * border is rounded again from 64-bit values).  A block with a value that is
+ * not finite reads back as not a number.
+ * Further errors: SFA_ERR_SHAPE (cache_scale).
+ */
+sfa_status sfa_cache4_append(const sfa_paged_params* p, double cache_scale, void* cache, const int32_t* block_table,
+                             const int32_t* act_seq_q, const int32_t* act_seq_kv, const void* k, const void* k_rope,
+                             const void* k_weight, double eps, const float* cos_sin, int64_t table_len,
+                             const void* q_rope, void* q_rope_out, int32_t* error, void* stream);
+
+/*
+ * sfa_paged_fwd over such a cache, by the values that its rows stand for.
+ */
+sfa_status sfa_paged4_workspace_size(const sfa_paged_params* p, size_t* bytes);
+sfa_status sfa_paged4_fwd(const sfa_paged_params* p, double cache_scale, const void* q, const void* q_rope,
+                          const void* cache, const int32_t* block_table, const int32_t* act_seq_q,
+                          const int32_t* act_seq_kv, void* out, float* softmax_max, float* softmax_sum,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct sfa_cache_params {
+  int32_t dtype;                  /* of the rows, or of a 4-bit row's rotated part */
+  int32_t bits;                   /* of the latent part: 16 or 4 */
+  int64_t num_pages, page_size, Dr; /* as in sfa_paged_params */
+  double scale;                   /* cache_scale; bits = 4 only */
+} sfa_cache_params;
+
+/*
+ * Values of a whole 4-bit cache: out (num_pages, page_size, 512 + Dr) in
+ * dtype.
+ */
+sfa_status sfa_cache4_unpack(const sfa_cache_params* c, const void* cache, void* out, void* stream);
+
+/*
+ * Append by a slot map, to a cache of either kind: token t's row goes to row
+ * slots[t] of the cache (page * page_size + place in the page), and its
+ * positions (n_axes, T1) turn k_rope and q_rope as in sfa_norm_rope_axes (axes
+ * null: every pair by the first axis).  p gives dtype, T1, N1, table_len, eps
+ * and interleaved.  A token with a negative slot is padding and left out, as
+ * is, with a code in `error` (optional), one whose slot lies behind the cache
+ * (SFA_DEVERR_PAGE) or with a position outside the table
+ * (SFA_DEVERR_POSITION).  The slots of a call differ: of tokens with the same
+ * one the row may get parts of each.
+ */
+sfa_status sfa_cache_append_slots(const sfa_cache_params* c, const sfa_rows_params* p, void* cache,
+                                  const int32_t* slots, int32_t n_axes, const uint8_t* axes, const int32_t* positions,
+                                  const void* k, const void* k_rope, const void* k_weight, const float* cos_sin,
+                                  const void* q_rope, void* q_rope_out, int32_t* error, void* stream);
+
+typedef struct sfa_plan_params {
+  int64_t B, max_pages;           /* requests, 1..8192, and entries of a row of the block table */
+  int64_t num_pages, page_size;   /* of the cache, as in sfa_paged_params */
+  int64_t tokens;                 /* room in slots and positions */
+} sfa_plan_params;
+
+/*
+ * Block tables and slot maps of a step, built on the device from the requests'
+ * lengths.  act_seq_kv int32 (B,): tokens in the cache; new_tokens int32 (B,):
+ * new ones, 0 for a request that waits, negative for one that has ended.
+ * free_pages int32 (num_pages,) holds the free pages in its first
+ * *free_count entries.  In this order: the pages of ended requests are put
+ * behind the free ones, request after request; then the requests take the
+ * pages that their new tokens need, in order, each from the end.  block_table
+ * (B, max_pages) and free_pages are changed in place, as far as that needs (an
+ * ended request's row keeps its entries, which mean nothing any more).
+ *   act_seq_q_out (B,): new tokens, 0 for an ended request;
+ *   act_seq_kv_out (B,): tokens with the new ones, 0 for an ended request;
+ *   free_count_out (1,);
+ *   slots, positions (tokens,): of the new tokens, request after request; -1
+ *       behind the last.
+ * Both act_seq arrays, with the table, are what sfa_cache_append and
+ * sfa_paged_fwd (TND) take; slots what sfa_cache_append_slots takes.  The
+ * outputs overlap no input.
+ * A step that does not fit changes nothing and gives act_seq_q_out 0,
+ * act_seq_kv_out and free_count_out as they were and slots -1: lengths that
+ * are negative or exceed the table, or new tokens that exceed `tokens`
+ * (SFA_DEVERR_SEQLENS); more pages needed than there are, or more free and
+ * returned ones than num_pages (SFA_DEVERR_POOL).  A page outside the cache
+ * is handed on like any other; a token in it gets slot -1 (SFA_DEVERR_PAGE).
+ * `error` (optional, device int32) receives the code and is not written
+ * otherwise.  Asynchronous on `stream`; no workspace; the same call gives the
+ * same result.
+ */
+sfa_status sfa_page_plan(const sfa_plan_params* p, int32_t* block_table, const int32_t* act_seq_kv,
+                         const int32_t* new_tokens, int32_t* free_pages, const int32_t* free_count,
+                         int32_t* act_seq_q_out, int32_t* act_seq_kv_out, int32_t* free_count_out, int32_t* slots,
+                         int32_t* positions, int32_t* error, void* stream);
 
 /*
  * Human-readable detail of the most recent SFA_ERR_RUNTIME returned on the

@@ -413,5 +413,6 @@ def read_device_error(workspace: torch.Tensor, stream=None) -> int:
     return code.value
 
 
-from .latent import (cache_append, make_paged_params, norm_rope, norm_rope_grad,  # noqa: E402
-                     norm_rope_grad_workspace_size, paged_fwd, paged_workspace_size)
+from .latent import (cache_append, cache_append_slots, cache_unpack, make_paged_params, norm_rope,  # noqa: E402
+                     norm_rope_grad, norm_rope_grad_workspace_size, page_plan, paged4_workspace_size, paged_fwd,
+                     paged_workspace_size)

@@ -123,9 +123,11 @@ constexpr int kMaxSms = 160;
 // qro, kro.  Gradient: dq, dk with q, k -> qo, ko and the weights' gradients;
 // qr, kr are then the rotated rows' gradients.
 struct RowsArgs {
-  const int* pos;        // (T) or null
+  const int* pos;        // (axes, T) or null
   const float* cs;       // (table_len, 64)
   long long table_len;
+  int axes;                      // 1..4
+  unsigned long long axis_map;   // two bits a pair: the axis whose position turns it
   const void *q, *qw, *qr, *k, *kw, *kr;
   void *qo, *qro, *ko, *kro;
   float *q_rstd, *k_rstd;
@@ -142,21 +144,57 @@ cudaError_t launch_norm_rope_grad(RowsArgs a, int nsm, cudaStream_t st);
 // Blocks (partial sums of dw) of the gradient over `rows` rows of 512.
 int norm_grad_blocks(long long rows, int nsm);
 
-// Append to the paged cache (append.cu).
+// Append to the paged cache (append.cu).  Where the rows go follows from the
+// lengths and the block table, or (slots not null) stands in a map, with the
+// positions beside it; of pg that case uses T, G, row and the cache's sizes.
 struct AppendArgs {
   Paged pg;
+  const int* slots;      // (T) or null
+  const int* pos;        // (axes, T), with slots
+  int axes;
+  unsigned long long axis_map;
+  int packed, scale_exp; // rows of 4 bits, in units of 2^scale_exp
   void* cache;
   const void *k, *kr, *kw, *qr;
   void* qro;
   const float* cs;       // null without rope
   long long table_len;
   int* error;            // or null
-  float eps;
+  double eps;
   int interleaved;
   int blocks_k;          // set by the launcher
 };
 template <typename T>
 cudaError_t launch_append(AppendArgs a, cudaStream_t st);
+
+// Values of a 4-bit cache (cache4.cu): all of it, rows in order, or (b not 0)
+// the pages that the block tables of pg name, with tables of their own.
+struct UnpackArgs {
+  const void* cache;
+  void* out;
+  long long rows;        // all of it: num_pages * page_size
+  int width, scale_exp;  // elements of a row: 512 or 576
+  Paged pg;              // the tables' form
+  int* table;            // tables of `out`
+  int by_page;           // out's pages are the cache's
+};
+template <typename T>
+cudaError_t launch_unpack(const UnpackArgs& a, int nsm, cudaStream_t st);
+template <typename T>
+cudaError_t launch_unpack_tables(const UnpackArgs& a, int nsm, cudaStream_t st);
+
+// Block tables and slot maps of a step (plan.cu).
+struct PlanArgs {
+  int* table;            // (B, max_pages)
+  const int *kv, *fresh; // (B): tokens in the cache; new ones, negative where the request has ended
+  int* free;             // (num_pages): the free pages, the first *count
+  const int* count;
+  int *q_out, *kv_out, *count_out, *slots, *pos;
+  int* error;            // or null
+  int B, max_pages, num_pages, page_size, tokens;
+};
+constexpr int kPlanRequests = 8192;   // most of a call: their sums lie in shared memory
+cudaError_t launch_plan(const PlanArgs& a, int nsm, cudaStream_t st);
 
 // Attention over the paged cache (paged.cu).
 struct PagedArgs {
@@ -165,11 +203,13 @@ struct PagedArgs {
   void* out;
   float *smax, *ssum;
   float scale;
+  int packed, scale_exp; // rows of 4 bits, in units of 2^scale_exp
   int brief;             // the wait limit is short against a suspension
   unsigned long long wait_ns;
   uint8_t* ws;
 };
 size_t paged_workspace(const Paged& p);
+size_t paged4_workspace(const Paged& p);   // rows of 4 bits
 template <typename T>
 cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st);
 

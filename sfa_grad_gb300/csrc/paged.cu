@@ -761,8 +761,39 @@ static int few_rows(const Paged& p, int nsm) {
   return rows <= 64 && keys >= 640LL * nsm ? 64 : 0;
 }
 
+// Where a packed cache's values go: tables, then pages.  Pages shared by
+// sequences are unpacked once where the cache has fewer than the tables name.
+static bool by_page(const Paged& p) { return p.num_pages <= (long long)p.B * p.max_pages; }
+static size_t table_bytes(const Paged& p) { return up256((size_t)p.B * p.max_pages * sizeof(int)); }
+
+size_t paged4_workspace(const Paged& p) {
+  const size_t pages = by_page(p) ? (size_t)p.num_pages : (size_t)p.B * p.max_pages;
+  return paged_workspace(p) + table_bytes(p) + pages * p.page_size * p.row * 2;
+}
+
+template <typename T>
+static cudaError_t launch_unpacked(PagedArgs a, int nsm, cudaStream_t st) {
+  const size_t base = paged_workspace(a.pg);
+  UnpackArgs u{};
+  u.cache = a.cache;
+  u.width = a.pg.row;
+  u.scale_exp = a.scale_exp;
+  u.pg = a.pg;
+  u.by_page = by_page(a.pg);
+  u.table = reinterpret_cast<int*>(a.ws + base);
+  u.out = a.ws + base + table_bytes(a.pg);
+  const cudaError_t e = launch_unpack_tables<T>(u, nsm, st);
+  if (e != cudaSuccess) return e;
+  a.packed = 0;
+  a.cache = u.out;
+  a.pg.table = u.table;
+  if (!u.by_page) a.pg.num_pages = a.pg.B * a.pg.max_pages;
+  return launch_paged<T>(a, nsm, st);
+}
+
 template <typename T>
 cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
+  if (a.packed) return launch_unpacked<T>(a, nsm, st);
   const Paged& p = a.pg;
   Args g;
   g.a = a;

@@ -8,6 +8,7 @@ namespace sfa {
 // Device error codes of the paged calls, beside common.cuh's.
 constexpr int kErrPage = 3;          // a block table entry outside the cache
 constexpr int kErrPosition = 4;      // append: a position outside the rotation table
+constexpr int kErrPool = 5;          // plan: fewer free pages than the step needs, or more than there are
 
 struct Paged {
   const int* table;    // (B, max_pages)

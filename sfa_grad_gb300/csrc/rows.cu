@@ -30,6 +30,7 @@ constexpr int kPieces = 8;
 
 __device__ __forceinline__ bool padded(const RowsArgs& a, int t) {
   if (!a.pos) return false;
+  if (a.axes > 1) return outside(load_places(a.pos, t, a.T, a.axes), a.table_len);
   const int p = __ldg(a.pos + t);
   return p < 0 || p >= a.table_len;
 }
@@ -50,11 +51,20 @@ __device__ void norm_rows(const RowsArgs& a, const T* x, const T* w, T* y, float
 }
 
 // Rows of 64 of one token, heads h0 .. h0 + 31: rotated by the token's angles.
-template <typename T, bool INTER>
+template <typename T, bool INTER, bool AXES>
 __device__ void rotate_rows(const RowsArgs& a, const T* x, T* y, int heads, int t, int h0, float sgn) {
   const int lane = threadIdx.x & 31;
-  const int pos = __ldg(a.pos + t);
-  const bool pad = pos < 0 || pos >= a.table_len;
+  Places at;
+  int pos = 0;
+  bool pad;
+  if constexpr (AXES) {
+    at = load_places(a.pos, t, a.T, a.axes);
+    pad = outside(at, a.table_len);
+    if (pad) at = Places{{0, 0, 0, 0}};
+  } else {
+    pos = __ldg(a.pos + t);
+    pad = pos < 0 || pos >= a.table_len;
+  }
   const size_t base = ((size_t)t * heads + h0) * 8;
   const int n = min(heads - h0, 4 * kPieces) * 8;
   const uint4* src = reinterpret_cast<const uint4*>(x) + base;
@@ -66,7 +76,10 @@ __device__ void rotate_rows(const RowsArgs& a, const T* x, T* y, int heads, int 
     if (lane + 32 * j < n) w[j] = src[lane + 32 * j];
   }
   Angles ang;
-  load_angles<INTER>(a.cs + (size_t)(pad ? 0 : pos) * 64, lane & 7, &ang);
+  if constexpr (AXES)
+    load_angles<INTER>(a.cs, at, a.axis_map, lane & 7, &ang);
+  else
+    load_angles<INTER>(a.cs + (size_t)(pad ? 0 : pos) * 64, lane & 7, &ang);
 #pragma unroll
   for (int j = 0; j < kPieces; ++j) {
     float v[8];
@@ -78,18 +91,18 @@ __device__ void rotate_rows(const RowsArgs& a, const T* x, T* y, int heads, int 
 
 // The rotated rows' warp items: 32 heads of one token each, the queries'
 // first, then one a token for the keys.
-template <typename T, bool INTER>
+template <typename T, bool INTER, bool AXES>
 __device__ void rotate_item(const RowsArgs& a, const T* qr, T* qro, const T* kr, T* kro, long long item, float sgn) {
   const int per = (a.G + 4 * kPieces - 1) / (4 * kPieces);
   const long long nq = qr ? (long long)a.T * per : 0;
   if (item < nq) {
-    rotate_rows<T, INTER>(a, qr, qro, a.G, (int)(item / per), (int)(item % per) * 4 * kPieces, sgn);
+    rotate_rows<T, INTER, AXES>(a, qr, qro, a.G, (int)(item / per), (int)(item % per) * 4 * kPieces, sgn);
   } else if (kr && item - nq < a.T) {
-    rotate_rows<T, INTER>(a, kr, kro, 1, (int)(item - nq), 0, sgn);
+    rotate_rows<T, INTER, AXES>(a, kr, kro, 1, (int)(item - nq), 0, sgn);
   }
 }
 
-template <typename T, bool INTER>
+template <typename T, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(RowsArgs a) {
   const int warp = threadIdx.x >> 5;
   int b = blockIdx.x;
@@ -105,14 +118,14 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(RowsArgs a) {
     return;
   }
   b -= a.blocks_q;
-  rotate_item<T, INTER>(a, (const T*)a.qr, (T*)a.qro, (const T*)a.kr, (T*)a.kro, (long long)b * kWarps + warp, 1.f);
+  rotate_item<T, INTER, AXES>(a, (const T*)a.qr, (T*)a.qro, (const T*)a.kr, (T*)a.kro, (long long)b * kWarps + warp, 1.f);
 }
 
 // Gradient of rows of 512: warps of `nblk` blocks take rows in strides, keep
 // their part of dw in registers and leave one fp32 sum a block in `part`.  A
 // row's 2 KB are on their way while the row before is worked on; packed, so
 // that the registers allow three blocks an SM.
-template <typename T>
+template <typename T, bool AXES>
 __device__ void norm_grad_rows(const RowsArgs& a, const T* x, const T* w, const float* rstd, const T* dy, T* dx,
                                int heads, int blk, int nblk, float* part, float* sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -125,20 +138,29 @@ __device__ void norm_grad_rows(const RowsArgs& a, const T* x, const T* w, const 
   uint4 nx[2], nd[2];
   float nr = 0.f;
   int npos = 0;
+  Places nat{};
   auto fetch = [&](long long row) {
     const uint4* px = reinterpret_cast<const uint4*>(x + row * 512);
     const uint4* pd = reinterpret_cast<const uint4*>(dy + row * 512);
     nx[0] = __ldcs(px + lane); nx[1] = __ldcs(px + lane + 32);
     nd[0] = __ldcs(pd + lane); nd[1] = __ldcs(pd + lane + 32);
     nr = __ldg(rstd + row);
-    if (a.pos) npos = __ldg(a.pos + row / heads);
+    if constexpr (AXES) {
+      nat = load_places(a.pos, (int)(row / heads), a.T, a.axes);
+    } else {
+      if (a.pos) npos = __ldg(a.pos + row / heads);
+    }
   };
   long long row = (long long)blk * kWarps + warp;
   if (row < rows) fetch(row);
   for (; row < rows; row += step) {
     const uint4 rx[2] = {nx[0], nx[1]}, rd[2] = {nd[0], nd[1]};
     const float r = nr;
-    const bool pad = a.pos && (npos < 0 || npos >= a.table_len);
+    bool pad;
+    if constexpr (AXES)
+      pad = outside(nat, a.table_len);
+    else
+      pad = a.pos && (npos < 0 || npos >= a.table_len);
     if (row + step < rows) fetch(row + step);
     uint4* out = reinterpret_cast<uint4*>(dx + row * 512);
     if (pad) {
@@ -184,23 +206,23 @@ __device__ void norm_grad_rows(const RowsArgs& a, const T* x, const T* w, const 
   }
 }
 
-template <typename T, bool INTER>
+template <typename T, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kernel(RowsArgs a) {
   __shared__ float sm[kWarps * 512];
   int b = blockIdx.x;
   if (b < a.blocks_k) {
-    norm_grad_rows<T>(a, (const T*)a.k, (const T*)a.kw, a.k_rstd, (const T*)a.dk, (T*)a.ko, 1, b, a.blocks_k, a.part,
+    norm_grad_rows<T, AXES>(a, (const T*)a.k, (const T*)a.kw, a.k_rstd, (const T*)a.dk, (T*)a.ko, 1, b, a.blocks_k, a.part,
                       sm);
     return;
   }
   b -= a.blocks_k;
   if (b < a.blocks_q) {
-    norm_grad_rows<T>(a, (const T*)a.q, (const T*)a.qw, a.q_rstd, (const T*)a.dq, (T*)a.qo, a.G, b, a.blocks_q,
+    norm_grad_rows<T, AXES>(a, (const T*)a.q, (const T*)a.qw, a.q_rstd, (const T*)a.dq, (T*)a.qo, a.G, b, a.blocks_q,
                       a.part + (size_t)a.blocks_k * 512, sm);
     return;
   }
   b -= a.blocks_q;
-  rotate_item<T, INTER>(a, (const T*)a.qr, (T*)a.qro, (const T*)a.kr, (T*)a.kro,
+  rotate_item<T, INTER, AXES>(a, (const T*)a.qr, (T*)a.qro, (const T*)a.kr, (T*)a.kro,
                         (long long)b * kWarps + (threadIdx.x >> 5), -1.f);
 }
 
@@ -246,10 +268,9 @@ cudaError_t launch_norm_rope(RowsArgs a, cudaStream_t st) {
   a.blocks_q = a.q ? (int)(((long long)a.T * a.G + kWarps - 1) / kWarps) : 0;
   const long long n = a.blocks_k + (long long)a.blocks_q + rope_blocks(a);
   if (n == 0) return cudaSuccess;
-  if (a.interleaved)
-    norm_rope_kernel<T, true><<<(unsigned)n, kWarps * 32, 0, st>>>(a);
-  else
-    norm_rope_kernel<T, false><<<(unsigned)n, kWarps * 32, 0, st>>>(a);
+  auto kern = a.axes > 1 ? (a.interleaved ? norm_rope_kernel<T, true, true> : norm_rope_kernel<T, false, true>)
+                         : (a.interleaved ? norm_rope_kernel<T, true, false> : norm_rope_kernel<T, false, false>);
+  kern<<<(unsigned)n, kWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -259,10 +280,10 @@ cudaError_t launch_norm_rope_grad(RowsArgs a, int nsm, cudaStream_t st) {
   a.blocks_q = a.dq ? norm_grad_blocks((long long)a.T * a.G, nsm) : 0;
   const long long n = a.blocks_k + (long long)a.blocks_q + rope_blocks(a);
   if (n > 0) {
-    if (a.interleaved)
-      norm_rope_grad_kernel<T, true><<<(unsigned)n, kWarps * 32, 0, st>>>(a);
-    else
-      norm_rope_grad_kernel<T, false><<<(unsigned)n, kWarps * 32, 0, st>>>(a);
+    auto kern = a.axes > 1
+                    ? (a.interleaved ? norm_rope_grad_kernel<T, true, true> : norm_rope_grad_kernel<T, false, true>)
+                    : (a.interleaved ? norm_rope_grad_kernel<T, true, false> : norm_rope_grad_kernel<T, false, false>);
+    kern<<<(unsigned)n, kWarps * 32, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

@@ -75,6 +75,39 @@ __device__ __forceinline__ void load_angles(const float* cs_row, int piece, Angl
     a->s[4] = s1.x; a->s[5] = s1.y; a->s[6] = s1.z; a->s[7] = s1.w;
   }
 }
+// Positions of a token on up to four axes; pair i turns by the one that bits
+// 2i, 2i + 1 of `map` name.  Axes that are not there repeat the first.
+struct Places {
+  int p[4];
+};
+__device__ __forceinline__ Places load_places(const int* pos, int t, int tokens, int axes) {
+  Places r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = __ldg(pos + (i < axes ? (size_t)i * tokens : 0) + t);
+  return r;
+}
+__device__ __forceinline__ bool outside(const Places& r, long long table_len) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= r.p[i] < 0 || r.p[i] >= table_len;
+  return bad;
+}
+// As above with a position for each pair.
+template <bool INTER>
+__device__ __forceinline__ void load_angles(const float* cs, const Places& r, unsigned long long map, int piece,
+                                            Angles* a) {
+  constexpr int kPairs = INTER ? 4 : 8;
+  const int first = INTER ? piece * 4 : (piece & 3) * 8;
+  const uint32_t m = (uint32_t)(map >> (2 * first));
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const uint32_t axis = m >> (2 * i) & 3;
+    const int at = axis == 0 ? r.p[0] : axis == 1 ? r.p[1] : axis == 2 ? r.p[2] : r.p[3];
+    const float* row = cs + (size_t)at * 64 + first + i;
+    a->c[i] = __ldg(row);
+    a->s[i] = __ldg(row + 32);
+  }
+}
 // Rotates the lane's piece (lane % 8 = piece) by +angle, or by -angle
 // (sgn = -1).  Not interleaved, a pair's halves sit four lanes apart: every
 // lane of the warp calls this.

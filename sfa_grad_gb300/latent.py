@@ -1,7 +1,8 @@
 """Binding of the latent-row operators (include/sfa_grad.h): the norm and
 position rotation of the attention's input rows with their gradients, the
-append to a paged cache, and the attention of new tokens over it.  Argument
-checks and marshalling only, like the rest of the binding.
+append to a paged cache of 16 or 4 bits, the attention of new tokens over it,
+and the block tables and slot maps of a step.  Argument checks and marshalling
+only, like the rest of the binding.
 """
 from __future__ import annotations
 
@@ -15,7 +16,11 @@ import torch
 from . import DTYPES, LAYOUTS, _check, _stream, _workspace, lib
 
 EXPORTS = ("sfa_norm_rope", "sfa_norm_rope_grad_workspace_size", "sfa_norm_rope_grad", "sfa_cache_append",
-           "sfa_paged_workspace_size", "sfa_paged_fwd")
+           "sfa_paged_workspace_size", "sfa_paged_fwd", "sfa_norm_rope_axes", "sfa_norm_rope_axes_grad",
+           "sfa_cache4_append", "sfa_paged4_workspace_size", "sfa_paged4_fwd", "sfa_cache4_unpack",
+           "sfa_cache_append_slots", "sfa_page_plan")
+
+CODES4 = 288        # bytes of a 4-bit row before its rotated part: 256 of codes, 32 of scales
 
 
 class RowsParams(ctypes.Structure):
@@ -32,11 +37,24 @@ class PagedParams(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("wait_limit_us", ctypes.c_int32)]
 
 
+class CacheParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("bits", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("Dr", ctypes.c_int64), ("scale", ctypes.c_double)]
+
+
+class PlanParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
+
 # The calls pass their parameters packed: a Structure costs more to fill than
 # the whole of a small call's checks.
 _pack_rows = struct.Struct("@iiqqqd").pack
 _pack_paged = struct.Struct("@iiqqqqqqqqqdqii").pack
-assert struct.calcsize("@iiqqqd") == ctypes.sizeof(RowsParams)
+_pack_cache = struct.Struct("@iiqqqd").pack
+_pack_plan = struct.Struct("@qqqqq").pack
+assert struct.calcsize("@iiqqqd") == ctypes.sizeof(RowsParams) == ctypes.sizeof(CacheParams)
+assert struct.calcsize("@qqqqq") == ctypes.sizeof(PlanParams)
 assert struct.calcsize("@iiqqqqqqqqqdqii") == ctypes.sizeof(PagedParams)
 
 _ready = None
@@ -54,6 +72,15 @@ def _lib():
         L.sfa_cache_append.argtypes = [P] + [vp] * 7 + [d, vp, i64] + [vp] * 4
         L.sfa_paged_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
         L.sfa_paged_fwd.argtypes = [P] + [vp] * 10 + [sz, vp]
+        i32 = ctypes.c_int32
+        L.sfa_norm_rope_axes.argtypes = [R, i32] + [vp] * 16
+        L.sfa_norm_rope_axes_grad.argtypes = [R, i32] + [vp] * 19 + [vp, sz, vp]
+        L.sfa_cache4_append.argtypes = [P, d] + [vp] * 7 + [d, vp, i64] + [vp] * 4
+        L.sfa_paged4_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
+        L.sfa_paged4_fwd.argtypes = [P, d] + [vp] * 10 + [sz, vp]
+        L.sfa_cache4_unpack.argtypes = [vp] * 4
+        L.sfa_cache_append_slots.argtypes = [vp, R, vp, vp, i32] + [vp] * 10
+        L.sfa_page_plan.argtypes = [vp] * 13
         for name in EXPORTS:
             getattr(L, name).restype = ctypes.c_int32
         _ready = L
@@ -115,7 +142,20 @@ def _call(index, stream, fn, what, *args):
 
 
 # ------------------------------------------------------------------ norm and rotation
-def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved):
+def _axes(axes, positions, tokens):
+    """Number of axes, and the axis of each pair as 32 bytes."""
+    at = bytes(tuple(axes))
+    if positions is None or positions.dim() < 1 or positions.numel() != positions.shape[0] * tokens:
+        raise ValueError(f"positions: expected (axes, ...) of {tokens} tokens")
+    n = positions.shape[0]
+    if not 1 <= n <= 4:
+        raise ValueError(f"positions: {n} axes, expected 1 to 4")
+    if len(at) != 32 or max(at) >= n:
+        raise ValueError(f"axes: expected 32 numbers below {n}, the axis of each rotated pair")
+    return n, at
+
+
+def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved, axes=None):
     """Parameters, leading shape, heads and addresses of the row tensors that
     are there (queries (..., N1, 512 / 64), keys (..., 1, 512 / 64))."""
     first = k if k is not None else q if q is not None else k_rope if k_rope is not None else q_rope
@@ -138,7 +178,7 @@ def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved):
     pos = cs = None
     table_len = 0
     if positions is not None:
-        if positions.numel() != tokens:
+        if axes is None and positions.numel() != tokens:
             raise ValueError(f"positions: {positions.numel()} elements, expected {tokens}")
         pos = _need("positions", positions, positions.shape, torch.int32, dev)
         if cos_sin is None:
@@ -151,15 +191,17 @@ def _rows(q, q_rope, k, k_rope, positions, cos_sin, eps, interleaved):
 
 @_on_stream
 def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None, q_weight=None, q_rope=None, eps=1e-6,
-              interleaved=True, outputs=None, stream=None):
+              interleaved=True, outputs=None, axes=None, stream=None):
     """sfa_norm_rope on torch CUDA tensors: normalises k (..., 1, 512) and q
     (..., N1, 512) by their weights (512,), rotates k_rope (..., 1, 64) and
     q_rope (..., N1, 64) by cos_sin[positions] (fp32 (P, 64): 32 cosines, 32
     sines).  Each of the four rows may be left out.  Returns (q, q_rope, k,
     k_rope, q_rstd, k_rstd), None where its input is; `outputs`: such a tuple
-    to write into, where an output may be its own input."""
+    to write into, where an output may be its own input.  `axes`: 32 numbers,
+    the axis of each rotated pair; positions then are (axes, ...), up to four
+    of them (sfa_norm_rope_axes)."""
     p, lead, heads, dt, dev, pos, cs, (qa, qra, ka, kra) = _rows(q, q_rope, k, k_rope, positions, cos_sin, eps,
-                                                                 interleaved)
+                                                                 interleaved, axes)
     kw = None if k is None else _need("k_weight", k_weight, (512,), dt, dev)
     qw = None if q is None else _need("q_weight", q_weight, (512,), dt, dev)
     if outputs is None:
@@ -173,21 +215,27 @@ def norm_rope(positions, cos_sin, *, k=None, k_weight=None, k_rope=None, q=None,
              for name, t, x in zip(("q", "q_rope", "k", "k_rope"), outputs, (q, q_rope, k, k_rope))]
         o += [None if x is None or t is None else _need(f"outputs: {name}", t, lead + (h,), torch.float32, dev)
               for name, t, x, h in (("q_rstd", outputs[4], q, heads), ("k_rstd", outputs[5], k, 1))]
-    _call(dev, stream, _lib().sfa_norm_rope, "sfa_norm_rope", _pack_rows(*p), pos, cs, qa, qw, qra, ka, kw, kra, *o)
+    if axes is None:
+        _call(dev, stream, _lib().sfa_norm_rope, "sfa_norm_rope", _pack_rows(*p), pos, cs, qa, qw, qra, ka, kw, kra, *o)
+    else:
+        _call(dev, stream, _lib().sfa_norm_rope_axes, "sfa_norm_rope_axes", _pack_rows(*p),
+              *_axes(axes, positions, p[2]), pos, cs, qa, qw, qra, ka, kw, kra, *o)
     return outputs
 
 
 @_on_stream
 def norm_rope_grad(positions, cos_sin, *, k=None, k_weight=None, k_rstd=None, dk=None, dk_rope=None, q=None,
-                   q_weight=None, q_rstd=None, dq=None, dq_rope=None, interleaved=True, workspace=None, stream=None):
+                   q_weight=None, q_rstd=None, dq=None, dq_rope=None, interleaved=True, workspace=None, axes=None,
+                   stream=None):
     """sfa_norm_rope_grad: gradients of norm_rope's inputs from those of its
     outputs (dq, dq_rope, dk, dk_rope, for instance sfa_grad's; where the row
     is key and value, dk is the sum of its dK and dV).  k, k_weight and k_rstd
-    (q, ...) are norm_rope's inputs and its saved rstd.  Returns (dq, dq_rope,
-    dk, dk_rope, dq_weight, dk_weight); the weights' gradients are fp32, summed
-    in a fixed order."""
+    (q, ...) are norm_rope's inputs and its saved rstd, positions and axes as
+    there.  Returns (dq, dq_rope, dk, dk_rope, dq_weight, dk_weight); the
+    weights' gradients are fp32, summed in a fixed order."""
     p, lead, heads, dt, dev, pos, cs, (dqa, dqra, dka, dkra) = _rows(dq, dq_rope, dk, dk_rope, positions, cos_sin, 0.0,
-                                                                     interleaved)
+                                                                     interleaved, axes)
+    several = () if axes is None else _axes(axes, positions, p[2])
     saved = {}
     for name, d, x, w, r, h in (("k", dk, k, k_weight, k_rstd, 1), ("q", dq, q, q_weight, q_rstd, heads)):
         saved[name] = (None, None, None) if d is None else (
@@ -208,8 +256,10 @@ def norm_rope_grad(positions, cos_sin, *, k=None, k_weight=None, k_rstd=None, dk
         ws, nbytes = _need("workspace", workspace, workspace.shape, workspace.dtype, dev), \
             workspace.numel() * workspace.element_size()
     o = [None if t is None else t.data_ptr() for t in out]
-    _call(dev, stream, _lib().sfa_norm_rope_grad, "sfa_norm_rope_grad", _pack_rows(*p), pos, cs, *saved["q"],
-          *saved["k"], dqa, dqra, dka, dkra, *o, ws, nbytes)
+    fn, what = (_lib().sfa_norm_rope_axes_grad, "sfa_norm_rope_axes_grad") if several else \
+        (_lib().sfa_norm_rope_grad, "sfa_norm_rope_grad")
+    _call(dev, stream, fn, what, _pack_rows(*p), *several, pos, cs, *saved["q"], *saved["k"], dqa, dqra, dka, dkra, *o,
+          ws, nbytes)
     return tuple(out)
 
 
@@ -222,25 +272,43 @@ def norm_rope_grad_workspace_size(p: RowsParams) -> int:
 
 # ------------------------------------------------------------------ paged cache
 def make_paged_params(cache, block_table, act_seq_kv, *, tokens, heads, layout="BSND", seq=None, act_seq_q=None,
-                      scale=1.0, sparse_mode=3, interleaved=True, wait_limit_us=0) -> PagedParams:
+                      scale=1.0, sparse_mode=3, interleaved=True, wait_limit_us=0, dtype=None) -> PagedParams:
     """Parameters of the paged calls, with checks of the cache and of the index
-    tensors.  `tokens`: rows of q (B * S1 for BSND, with `seq` = S1)."""
+    tensors.  `tokens`: rows of q (B * S1 for BSND, with `seq` = S1); `dtype`:
+    theirs, for a cache of 4 bits."""
+    if cache.dtype is torch.uint8 and dtype is None:
+        raise ValueError("dtype is required for a cache of 4 bits")
     return PagedParams(*_paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale,
-                               sparse_mode, interleaved, wait_limit_us)[0])
+                               sparse_mode, interleaved, wait_limit_us, dtype)[0])
+
+
+def _cache(cache, dtype, cache_scale):
+    """dtype of the rows, width of their rotated part, and the scale of a cache
+    of 4 bits (None: 16 bits)."""
+    if cache.dtype is torch.uint8:
+        if cache.dim() != 3 or cache.shape[2] not in (CODES4, CODES4 + 128):
+            raise ValueError("cache of 4 bits: expected (num_pages, page_size, 416) or (num_pages, page_size, 288)")
+        if dtype not in DTYPES:
+            raise ValueError("rows must be bfloat16 or float16")
+        return dtype, (cache.shape[2] - CODES4) // 2, 1.0 if cache_scale is None else cache_scale
+    if cache.dtype not in DTYPES:
+        raise ValueError("cache must be bfloat16 or float16, or uint8 (rows of 4 bits)")
+    if cache.dim() != 3 or cache.shape[2] not in (512, 576):
+        raise ValueError("cache: expected (num_pages, page_size, 576) or (num_pages, page_size, 512)")
+    if cache_scale is not None:
+        raise ValueError("cache_scale given for a cache of 16 bits")
+    return cache.dtype, cache.shape[2] - 512, None
 
 
 def _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale, sparse_mode, interleaved,
-           wait_limit_us):
-    """The fields of PagedParams, and the addresses of cache, block_table,
-    act_seq_q and act_seq_kv."""
-    if cache.dtype not in DTYPES:
-        raise ValueError("cache must be bfloat16 or float16")
-    if cache.dim() != 3 or cache.shape[2] not in (512, 576):
-        raise ValueError("cache: expected (num_pages, page_size, 576) or (num_pages, page_size, 512)")
+           wait_limit_us, dtype=None, cache_scale=None):
+    """The fields of PagedParams, the addresses of cache, block_table,
+    act_seq_q and act_seq_kv, and of a cache of 4 bits its scale."""
+    dt, dr, unit = _cache(cache, dtype, cache_scale)
     if block_table.dim() != 2:
         raise ValueError("block_table: expected (B, max_pages)")
     dev = cache.get_device()
-    pages, page, width = cache.shape
+    pages, page, _ = cache.shape
     b, per = block_table.shape
     at = (_need("cache", cache, cache.shape, cache.dtype, dev),
           _need("block_table", block_table, block_table.shape, torch.int32, dev))
@@ -251,8 +319,8 @@ def _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q
         qla = _need("act_seq_q", act_seq_q, (b,), torch.int32, dev)
     if lay == 0 and tokens != b * seq:
         raise ValueError(f"BSND rows of {tokens} tokens do not match {b} sequences of {seq}")
-    return (lay, DTYPES[cache.dtype], b, 0 if lay else seq, tokens if lay else 0, heads, 512, width - 512, pages, page,
-            per, scale, sparse_mode, 1 if interleaved else 0, wait_limit_us), at + (qla, kva)
+    return (lay, DTYPES[dt], b, 0 if lay else seq, tokens if lay else 0, heads, 512, dr, pages, page, per, scale,
+            sparse_mode, 1 if interleaved else 0, wait_limit_us), at + (qla, kva), unit
 
 
 def _leading(name, t, layout):
@@ -268,9 +336,11 @@ def _leading(name, t, layout):
 @_on_stream
 def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *, k_weight=None, eps=1e-6,
                  interleaved=True, q_rope=None, q_rope_out=None, layout="BSND", act_seq_q=None, error=None,
-                 stream=None):
+                 cache_scale=None, stream=None):
     """sfa_cache_append: writes the new tokens' rows [norm(k) || rotated
-    k_rope] into `cache` (num_pages, page_size, 576 or 512); k is (B, S1, 1,
+    k_rope] into `cache`, (num_pages, page_size, 576 or 512) or, of 4 bits in
+    units of cache_scale (a power of two; 1 unless given), uint8 (num_pages,
+    page_size, 416 or 288) (sfa_cache4_append); k is (B, S1, 1,
     512) or (T1, 1, 512).  act_seq_kv counts the new tokens too, and their
     positions are the last of their sequences.  With q_rope (..., N1, 64) the
     same launch rotates it into q_rope_out (allocated unless given; q_rope
@@ -278,14 +348,27 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
     SFA_DEVERR_* code.  Returns (cache, q_rope_out)."""
     lead, tokens, seq = _leading("k", k, layout)
     heads = 1 if q_rope is None else q_rope.shape[-2]
-    p, (ca, bta, aq, akv) = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, 1.0, 3,
-                                   interleaved, 0)
-    dt, dev = cache.dtype, cache.get_device()
+    p, (ca, bta, aq, akv), unit = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, 1.0, 3,
+                                         interleaved, 0, k.dtype, cache_scale)
+    (ka, kra, kw, cs, qra, qroa), table_len, err, q_rope_out = _new_rows(
+        cache, p[7], lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error)
+    args = (ca, bta, aq, akv, ka, kra, kw, eps, cs, table_len, qra, qroa, err)
+    if unit is None:
+        _call(cache.get_device(), stream, _lib().sfa_cache_append, "sfa_cache_append", _pack_paged(*p), *args)
+    else:
+        _call(cache.get_device(), stream, _lib().sfa_cache4_append, "sfa_cache4_append", _pack_paged(*p), unit, *args)
+    return cache, q_rope_out
+
+
+def _new_rows(cache, dr, lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error):
+    """Addresses of an append's rows, its table's length and error word, and
+    q_rope_out."""
+    dt, dev = k.dtype if cache.dtype is torch.uint8 else cache.dtype, cache.get_device()
     ka = _need("k", k, lead + (1, 512), dt, dev)
     kw = None if k_weight is None else _need("k_weight", k_weight, (512,), dt, dev)
     kra = cs = qra = qroa = None
     table_len = 0
-    if cache.shape[2] == 576:
+    if dr:
         kra = _need("k_rope", k_rope, lead + (1, 64), dt, dev)
         if cos_sin is None:
             raise ValueError("cos_sin is required")
@@ -299,9 +382,110 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
     elif k_rope is not None or q_rope is not None:
         raise ValueError("rope rows given for a cache without them")
     err = None if error is None else _need("error", error, (1,), torch.int32, dev)
-    _call(dev, stream, _lib().sfa_cache_append, "sfa_cache_append", _pack_paged(*p), ca, bta, aq, akv, ka, kra, kw, eps,
-          cs, table_len, qra, qroa, err)
+    return (ka, kra, kw, cs, qra, qroa), table_len, err, q_rope_out
+
+
+@_on_stream
+def cache_append_slots(cache, slots, positions, k, k_rope=None, cos_sin=None, *, k_weight=None, eps=1e-6,
+                       interleaved=True, q_rope=None, q_rope_out=None, axes=None, error=None, cache_scale=None,
+                       stream=None):
+    """sfa_cache_append_slots: as cache_append, with the rows' places in a slot
+    map (tokens,) int32 (page_plan's, for instance; negative: padding, left
+    out) and their positions given, (tokens,) or, with `axes` (32 numbers, the
+    axis of each rotated pair), (axes, tokens).  k is (tokens, 1, 512).
+    Positions are not needed for a cache without rotated rows.  Returns (cache,
+    q_rope_out)."""
+    dt, dr, unit = _cache(cache, k.dtype, cache_scale)
+    dev = cache.get_device()
+    if k.dim() != 3:
+        raise ValueError("k: expected (tokens, 1, 512)")
+    lead, tokens = k.shape[:1], k.shape[0]
+    heads = 1 if q_rope is None else q_rope.shape[-2]
+    ca = _need("cache", cache, cache.shape, cache.dtype, dev)
+    sa = _need("slots", slots, (tokens,), torch.int32, dev)
+    (ka, kra, kw, cs, qra, qroa), table_len, err, q_rope_out = _new_rows(
+        cache, dr, lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error)
+    n, at, pos = 1, None, None
+    if dr:
+        if positions is None:
+            raise ValueError("positions is required")
+        if axes is not None:
+            n, at = _axes(axes, positions, tokens)
+        pos = _need("positions", positions, (tokens,) if axes is None else (n, tokens), torch.int32, dev)
+    elif axes is not None:
+        raise ValueError("axes given for a cache without rope rows")
+    pages, page, _ = cache.shape
+    _call(dev, stream, _lib().sfa_cache_append_slots, "sfa_cache_append_slots",
+          _pack_cache(DTYPES[dt], 16 if unit is None else 4, pages, page, dr, 0.0 if unit is None else unit),
+          _pack_rows(DTYPES[dt], 1 if interleaved else 0, tokens, heads, table_len, eps), ca, sa, n, at, pos, ka, kra,
+          kw, cs, qra, qroa, err)
     return cache, q_rope_out
+
+
+@_on_stream
+def cache_unpack(cache, dtype, *, cache_scale=None, out=None, stream=None):
+    """sfa_cache4_unpack: the values of a 4-bit cache, (num_pages, page_size,
+    576 or 512) in dtype, which is the one its rows were appended in."""
+    if cache.dtype is not torch.uint8:
+        raise ValueError("cache must be uint8 (rows of 4 bits)")
+    dt, dr, unit = _cache(cache, dtype, cache_scale)
+    dev = cache.get_device()
+    shape = cache.shape[:2] + (512 + dr,)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=cache.device)
+    _call(dev, stream, _lib().sfa_cache4_unpack, "sfa_cache4_unpack",
+          _pack_cache(DTYPES[dt], 4, shape[0], shape[1], dr, unit),
+          _need("cache", cache, cache.shape, torch.uint8, dev), _need("out", out, shape, dt, dev))
+    return out
+
+
+# ------------------------------------------------------------------ a step's tables
+def _words(shape, like):
+    return torch.empty_strided(shape, (1,), dtype=torch.int32, device=like.device)
+
+
+@_on_stream
+def page_plan(block_table, act_seq_kv, new_tokens, free_pages, free_count, *, page_size, tokens, error=None,
+              outputs=None, stream=None):
+    """sfa_page_plan: gives the requests of a step the pages that their new
+    tokens need and takes back those of ended ones (new_tokens negative), on
+    the device.  block_table (B, max_pages) and free_pages (num_pages,), of
+    which the first free_count (1,) are free, are changed in place; all int32.
+    Returns (act_seq_q, act_seq_kv, free_count, slots, positions): the new
+    tokens and lengths of the step, what is left, and the row of the cache and
+    position of each new token, `tokens` of them (-1 behind the last).
+    `outputs`: such a tuple to write into, overlapping no input.  `error`:
+    optional int32 (1,) that receives a SFA_DEVERR_* code; a step that does not
+    fit changes nothing."""
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("expected block_table (B, max_pages) and free_pages (num_pages,)")
+    b, per = block_table.shape
+    dev, i32 = block_table.get_device(), torch.int32
+    at = (_need("block_table", block_table, block_table.shape, i32, dev),
+          _need("act_seq_kv", act_seq_kv, (b,), i32, dev), _need("new_tokens", new_tokens, (b,), i32, dev),
+          _need("free_pages", free_pages, free_pages.shape, i32, dev),
+          _need("free_count", free_count, (1,), i32, dev))
+    if outputs is None:
+        if tokens < 0:
+            raise ValueError("tokens must not be negative")
+        outputs = (_words((b,), block_table), _words((b,), block_table), _words((1,), block_table),
+                   _words((tokens,), block_table), _words((tokens,), block_table))
+        o = [t.data_ptr() for t in outputs]
+    else:
+        o = [_need(f"outputs: {name}", t, shape, i32, dev) for name, t, shape in
+             zip(("act_seq_q", "act_seq_kv", "free_count", "slots", "positions"), outputs,
+                 ((b,), (b,), (1,), (tokens,), (tokens,)))]
+    err = None if error is None else _need("error", error, (1,), i32, dev)
+    _call(dev, stream, _lib().sfa_page_plan, "sfa_page_plan",
+          _pack_plan(b, per, free_pages.shape[0], page_size, tokens), *at, *o, err)
+    return outputs
+
+
+# ------------------------------------------------------------------ attention over the cache
+def paged4_workspace_size(p: PagedParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib().sfa_paged4_workspace_size(ctypes.byref(p), ctypes.byref(n)), "sfa_paged4_workspace_size")
+    return n.value
 
 
 def paged_workspace_size(p: PagedParams) -> int:
@@ -312,21 +496,23 @@ def paged_workspace_size(p: PagedParams) -> int:
 
 @_on_stream
 def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="BSND", act_seq_q=None, sparse_mode=3,
-              out=None, softmax_max=None, softmax_sum=None, workspace=None, stream=None, wait_limit_us=0):
+              out=None, softmax_max=None, softmax_sum=None, workspace=None, stream=None, wait_limit_us=0,
+              cache_scale=None):
     """sfa_paged_fwd: attention of the new tokens' q (B, S1, N1, 512) or (T1,
     N1, 512) over their sequences' rows in the paged cache; returns (out,
     softmax_max, softmax_sum), the statistics (B, 1, S1, N1) or (1, T1, N1) as
     fwd's.  Rows of no sequence (BSND past act_seq_q, TND past the last
-    sequence) are left as they were.  read_device_error reads a passed
-    workspace's error word."""
+    sequence) are left as they were.  A uint8 cache holds rows of 4 bits in
+    units of cache_scale, as cache_append's (sfa_paged4_fwd).
+    read_device_error reads a passed workspace's error word."""
     lead, tokens, seq = _leading("q", q, layout)
     heads = q.shape[-2]
-    p, (ca, bta, aq, akv) = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale,
-                                   sparse_mode, True, wait_limit_us)
-    dt, dev = cache.dtype, cache.get_device()
+    p, (ca, bta, aq, akv), unit = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale,
+                                         sparse_mode, True, wait_limit_us, q.dtype, cache_scale)
+    dt, dev = q.dtype if unit is not None else cache.dtype, cache.get_device()
     qa = _need("q", q, lead + (heads, 512), dt, dev)
     qra = None
-    if cache.shape[2] == 576:
+    if p[7]:
         qra = _need("q_rope", q_rope, lead + (heads, 64), dt, dev)
     elif q_rope is not None:
         raise ValueError("q_rope given for a cache without rope rows")
@@ -341,8 +527,12 @@ def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="
     ma = _need("softmax_max", softmax_max, st_shape, torch.float32, dev)
     sa = _need("softmax_sum", softmax_sum, st_shape, torch.float32, dev)
     if workspace is None or workspace.get_device() != dev:
-        workspace = _workspace(paged_workspace_size(PagedParams(*p)), cache.device, workspace)
+        size = paged_workspace_size if unit is None else paged4_workspace_size
+        workspace = _workspace(size(PagedParams(*p)), cache.device, workspace)
     ws = _need("workspace", workspace, workspace.shape, workspace.dtype, dev)
-    _call(dev, stream, _lib().sfa_paged_fwd, "sfa_paged_fwd", _pack_paged(*p), qa, qra, ca, bta, aq, akv, oa, ma, sa, ws,
-          workspace.numel() * workspace.element_size())
+    args = (qa, qra, ca, bta, aq, akv, oa, ma, sa, ws, workspace.numel() * workspace.element_size())
+    if unit is None:
+        _call(dev, stream, _lib().sfa_paged_fwd, "sfa_paged_fwd", _pack_paged(*p), *args)
+    else:
+        _call(dev, stream, _lib().sfa_paged4_fwd, "sfa_paged4_fwd", _pack_paged(*p), unit, *args)
     return out, softmax_max, softmax_sum
