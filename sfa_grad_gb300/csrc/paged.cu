@@ -761,12 +761,20 @@ static int few_rows(const Paged& p, int nsm) {
   return rows <= 64 && keys >= 640LL * nsm ? 64 : 0;
 }
 
+// Rows of 4 bits that are unpacked on the way to the MMAs, in tiles of few
+// rows, cost every row tile its unpacking; unpacked ahead of the call, once.
+static int few_rows4(const Paged& p) {
+  const long long rows = (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G;
+  return rows <= 32 ? 32 : rows <= 512 ? 64 : 0;
+}
+
 // Where a packed cache's values go: tables, then pages.  Pages shared by
 // sequences are unpacked once where the cache has fewer than the tables name.
 static bool by_page(const Paged& p) { return p.num_pages <= (long long)p.B * p.max_pages; }
 static size_t table_bytes(const Paged& p) { return up256((size_t)p.B * p.max_pages * sizeof(int)); }
 
 size_t paged4_workspace(const Paged& p) {
+  if (few_rows4(p)) return paged_workspace(p);
   const size_t pages = by_page(p) ? (size_t)p.num_pages : (size_t)p.B * p.max_pages;
   return paged_workspace(p) + table_bytes(p) + pages * p.page_size * p.row * 2;
 }
@@ -793,8 +801,9 @@ static cudaError_t launch_unpacked(PagedArgs a, int nsm, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
-  if (a.packed) return launch_unpacked<T>(a, nsm, st);
   const Paged& p = a.pg;
+  const int few = a.packed ? few_rows4(p) : few_rows(p, nsm);
+  if (a.packed && !few) return launch_unpacked<T>(a, nsm, st);
   Args g;
   g.a = a;
   g.workers = nsm / 2;
@@ -805,7 +814,8 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   g.piece = reinterpret_cast<Piece*>(a.ws + kOffPiece);
   g.stats = reinterpret_cast<float4*>(a.ws + kOffStats);
   g.part = reinterpret_cast<float*>(a.ws + kOffPart);
-  if (const int few = few_rows(p, nsm)) {
+  if (few) {
+    if (a.packed) g.vbox = 16;   // rows of 4 bits come in groups of 16
     g.workers = g.ctas = nsm;
     return launch_paged_few<T>(g, few, st);
   }

@@ -30,6 +30,9 @@
 // Warps: 0..7 softmax, rescaling, epilogue, 8 the scores' MMAs, 15 the values',
 // 9 the walk with the page table and the query rows, 10..13 the loads of a
 // tile's slots, one each, 14 those of its rope panel.
+#include <type_traits>
+
+#include "cache4.cuh"
 #include "paged_work.cuh"
 
 namespace sfa {
@@ -37,24 +40,30 @@ namespace {
 
 constexpr int kKeys = 64;
 constexpr int kSoft = 8;                    // softmax warps, the first ones
-constexpr int kThreads = 32 * (kSoft + 8);
+constexpr int kDecode = 8;                  // warps that unpack rows of 4 bits
 constexpr int kSegs = 4;                    // work descriptors in flight
 constexpr int kTiles = 8;                   // tiles whose cache rows are known in advance
 constexpr int kMaxSlots = 10;
+constexpr int kGroup = 16;                  // rows of 4 bits that arrive together: never of two pages
+constexpr int kMaxRaw = 8;
 constexpr uint32_t kPanel = 8192;           // 64 rows of 128 bytes
 constexpr uint32_t kSlot = 2 * kPanel;
 constexpr uint32_t kColS = 256;             // tensor memory: O^T, 64 columns a block of 128 features, then two S^T
 
-// What follows from the rows of a row tile.
-template <int R>
+// What follows from the rows of a row tile, and from the cache's.
+template <int R, bool Q4, bool ROPE>
 struct Few {
+  static constexpr int kThreads = 32 * (kSoft + 8 + (Q4 ? kDecode - 4 : 0));
   static constexpr int kWide = R / 2;                  // rows of a softmax warp
-  static constexpr int kSlots = R == 32 ? 10 : 8;
+  static constexpr int kSlots = Q4 ? (R == 32 ? 7 : 6) : R == 32 ? 10 : 8;
+  static constexpr int kRaw = R == 32 ? 8 : 4;         // groups of packed rows on their way
+  static constexpr uint32_t kRowBytes = kRopeAt + (ROPE ? 128 : 0);
   static constexpr uint32_t kQPanel = R * 128;
   static constexpr uint32_t kOffP = 9 * kQPanel;       // P^T: 64 keys x 64 rows
   static constexpr uint32_t kOffRope = kOffP + kPanel;
   static constexpr uint32_t kOffRing = kOffRope + 2 * kPanel;
-  static constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
+  static constexpr uint32_t kOffRaw = kOffRing + kSlots * kSlot;
+  static constexpr uint32_t kOffCtl = kOffRaw + (Q4 ? kRaw * kGroup * kRowBytes : 0);
   using W = Work<R, kKeys, kThreads, 2>;
 };
 
@@ -62,6 +71,7 @@ struct Ctl {
   uint64_t full[kMaxSlots], empty[kMaxSlots], rfull[2], rempty[2];
   uint64_t qfull, qempty, sfull[2], sfree[2], pready, pfree, ofree;
   uint64_t xch, fch, settle[2];
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t tile_full[kTiles], tile_empty[kTiles];
   uint64_t flags[2];                        // a byte a softmax warp: some row's max rises
@@ -70,14 +80,18 @@ struct Ctl {
   int abort;
   Seg seg[kSegs];
   int y[kTiles][4];                         // cache row of each box of a tile
-  int loads[kMaxSlots], rloads[2];          // uses of a slot that have been issued
+  int loads[kMaxSlots], rloads[2];          // uses of a slot (4 bits: of a group's place) that have been issued
+  int none[kMaxRaw];                        // a group without a page: zeros
   alignas(16) float rbuf[64];               // a row's reference, times log2
   float fbuf[64];                           // ... and its factor for O
 };
-template <int R>
-constexpr uint32_t kSmem = Few<R>::kOffCtl + sizeof(Ctl) + 1024;
-static_assert(kSmem<32> <= 227 * 1024 && kSmem<64> <= 227 * 1024, "shared memory");
-static_assert(kSmem<32> > kOneCtaSmem && kSmem<64> > kOneCtaSmem, "one CTA an SM: it allocates all of tensor memory");
+template <int R, bool Q4, bool ROPE>
+constexpr uint32_t kSmem = Few<R, Q4, ROPE>::kOffCtl + sizeof(Ctl) + 1024;
+static_assert(kSmem<32, false, true> <= 227 * 1024 && kSmem<64, false, true> <= 227 * 1024, "shared memory");
+static_assert(kSmem<32, true, true> <= 227 * 1024 && kSmem<64, true, true> <= 227 * 1024, "shared memory");
+static_assert(kSmem<32, false, false> > kOneCtaSmem && kSmem<64, false, false> > kOneCtaSmem &&
+                  kSmem<32, true, false> > kOneCtaSmem && kSmem<64, true, false> > kOneCtaSmem,
+              "one CTA an SM: it allocates all of tensor memory");
 
 // The four steps of a contraction over 64 elements, by the elected lane of a
 // converged warp; SA, SB: a step in encoded descriptor units.
@@ -129,10 +143,22 @@ struct MapsFew {
   CUtensorMap c2, c1;  // the cache, boxes of vbox rows of two panels (vbox = 64 only) and of one
 };
 
-template <typename T, bool ROPE, int R>
-__global__ void __launch_bounds__(kThreads, 1)
+// Bytes of packed rows into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+template <typename T, bool ROPE, int R, bool Q4>
+__global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
     paged_few_kernel(const __grid_constant__ MapsFew maps, const Args args) {
-  using F = Few<R>;
+  using F = Few<R, Q4, ROPE>;
   using W = typename F::W;
   constexpr int kSlots = F::kSlots;
   constexpr uint32_t kQPanel = F::kQPanel, kOffP = F::kOffP, kOffRope = F::kOffRope, kOffRing = F::kOffRing;
@@ -154,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     c->abort = 0;
     c->flags[0] = c->flags[1] = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c->rfull[i], 1);
+      mbar_init(&c->rfull[i], Q4 ? kDecode : 1);
       mbar_init(&c->rempty[i], 1);
       c->rloads[i] = 0;
       mbar_init(&c->sfull[i], 1);
@@ -173,14 +199,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane < kSegs) mbar_init(&c->seg_full[lane], 1), mbar_init(&c->seg_empty[lane], kSoft + 2);
     c->rbuf[lane] = c->rbuf[lane + 32] = -INFINITY;
-    if (lane < kTiles) mbar_init(&c->tile_full[lane], 1), mbar_init(&c->tile_empty[lane], 4 + ROPE);
+    if (lane < kTiles) mbar_init(&c->tile_full[lane], 1), mbar_init(&c->tile_empty[lane], Q4 ? 1 : 4 + ROPE);
     if (lane < kSlots) {
-      mbar_init(&c->full[lane], 1);
+      mbar_init(&c->full[lane], Q4 ? kDecode : 1);
       mbar_init(&c->empty[lane], 1);
-      c->loads[lane] = 0;
     }
+    if (lane < kMaxSlots) c->loads[lane] = 0;
+    if (Q4 && lane < F::kRaw) mbar_init(&c->raw_full[lane], 1), mbar_init(&c->raw_empty[lane], kDecode / 4);
     mbar_fence_init();
-  } else if (warp == 2 && lane < 4) {
+  } else if (warp == 2 && lane < (Q4 ? 2 : 4)) {
     const CUtensorMap* m = lane == 0 ? &maps.q : lane == 1 ? &maps.qr : lane == 2 ? &maps.c2 : &maps.c1;
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   }
@@ -268,7 +295,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // rows on their way, where another warp gave up
     if (issued > 0) mbar_settle(&c->qfull, (issued - 1) & 1, status);
-  } else if (work && warp >= kSoft + 2 && warp < kSoft + 6 + ROPE) {
+  } else if (Q4 && work && warp == kSoft + 2) {
+    // ---------------------------------------------------------------- packed rows, a group a place
+    const int none = p.num_pages * p.page_size;
+    for (int t = 0; t < ntiles; ++t) {
+      const int i = t % kTiles;
+      if (!warp_wait(&c->tile_full[i], (t / kTiles) & 1, w)) break;
+      const int y = c->y[i][lane & 3];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->tile_empty[i]);
+      bool ok = true;
+      for (int g = 0; g < 4 && ok; ++g) {
+        const int u = 4 * t + g, s = u % F::kRaw, use = u / F::kRaw;
+        if (use > 0 && !(ok = warp_wait(&c->raw_empty[s], (use - 1) & 1, w))) break;
+        if (lane == g) {
+          c->none[s] = y == none;
+          c->loads[s] = use + 1;
+          if (y == none) {
+            mbar_arrive(&c->raw_full[s]);
+          } else {
+            mbar_expect_tx(&c->raw_full[s], kGroup * F::kRowBytes);
+            bulk_load(smem_u32(sm) + F::kOffRaw + s * kGroup * F::kRowBytes,
+                      (const uint8_t*)args.a.cache + (size_t)y * F::kRowBytes, kGroup * F::kRowBytes, &c->raw_full[s]);
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+  } else if (Q4 && work && ((warp > kSoft + 2 && warp < kSoft + 7) || warp > kSoft + 7)) {
+    // ---------------------------------------------------------------- rows of 4 bits to panels
+    // Warp: a group's keys, one of a slot's two panels.  Lane: a key and half
+    // a panel's row, 32 features; eight neighbouring lanes have four keys and
+    // both halves, which keeps the reads (416 bytes apart) and the swizzled
+    // writes free of bank conflicts.
+    const int d = warp < kSoft + 7 ? warp - (kSoft + 3) : warp - (kSoft + 4);
+    const int g = d & 3, half = d >> 2;
+    const int key = (lane & 3) + 4 * (lane >> 3), part = (lane >> 2) & 1;
+    const uint32_t row = (g * kGroup + key) * 128, swz = key & 7;
+    const Dec4<T> dec(args.a.scale_exp);
+    int s = 0, ph = 1;   // ring slot, and the phase of its release (the first use waits for none)
+    bool ok = true;
+    for (int t = 0; t < ntiles && ok; ++t) {
+      const int u = 4 * t + g, rs = u % F::kRaw;
+      if (!(ok = warp_wait(&c->raw_full[rs], (u / F::kRaw) & 1, w))) break;
+      const uint32_t src = smem_u32(sm) + F::kOffRaw + (rs * kGroup + key) * F::kRowBytes;
+      uint4 code[4], rope4[2];
+      uint32_t two[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int panel = 2 * i + half;
+        code[i] = lds128(src + panel * 32 + part * 16);
+        two[i] = lds_u16(src + kCodes + panel * 4 + part * 2);
+      }
+      if (ROPE) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) rope4[i] = lds128(src + kRopeAt + (4 * half + 2 * i + part) * 16);
+      }
+      if (c->none[rs]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = make_uint4(0, 0, 0, 0), two[i] = 0;
+        rope4[0] = rope4[1] = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->raw_empty[rs]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t sc[2];
+        dec.scales(two[i], sc);
+        if (!(ok = warp_wait(&c->empty[s], ph, w))) break;
+        const uint32_t dst = ring + s * kSlot + half * kPanel + row;
+        sts128(dst + (((4 * part + 0) ^ swz) << 4), dec.eight(code[i].x, sc[0]));
+        sts128(dst + (((4 * part + 1) ^ swz) << 4), dec.eight(code[i].y, sc[0]));
+        sts128(dst + (((4 * part + 2) ^ swz) << 4), dec.eight(code[i].z, sc[1]));
+        sts128(dst + (((4 * part + 3) ^ swz) << 4), dec.eight(code[i].w, sc[1]));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->full[s]);
+        if (++s == kSlots) s = 0, ph ^= 1;
+      }
+      if (!ok || !ROPE) continue;
+      const int b = t & 1;
+      if (t >= 2 && !(ok = warp_wait(&c->rempty[b], ((t >> 1) - 1) & 1, w))) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        sts128(rope + b * kPanel + row + (((4 * half + 2 * i + part) ^ swz) << 4), rope4[i]);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->rfull[b]);
+    }
+  } else if (!Q4 && work && warp >= kSoft + 2 && warp < kSoft + 6 + ROPE) {
     // ---------------------------------------------------------------- TMA loads
     const int boxes = kKeys / args.vbox;
     const int pl = boxes == 1 ? 0 : lane / boxes, pb = boxes == 1 ? 0 : lane % boxes;   // panel, box of a lane
@@ -608,7 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (c->abort && tid < kSlots + 2) {   // copies on their way, where some warp gave up
+  if (Q4) {
+    if (c->abort && tid < F::kRaw && c->loads[tid] > 0) mbar_settle(&c->raw_full[tid], (c->loads[tid] - 1) & 1, status);
+  } else if (c->abort && tid < kSlots + 2) {   // copies on their way, where some warp gave up
     const int s = tid < kSlots ? tid : tid - kSlots, n = tid < kSlots ? c->loads[s] : c->rloads[s];
     if (n > 0) mbar_settle(tid < kSlots ? &c->full[s] : &c->rfull[s], (n - 1) & 1, status);
   }
@@ -617,21 +735,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-template <typename T, int R>
+template <typename T, int R, bool Q4, bool ROPE>
 static cudaError_t launch_few(const Args& g, cudaStream_t st) {
   const Paged& p = g.a.pg;
-  MapsFew m;
-  const bool f16 = Elt<T>::is_f16, rope = p.row == 576;
+  MapsFew m{};
+  const bool f16 = Elt<T>::is_f16;
   const uint64_t rows = (uint64_t)p.T * p.G, cached = (uint64_t)p.num_pages * p.page_size;
   if (!encode_map2d(&m.q, f16, g.a.q, 512, rows, R) ||
-      !encode_map2d(&m.qr, f16, rope ? g.a.qr : g.a.q, rope ? 64 : 512, rows, R) ||
-      !encode_map_panels(&m.c2, f16, g.a.cache, p.row, cached, g.vbox, g.vbox == 64 ? 2 : 1) ||
-      !encode_map_panels(&m.c1, f16, g.a.cache, p.row, cached, g.vbox, 1))
+      !encode_map2d(&m.qr, f16, ROPE ? g.a.qr : g.a.q, ROPE ? 64 : 512, rows, R) ||
+      (!Q4 && (!encode_map_panels(&m.c2, f16, g.a.cache, p.row, cached, g.vbox, g.vbox == 64 ? 2 : 1) ||
+               !encode_map_panels(&m.c1, f16, g.a.cache, p.row, cached, g.vbox, 1))))
     return cudaErrorInvalidValue;
-  auto kern = rope ? paged_few_kernel<T, true, R> : paged_few_kernel<T, false, R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
+  auto kern = paged_few_kernel<T, ROPE, R, Q4>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R, Q4, ROPE>);
   if (e != cudaSuccess) return e;
-  kern<<<g.ctas, kThreads, kSmem<R>, st>>>(m, g);
+  kern<<<g.ctas, Few<R, Q4, ROPE>::kThreads, kSmem<R, Q4, ROPE>, st>>>(m, g);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_paged_merge<T>(g, R, st);
@@ -639,7 +757,13 @@ static cudaError_t launch_few(const Args& g, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_paged_few(const Args& g, int rows, cudaStream_t st) {
-  return rows == 32 ? launch_few<T, 32>(g, st) : launch_few<T, 64>(g, st);
+  const bool rope = g.a.pg.row == 576;
+  auto pick = [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    if (g.a.packed) return rope ? launch_few<T, R, true, true>(g, st) : launch_few<T, R, true, false>(g, st);
+    return rope ? launch_few<T, R, false, true>(g, st) : launch_few<T, R, false, false>(g, st);
+  };
+  return rows == 32 ? pick(std::integral_constant<int, 32>{}) : pick(std::integral_constant<int, 64>{});
 }
 
 template cudaError_t launch_paged_few<__nv_bfloat16>(const Args&, int, cudaStream_t);
