@@ -102,6 +102,9 @@ bool encode_map2d(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uin
 // box_rows x box_panels.
 bool encode_map_panels(CUtensorMap* m, bool f16, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows,
                        uint32_t box_panels);
+// Rows of bytes, boxes of box_bytes (128 with 128-byte swizzle, or fewer) x box_rows.
+bool encode_map_bytes(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
+                      uint32_t box_rows);
 
 // Deterministic key-side reduction (det.cu): counting sort of the chunk's
 // (kv row, token, slot) entries by row (count, then launch_blk_scan over the

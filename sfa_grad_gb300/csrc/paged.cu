@@ -30,23 +30,36 @@
 // Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
 // MMAs (only in the pair's first CTA), 6 the walk over the work with the page
 // table and the query rows, 8..15 softmax and epilogue.
+#include "cache4.cuh"
 #include "paged_work.cuh"
 
 namespace sfa {
 namespace {
 
-constexpr int kThreads = 544;
+template <bool Q4>
+constexpr int kThreads = Q4 ? 896 : 544;
 constexpr int kTiles = 4;                   // tiles whose cache rows are known in advance
 constexpr int kSoft = 8;                    // softmax warps, from warp 8
 constexpr int kRows = 128;                  // rows of a row tile
 constexpr int kKeys = 256;                  // keys of a tile
-constexpr int kSlots = 7;                   // ring slots
+constexpr int kMaxSlots = 7;                // ring slots; rows of 4 bits leave room for fewer
+template <bool Q4>
+constexpr int kRingSlots = Q4 ? 4 : 7;
 constexpr uint32_t kPanel = 8192;           // 64 rows of 128 bytes
 constexpr uint32_t kSlot = 2 * kPanel;      // keys: 128 rows x 64 features; values: 64 rows x 128 features
 constexpr int kVSlots = 8;                  // ring slots of a tile's values
 constexpr uint32_t kOffP = 9 * kPanel;      // P: 64 rows x 256 keys
 constexpr uint32_t kOffRing = kOffP + 4 * kPanel;
-constexpr uint32_t kOffCtl = kOffRing + kSlots * kSlot;
+// Rows of 4 bits arrive in units of 128 keys x 256 features, codes and scales,
+// each the source of four slots: sets of four warps unpack a slot each.  Their
+// rotated parts have a place of their own, loaded a tile ahead.
+constexpr int kSets = 4, kSetWarps = 4, kUnits = 2;
+constexpr uint32_t kUnitScales = 128 * 128, kUnit = kUnitScales + 128 * 16;
+template <bool Q4>
+constexpr uint32_t kOffRope4 = kOffRing + kRingSlots<Q4> * kSlot;
+constexpr uint32_t kOffUnits = kOffRope4<true> + kSlot;
+template <bool Q4>
+constexpr uint32_t kOffCtl = Q4 ? kOffUnits + kUnits * kUnit : kOffRope4<Q4>;
 constexpr uint32_t kColS = 256;             // tensor memory: O, then two S tiles of 128 columns
 constexpr int kSegs = 8;                    // work descriptors in flight
 // What the loads of a key tile need.
@@ -56,29 +69,32 @@ struct Tile {
 };
 
 struct Ctl {
-  uint64_t full[kSlots], empty[kSlots];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t qfull, qempty;
   uint64_t sfull[2], sfree[2];
-  uint64_t pready, pfree, ofree, vloc[kSlots];
+  uint64_t pready, pfree, ofree, vloc[kMaxSlots];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t tile_full[kTiles], tile_empty[kTiles];
   uint64_t xch[2];
+  uint64_t unit_full[kUnits], unit_empty[kUnits], rfull, rempty;   // rows of 4 bits
   uint64_t settle;
   Seg seg[kSegs];
   Tile tile[kTiles];
   float xbuf[2][4][64];
-  long long scan64[3 * kThreads / 32];
+  long long scan64[3 * kThreads<true> / 32];
   Share share;
   uint32_t tmem;
   int abort, peer_abort;
   // what this CTA's loaders have issued, for the end after a wait that gave up
-  int loads[kSlots];      // uses of a slot
-  int q_issued;
+  int loads[kMaxSlots];   // uses of a slot
+  int q_issued, rope_issued;
 };
 
-constexpr uint32_t kSmem = kOffCtl + sizeof(Ctl) + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory");
-static_assert(kSmem > kOneCtaSmem, "one CTA an SM: it allocates all of tensor memory");
+template <bool Q4>
+constexpr uint32_t kSmem = kOffCtl<Q4> + sizeof(Ctl) + 1024;
+static_assert(kSmem<false> <= 227 * 1024 && kSmem<true> <= 227 * 1024, "shared memory");
+static_assert(kSmem<false> > kOneCtaSmem && kSmem<true> > kOneCtaSmem,
+              "one CTA an SM: it allocates all of tensor memory");
 
 // ------------------------------------------------------------------ cluster
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -111,6 +127,11 @@ __device__ __forceinline__ void store_at(uint32_t cluster_addr, int v) {
 __device__ __forceinline__ int load_from(uint32_t cluster_addr) {
   int v;
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
 // ------------------------------------------------------------------ tensor cores, both SMs of the pair
@@ -166,27 +187,31 @@ __device__ __forceinline__ void pair_tma3(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 // (a row tile's beginning and end take about as long as a key tile and a half)
-using W = Work<kRows, kKeys, kThreads, 1>;
+template <bool Q4>
+using PairWork = Work<kRows, kKeys, kThreads<Q4>, 1>;
 
 struct Maps2 {
   CUtensorMap q, qr;   // boxes of 64 columns x 64 rows
   // the cache as (64 columns, rows, panels); k: boxes of kbox rows of a
-  // panel, v: of vbox rows, of two panels when vbox = 64
+  // panel, v: of vbox rows, of two panels when vbox = 64.  Rows of 4 bits: k:
+  // boxes of kbox rows x 128 bytes, v: x 16 bytes
   CUtensorMap k, v;
 };
 
-template <typename T, bool ROPE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <typename T, bool ROPE, bool Q4>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<Q4>, 1)
     paged_kernel(const __grid_constant__ Maps2 maps, const Args args) {
+  using W = PairWork<Q4>;
+  constexpr int kSlots = kRingSlots<Q4>;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  Ctl* c = reinterpret_cast<Ctl*>(sm + kOffCtl);
+  Ctl* c = reinterpret_cast<Ctl*>(sm + kOffCtl<Q4>);
   const Paged& p = args.a.pg;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cta_rank();
   const int pair = blockIdx.x >> 1;
   const bool leader = rank == 0;
-  constexpr int kKSlots = ROPE ? 9 : 8;       // ring slots of a tile's keys
+  constexpr int kKSlots = ROPE && !Q4 ? 9 : 8;   // ring slots of a tile's keys
   int* status = args.status + blockIdx.x;
 
   // programmatic launch: the merge may be set up from now on (it waits for
@@ -195,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     *status = 0;
     c->abort = 0;
-    c->q_issued = 0;
+    c->q_issued = c->rope_issued = 0;
     mbar_init(&c->qfull, 2);
     mbar_init(&c->qempty, 1);
     mbar_init(&c->settle, 1);
@@ -211,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane < kSlots) {
       mbar_init(&c->vloc[lane], 1);
-      mbar_init(&c->full[lane], 2);
+      mbar_init(&c->full[lane], Q4 ? 2 * kSetWarps : 2);
       mbar_init(&c->empty[lane], 1);
       c->loads[lane] = 0;
     }
@@ -226,9 +251,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&c->seg_full[lane], 1);
       mbar_init(&c->seg_empty[lane], kSoft + (leader ? 1 : 0));
     }
+    if (Q4 && lane < kUnits) {
+      mbar_init(&c->unit_full[lane], 1);
+      mbar_init(&c->unit_empty[lane], kSets * kSetWarps);
+      if (lane == 0) mbar_init(&c->rfull, 2), mbar_init(&c->rempty, 1);
+    }
     if (lane < kTiles) {
       mbar_init(&c->tile_full[lane], 1);
-      mbar_init(&c->tile_empty[lane], kSlots);
+      mbar_init(&c->tile_empty[lane], Q4 ? kSets * kSetWarps + 1 + ROPE : kSlots);
     }
     mbar_fence_init();
   } else if (warp == 3 && lane < 4) {
@@ -336,7 +366,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // (the last query release: none is on its way to a CTA that has ended)
       if (ok && left == 0) ok = warp_wait(&c->qempty, n & 1, w);
     }
-  } else if (work && (warp < 4 || warp == 5 || warp == 7 || warp == 16)) {
+  } else if (Q4 && work && warp == 5) {
+    // ---------------------------------------------------------------- rows of 4 bits: TMA loads of units
+    // Two of a tile's keys (this CTA's 128, each half of the features), two of
+    // its values (each half of the keys, this CTA's 256 features).
+    const int nb = 128 / args.kbox, b = lane & 7, kstep = args.kbox / 16;
+    const bool codes = lane < nb, issues = codes || (lane >= 8 && lane < 8 + nb);
+    const uint32_t bytes = codes ? 128 : 16;
+    bool ok = true;
+    int u = 0;
+    auto load = [&](const Tile& t, int first, int half) {   // rows from key 128 * first, bytes of this half
+      const int s = u % kUnits, use = u / kUnits;
+      const int y = issues ? t.y[first * 8 + b * kstep] : 0;
+      if (use > 0 && !(ok = warp_wait(&c->unit_empty[s], (use - 1) & 1, w))) return;
+      if (lane == 0) mbar_expect_tx(&c->unit_full[s], kUnit);
+      __syncwarp();
+      if (issues)
+        tma_2d(smem_u32(sm) + kOffUnits + s * kUnit + (codes ? 0 : kUnitScales) + b * args.kbox * bytes,
+               codes ? &maps.k : &maps.v, codes ? half * 128 : kCodes + half * 16, y, &c->unit_full[s]);
+      ++u;
+    };
+    for (int t = -1; t < ntiles && ok; ++t) {
+      if (t + 1 < ntiles) {
+        const int i = (t + 1) % kTiles;
+        if (!(ok = warp_wait(&c->tile_full[i], ((t + 1) / kTiles) & 1, w))) break;
+        for (int h = 0; h < 2 && ok; ++h) load(c->tile[i], rank, h);
+      }
+      if (t >= 0) {
+        for (int h = 0; h < 2 && ok; ++h) load(c->tile[t % kTiles], h, rank);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->tile_empty[t % kTiles]);
+      }
+    }
+    // the copies on their way, whatever else gave up
+    for (int k = max(0, u - kUnits); k < u; ++k) mbar_settle(&c->unit_full[k % kUnits], (k / kUnits) & 1, status);
+  } else if (Q4 && ROPE && work && warp == 7) {
+    // ---------------------------------------------------------------- rows of 4 bits: rotated parts
+    const int nb = 128 / args.kbox, kstep = args.kbox / 16;
+    const uint32_t bar = map_to(smem_u32(&c->rfull), lead);
+    bool ok = true;
+    for (int t = 0; t < ntiles && ok; ++t) {
+      const int i = t % kTiles;
+      if (!(ok = warp_wait(&c->tile_full[i], (t / kTiles) & 1, w))) break;
+      const int y = lane < nb ? c->tile[i].y[(int)rank * 8 + lane * kstep] : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->tile_empty[i]);
+      if (t > 0 && !(ok = warp_wait(&c->rempty, (t - 1) & 1, w))) break;
+      if (lane == 0) {
+        expect_at(bar, kSlot);
+        c->rope_issued = t + 1;
+      }
+      __syncwarp();
+      if (lane < nb) pair_tma(smem_u32(sm) + kOffRope4<true> + lane * args.kbox * 128, &maps.k, kRopeAt, y, bar);
+    }
+    if (ok) warp_wait(&c->rempty, (ntiles - 1) & 1, w);   // the last release: none is on its way to a CTA that has ended
+  } else if (Q4 && work && (warp < 4 || warp > 15)) {
+    // ---------------------------------------------------------------- rows of 4 bits: units to slots
+    // Set k takes slot k of every unit; a warp 32 keys of a slot of keys (two
+    // steps of 16), or 16 keys of a slot of values (two steps of a panel).
+    // Lane: a key of a step's 16 and 32 of its 64 features, so that neighbouring
+    // lanes read and write the same piece of eight swizzled rows.
+    const int d = warp < 4 ? warp : warp - 12;
+    const int set = d >> 2, j = d & 3;
+    const int key16 = lane & 15, part = lane >> 4, swz = lane & 7;
+    const uint32_t units = smem_u32(sm) + kOffUnits;
+    static_assert(!Q4 || kSlots == kSets, "a set has a slot of its own");
+    const Dec4<T> dec(args.a.scale_exp);
+    const int n_units = 4 * ntiles;
+    const uint32_t full = map_to(smem_u32(&c->full[set & 3]), lead);
+    uint4 code[2];
+    uint32_t two[2];
+    // a unit's codes and scales: K(0) K(1) V(0) K(2) V(1) ... K(N-1) V(N-2) V(N-1), two units each
+    auto fetch = [&](int n) {
+      const int m = (n >> 1) - 1, end = 2 * (ntiles - 1);
+      const bool values = m >= 0 && ((m & 1) || m == end);
+      const int t = m == end ? ntiles - 1 : m >> 1;   // of values
+      const uint32_t src = units + (n % kUnits) * kUnit;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // key of the unit, panel of its four
+        const int key = values ? (set >> 1) * 64 + 16 * j + key16 : 32 * j + 16 * h + key16;
+        const int panel = values ? (set & 1) * 2 + h : set;
+        code[h] = lds128(src + key * 128 + (((2 * panel + part) ^ swz) << 4));
+        two[h] = lds_u16(src + kUnitScales + key * 16 + panel * 4 + part * 2);
+      }
+      const Tile& tl = c->tile[t % kTiles];
+      const int at = tl.key0 + (n & 1) * 128 + (set >> 1) * 64 + 16 * j + key16;
+      if (values && at > tl.least) {
+        // Values of masked keys: rows no query row sees become zeros (they may
+        // hold anything), and non-finite values of the others, which would
+        // reach rows that do not see them as 0 x inf (a row that sees them has
+        // a non-finite score from the same cache row).
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (at >= tl.kend) code[h] = make_uint4(0, 0, 0, 0), two[h] = 0;
+          if ((two[h] & 0x7f) == 0x7f) two[h] &= 0xff00;
+          if ((two[h] & 0x7f00) == 0x7f00) two[h] &= 0xff;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&c->unit_empty[n % kUnits]);
+        if (values && (n & 1)) mbar_arrive(&c->tile_empty[t % kTiles]);
+      }
+    };
+    bool ok = warp_wait(&c->unit_full[0], 0, w);
+    if (ok) fetch(0);
+    for (int n = 0; n < n_units && ok; ++n) {
+      // (unpacked before the slot is free: what follows its release is short)
+      uint4 v[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t sc[2];
+        dec.scales(two[h], sc);
+        v[h][0] = dec.eight(code[h].x, sc[0]);
+        v[h][1] = dec.eight(code[h].y, sc[0]);
+        v[h][2] = dec.eight(code[h].z, sc[1]);
+        v[h][3] = dec.eight(code[h].w, sc[1]);
+      }
+      // the next unit's codes now, if they are there, else after the slot
+      const int next = n + 1;
+      uint64_t* arrived = &c->unit_full[next % kUnits];
+      const uint32_t phase = (next / kUnits) & 1;
+      const bool early = next < n_units && __all_sync(~0u, mbar_poll(smem_u32(arrived), phase));
+      const int m = (n >> 1) - 1;
+      const bool values = m >= 0 && ((m & 1) || m == 2 * (ntiles - 1));
+      if (early) fetch(next);
+      if (n > 0 && !(ok = warp_wait(&c->empty[set], (n - 1) & 1, w))) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at =
+            ring + set * kSlot + (values ? h * kPanel + (16 * j + key16) * 128 : (32 * j + 16 * h + key16) * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts128(at + (((4 * part + i) ^ swz) << 4), v[h][i]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_at(full);
+      if (!early && next < n_units) {
+        if (!(ok = warp_wait(arrived, phase, w))) break;
+        fetch(next);
+      }
+    }
+    // the slot's last release has arrived: none is on its way to a CTA that has ended
+    if (ok && j == 0) warp_wait(&c->empty[set], (n_units - 1) & 1, w);
+  } else if (!Q4 && work && (warp < 4 || warp == 5 || warp == 7 || warp == 16)) {
     // ---------------------------------------------------------------- TMA loads
     // Slot s: the ring's uses s, s + kSlots, ...
     const int s = warp < 4 ? warp : warp == 5 ? 4 : warp == 7 ? 5 : 6;
@@ -468,12 +642,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (t >= 2 && !(ok = warp_wait(&c->sfree[t & 1], (t / 2 - 1) & 1, w))) return;
       tc_fence_after();   // the softmax warps' reads of this S buffer
       const uint32_t d = tmem + kColS + (t & 1) * 128;
+      if (Q4 && ROPE) {
+        if (!(ok = warp_wait(&c->rfull, t & 1, w))) return;
+        const uint64_t a = dq + desc_off(8 * kPanel), b = dk + desc_off(kSlots * kSlot);
+        pair_mma_first3<2, 2>(el, d, a, b, ids, 0);
+        pair_mma_last<2, 2>(el, d, a, b, ids);
+        pair_commit(el, &c->rempty);
+      }
 #pragma unroll 3
       for (int i = 0; i < kKSlots; ++i) {
         const int s = slot();
         if (!ok) return;
         const uint64_t a = dq + desc_off(i * kPanel), b = dk + desc_off(s * kSlot);
-        pair_mma_first3<2, 2>(el, d, a, b, ids, i > 0);
+        pair_mma_first3<2, 2>(el, d, a, b, ids, (Q4 && ROPE) || i > 0);
         peek();
         pair_mma_last<2, 2>(el, d, a, b, ids);
         pair_commit(el, &c->empty[s]);
@@ -519,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     for (int t = max(0, ntiles - 2); t < ntiles && ok; ++t) ok = warp_wait(&c->sfree[t & 1], (t >> 1) & 1, w);
     if (ok) warp_wait(&c->ofree, (pv_segs - 1) & 1, w);
-  } else if (work && warp >= 8) {
+  } else if (work && warp >= 8 && warp < 16) {
     // ---------------------------------------------------------------- softmax, epilogue
     // Thread: row r of this CTA's 64, keys 128 h + 64 g .. + 63 of a tile, and
     // features 256 h + 128 g .. + 127 of O; the four threads of a row exchange
@@ -728,6 +909,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       for (int i = 0; i < kSlots; ++i) finish(&c->full[i], c->loads[i], load_from(map_to(smem_u32(&c->loads[i]), 1)));
       finish(&c->qfull, c->q_issued, load_from(map_to(smem_u32(&c->q_issued), 1)));
+      if (Q4) finish(&c->rfull, c->rope_issued, load_from(map_to(smem_u32(&c->rope_issued), 1)));
     }
   }
   if (gave_up) cluster_sync();
@@ -761,11 +943,14 @@ static int few_rows(const Paged& p, int nsm) {
   return rows <= 64 && keys >= 640LL * nsm ? 64 : 0;
 }
 
-// Rows of 4 bits that are unpacked on the way to the MMAs, in tiles of few
-// rows, cost every row tile its unpacking; unpacked ahead of the call, once.
+// Rows of 4 bits that are unpacked on the way to the MMAs cost every row tile
+// its unpacking; unpacked ahead of the call, once.
+static bool many_rows4(const Paged& p) {
+  return (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G > 512;
+}
+
 static int few_rows4(const Paged& p) {
-  const long long rows = (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G;
-  return rows <= 32 ? 32 : rows <= 512 ? 64 : 0;
+  return (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G <= 32 ? 32 : 0;
 }
 
 // Where a packed cache's values go: tables, then pages.  Pages shared by
@@ -774,7 +959,7 @@ static bool by_page(const Paged& p) { return p.num_pages <= (long long)p.B * p.m
 static size_t table_bytes(const Paged& p) { return up256((size_t)p.B * p.max_pages * sizeof(int)); }
 
 size_t paged4_workspace(const Paged& p) {
-  if (few_rows4(p)) return paged_workspace(p);
+  if (!many_rows4(p)) return paged_workspace(p);
   const size_t pages = by_page(p) ? (size_t)p.num_pages : (size_t)p.B * p.max_pages;
   return paged_workspace(p) + table_bytes(p) + pages * p.page_size * p.row * 2;
 }
@@ -799,11 +984,32 @@ static cudaError_t launch_unpacked(PagedArgs a, int nsm, cudaStream_t st) {
   return launch_paged<T>(a, nsm, st);
 }
 
+template <typename T, bool ROPE, bool Q4>
+static cudaError_t launch_pairs(const Args& g, cudaStream_t st) {
+  const Paged& p = g.a.pg;
+  Maps2 m{};
+  const bool f16 = Elt<T>::is_f16;
+  const uint64_t rows = (uint64_t)p.T * p.G, cached = (uint64_t)p.num_pages * p.page_size;
+  if (!encode_map2d(&m.q, f16, g.a.q, 512, rows, 64) ||
+      !encode_map2d(&m.qr, f16, ROPE ? g.a.qr : g.a.q, ROPE ? 64 : 512, rows, 64) ||
+      (!Q4 && (!encode_map_panels(&m.k, f16, g.a.cache, p.row, cached, g.kbox, 1) ||
+               !encode_map_panels(&m.v, f16, g.a.cache, p.row, cached, g.vbox, g.vbox == 64 ? 2 : 1))) ||
+      (Q4 && (!encode_map_bytes(&m.k, g.a.cache, kRopeAt + (ROPE ? 128 : 0), cached, 128, g.kbox) ||
+              !encode_map_bytes(&m.v, g.a.cache, kRopeAt + (ROPE ? 128 : 0), cached, 16, g.kbox))))
+    return cudaErrorInvalidValue;
+  auto kern = paged_kernel<T, ROPE, Q4>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<Q4>);
+  if (e != cudaSuccess) return e;
+  kern<<<g.ctas, kThreads<Q4>, kSmem<Q4>, st>>>(m, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_paged_merge<T>(g, kRows, st);
+}
+
 template <typename T>
 cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   const Paged& p = a.pg;
-  const int few = a.packed ? few_rows4(p) : few_rows(p, nsm);
-  if (a.packed && !few) return launch_unpacked<T>(a, nsm, st);
+  if (a.packed && many_rows4(p)) return launch_unpacked<T>(a, nsm, st);
   Args g;
   g.a = a;
   g.workers = nsm / 2;
@@ -814,26 +1020,13 @@ cudaError_t launch_paged(const PagedArgs& a, int nsm, cudaStream_t st) {
   g.piece = reinterpret_cast<Piece*>(a.ws + kOffPiece);
   g.stats = reinterpret_cast<float4*>(a.ws + kOffStats);
   g.part = reinterpret_cast<float*>(a.ws + kOffPart);
-  if (few) {
-    if (a.packed) g.vbox = 16;   // rows of 4 bits come in groups of 16
+  if (a.packed) g.vbox = 16;   // the walk's grain
+  if (const int few = a.packed ? few_rows4(p) : few_rows(p, nsm)) {
     g.workers = g.ctas = nsm;
     return launch_paged_few<T>(g, few, st);
   }
-  Maps2 m;
-  const bool f16 = Elt<T>::is_f16, rope = p.row == 576;
-  const uint64_t rows = (uint64_t)p.T * p.G, cached = (uint64_t)p.num_pages * p.page_size;
-  if (!encode_map2d(&m.q, f16, a.q, 512, rows, 64) ||
-      !encode_map2d(&m.qr, f16, rope ? a.qr : a.q, rope ? 64 : 512, rows, 64) ||
-      !encode_map_panels(&m.k, f16, a.cache, p.row, cached, g.kbox, 1) ||
-      !encode_map_panels(&m.v, f16, a.cache, p.row, cached, g.vbox, g.vbox == 64 ? 2 : 1))
-    return cudaErrorInvalidValue;
-  auto kern = rope ? paged_kernel<T, true> : paged_kernel<T, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<g.ctas, kThreads, kSmem, st>>>(m, g);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_paged_merge<T>(g, kRows, st);
+  return a.packed ? (p.row == 576 ? launch_pairs<T, true, true>(g, st) : launch_pairs<T, false, true>(g, st))
+                  : (p.row == 576 ? launch_pairs<T, true, false>(g, st) : launch_pairs<T, false, false>(g, st));
 }
 
 template cudaError_t launch_paged<__nv_bfloat16>(const PagedArgs&, int, cudaStream_t);

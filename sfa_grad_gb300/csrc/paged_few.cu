@@ -55,8 +55,8 @@ template <int R, bool Q4, bool ROPE>
 struct Few {
   static constexpr int kThreads = 32 * (kSoft + 8 + (Q4 ? kDecode - 4 : 0));
   static constexpr int kWide = R / 2;                  // rows of a softmax warp
-  static constexpr int kSlots = Q4 ? (R == 32 ? 7 : 6) : R == 32 ? 10 : 8;
-  static constexpr int kRaw = R == 32 ? 8 : 4;         // groups of packed rows on their way
+  static constexpr int kSlots = Q4 ? (R == 32 ? 8 : 6) : R == 32 ? 10 : 8;
+  static constexpr int kRaw = 4;                        // groups of packed rows on their way: a place each, so that a warp meets every phase of its own
   static constexpr uint32_t kRowBytes = kRopeAt + (ROPE ? 128 : 0);
   static constexpr uint32_t kQPanel = R * 128;
   static constexpr uint32_t kOffP = 9 * kQPanel;       // P^T: 64 keys x 64 rows
@@ -363,12 +363,12 @@ __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
       for (int i = 0; i < 4; ++i) {
         uint32_t sc[2];
         dec.scales(two[i], sc);
+        const uint4 v[4] = {dec.eight(code[i].x, sc[0]), dec.eight(code[i].y, sc[0]), dec.eight(code[i].z, sc[1]),
+                            dec.eight(code[i].w, sc[1])};
         if (!(ok = warp_wait(&c->empty[s], ph, w))) break;
         const uint32_t dst = ring + s * kSlot + half * kPanel + row;
-        sts128(dst + (((4 * part + 0) ^ swz) << 4), dec.eight(code[i].x, sc[0]));
-        sts128(dst + (((4 * part + 1) ^ swz) << 4), dec.eight(code[i].y, sc[0]));
-        sts128(dst + (((4 * part + 2) ^ swz) << 4), dec.eight(code[i].z, sc[1]));
-        sts128(dst + (((4 * part + 3) ^ swz) << 4), dec.eight(code[i].w, sc[1]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sts128(dst + (((4 * part + k) ^ swz) << 4), v[k]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->full[s]);

@@ -190,14 +190,25 @@ struct Work {
     }
     if (lane == 31) scan[w] = u, scan[kWarps + w] = t, scan[2 * kWarps + w] = g;
     const bool any = __syncthreads_or(bad);
-    long long total = 0, toks_all = 0, tiles_all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < w) u += scan[i], t += scan[kWarps + i], g += (int)scan[2 * kWarps + i];
-      total += scan[i];
-      toks_all += scan[kWarps + i];
-      tiles_all += scan[2 * kWarps + i];
-    }
+    // the warps' sums, one a lane: what lies before this warp, and all of them
+    // (added up in a loop, unrolled over the warps, they took 4400 clk, most of
+    // it for fetching the code: this runs once a launch)
+    static_assert(kWarps <= 32, "a lane a warp");
+    long long total, toks_all, tiles_all;
+    auto sum = [&](int which, long long* all) {
+      long long x = lane < kWarps ? scan[which * kWarps + lane] : 0;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+      }
+      *all = __shfl_sync(~0u, x, 31);
+      const long long before = __shfl_sync(~0u, x, (w + 31) & 31);
+      return w ? before : 0;
+    };
+    u += sum(0, &total);
+    t += sum(1, &toks_all);
+    g += (int)sum(2, &tiles_all);
     const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)workers * (INT32_MAX / 2);
     const int np = total < 1 ? 1 : total < workers ? (int)total : workers;
     const int own = total > workers ? kOwn : 0;
@@ -213,7 +224,7 @@ struct Work {
       c->ntiles = 0;
       if (last == cost) c->end_seq[1] = -1, c->end_units[1] = total;
     }
-#pragma unroll
+#pragma unroll 1
     for (int e = 0; e < 2; ++e) {
       const long long at = e ? last : first;
       if (!mine || at < from || at >= to) continue;
