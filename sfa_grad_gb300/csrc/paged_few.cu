@@ -30,8 +30,6 @@
 // Warps: 0..7 softmax, rescaling, epilogue, 8 the scores' MMAs, 15 the values',
 // 9 the walk with the page table and the query rows, 10..13 the loads of a
 // tile's slots, one each, 14 those of its rope panel.
-#include <type_traits>
-
 #include "cache4.cuh"
 #include "paged_work.cuh"
 
@@ -55,7 +53,10 @@ template <int R, bool Q4, bool ROPE>
 struct Few {
   static constexpr int kThreads = 32 * (kSoft + 8 + (Q4 ? kDecode - 4 : 0));
   static constexpr int kWide = R / 2;                  // rows of a softmax warp
-  static constexpr int kSlots = Q4 ? (R == 32 ? 8 : 6) : R == 32 ? 10 : 8;
+  // Rows of 4 bits: a sum of its own for each slot of a tile, added up in fp32.
+  // The tensor core rounds every step of a sum towards zero, by the sum so far.
+  static constexpr int kSums = Q4 ? 4 : 1;
+  static constexpr int kSlots = R == 32 && !Q4 ? 10 : 8;
   static constexpr int kRaw = 4;                        // groups of packed rows on their way: a place each, so that a warp meets every phase of its own
   static constexpr uint32_t kRowBytes = kRopeAt + (ROPE ? 128 : 0);
   static constexpr uint32_t kQPanel = R * 128;
@@ -88,9 +89,9 @@ struct Ctl {
 template <int R, bool Q4, bool ROPE>
 constexpr uint32_t kSmem = Few<R, Q4, ROPE>::kOffCtl + sizeof(Ctl) + 1024;
 static_assert(kSmem<32, false, true> <= 227 * 1024 && kSmem<64, false, true> <= 227 * 1024, "shared memory");
-static_assert(kSmem<32, true, true> <= 227 * 1024 && kSmem<64, true, true> <= 227 * 1024, "shared memory");
+static_assert(kSmem<32, true, true> <= 227 * 1024, "shared memory");
 static_assert(kSmem<32, false, false> > kOneCtaSmem && kSmem<64, false, false> > kOneCtaSmem &&
-                  kSmem<32, true, false> > kOneCtaSmem && kSmem<64, true, false> > kOneCtaSmem,
+                  kSmem<32, true, false> > kOneCtaSmem,
               "one CTA an SM: it allocates all of tensor memory");
 
 // The four steps of a contraction over 64 elements, by the elected lane of a
@@ -136,6 +137,24 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 4 * N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same at `Sums` places, `step` columns apart: the first in v, the others in w.
+template <int N, int Sums, int Step>
+__device__ __forceinline__ void tmem_ld_frags(uint32_t taddr, float* v, float (*w)[4 * N]) {
+  static_assert(N == 2, "");
+  uint32_t r[Sums][8];
+#pragma unroll
+  for (int k = 0; k < Sums; ++k)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[k][0]), "=r"(r[k][1]), "=r"(r[k][2]), "=r"(r[k][3]), "=r"(r[k][4]), "=r"(r[k][5]),
+                   "=r"(r[k][6]), "=r"(r[k][7])
+                 : "r"(taddr + k * Step));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < Sums; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) (k ? w[k - 1] : v)[i] = __uint_as_float(r[k][i]);
 }
 
 struct MapsFew {
@@ -431,19 +450,20 @@ __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
       const int buf = t & 1;
       if (t >= 2 && !(ok = warp_wait(&c->sfree[buf], (t / 2 - 1) & 1, w))) break;
       tc_fence_after();   // the softmax warps' reads of this S buffer
-      const uint32_t d = tmem + kColS + buf * 64;
+      const uint32_t d0 = tmem + kColS + buf * (Q4 ? 128 : 64);
 #pragma unroll 2
       for (int i = 0; i < 4; ++i) {
+        const uint32_t d = d0 + (Q4 ? i * R : 0);
         if (!(ok = warp_wait(&c->full[s], ph, w))) break;
         const uint64_t a = dk + desc_off(s * kSlot), b = dq + desc_off(2 * i * kQPanel);
-        mma_k64<2, 2>(el, d, a, b, ids, i > 0);
+        mma_k64<2, 2>(el, d, a, b, ids, !Q4 && i > 0);
         mma_k64<2, 2>(el, d, a + desc_off(kPanel), b + desc_off(kQPanel), ids, 1);
         if (++s == kSlots) s = 0, ph ^= 1;
       }
       if (!ok) break;
       if (ROPE) {
         if (!(ok = warp_wait(&c->rfull[buf], (t >> 1) & 1, w))) break;
-        mma_k64<2, 2>(el, d, dr + desc_off(buf * kPanel), dq + desc_off(8 * kQPanel), ids, 1);
+        mma_k64<2, 2>(el, d0 + (Q4 ? 3 * R : 0), dr + desc_off(buf * kPanel), dq + desc_off(8 * kQPanel), ids, 1);
         commit(el, &c->rempty[buf]);
       }
       commit(el, &c->sfull[buf]);
@@ -562,7 +582,14 @@ __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
         tc_fence_after();
         const bool edge = (kt + 1) * kKeys > least + 1;
         float x[2 * kHas];   // [4 j + 2 h + e]: key + 8 h, row(2 j + e)
-        tmem_ld_frag<kWide / 8>(tq + kColS + buf * 64 + c0, x);
+        if constexpr (Q4) {
+          float y[F::kSums - 1][2 * kHas];
+          tmem_ld_frags<kWide / 8, F::kSums, R>(tq + kColS + buf * 128 + c0, x, y);
+#pragma unroll
+          for (int i = 0; i < 2 * kHas; ++i) x[i] = (x[i] + y[0][i]) + (y[1][i] + y[2][i]);
+        } else {
+          tmem_ld_frag<kWide / 8>(tq + kColS + buf * 64 + c0, x);
+        }
         if (sc.negative) {
 #pragma unroll
           for (int i = 0; i < 2 * kHas; ++i) x[i] = -x[i];
@@ -758,12 +785,9 @@ static cudaError_t launch_few(const Args& g, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_paged_few(const Args& g, int rows, cudaStream_t st) {
   const bool rope = g.a.pg.row == 576;
-  auto pick = [&](auto r) {
-    constexpr int R = decltype(r)::value;
-    if (g.a.packed) return rope ? launch_few<T, R, true, true>(g, st) : launch_few<T, R, true, false>(g, st);
-    return rope ? launch_few<T, R, false, true>(g, st) : launch_few<T, R, false, false>(g, st);
-  };
-  return rows == 32 ? pick(std::integral_constant<int, 32>{}) : pick(std::integral_constant<int, 64>{});
+  if (g.a.packed) return rope ? launch_few<T, 32, true, true>(g, st) : launch_few<T, 32, true, false>(g, st);
+  if (rows == 32) return rope ? launch_few<T, 32, false, true>(g, st) : launch_few<T, 32, false, false>(g, st);
+  return rope ? launch_few<T, 64, false, true>(g, st) : launch_few<T, 64, false, false>(g, st);
 }
 
 template cudaError_t launch_paged_few<__nv_bfloat16>(const Args&, int, cudaStream_t);
