@@ -91,12 +91,12 @@ __device__ __forceinline__ void spot_angles(const AppendArgs& a, const Spot& s, 
 // roundings could carry over a border between two codes or two scales is
 // found, and its row is quantised again from y in 64 bits.
 //
-// Steps of fp32 on the way: squares are exact or 2^-24 off, their sum 16 + 5
-// additions, the square root halves that, and a root, a reciprocal, two
-// products, the division by 6, the reciprocal of the scale and the product
-// with it add 2^-24 each: less than 19 x 2^-24 in all.  32 of them (2^-19) are
-// taken as near.
-constexpr float kNear = 1.0f / (1 << 19);
+// Roundings of fp32 on the way, 2^-24 each: 4 + 2 + 5 additions of squares and
+// the one of eps, halved by the square root; root, reciprocal, two products; the
+// division by 6 or by the scale, two more; 12 in all, and one to look aside.
+// What is within 16 of them (2^-20) of a border is near: a scale of one normal row in
+// 800, a code of one in 400.
+constexpr float kNear = 1.0f / (1 << 20);
 
 __device__ __forceinline__ uint32_t to_e4m3(float x) {   // one byte, to nearest, at most 448
   uint16_t r;
@@ -114,55 +114,35 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   memcpy(&v, &h, 4);
   return __low2float(v);
 }
-// The nearest scale to top / 6; a block with a value that is not finite gets
-// a scale that is not a number.
-template <typename F>
-__device__ __forceinline__ uint32_t exact_scale(F top) {
-  const F want = top / (F)6;
-  int e;
-  frexp(want, &e);
-  const F step = ldexp((F)1, max(e - 1, -6) - 3);
-  return to_e4m3(fminf((float)(rint(want / step) * step), 448.f));
-}
-template <typename F>
-__device__ __forceinline__ uint32_t exact_code(F y, F s) {
-  const F a = fabs(y);
-  // (products of a border's 3 bits and a scale's 4 are exact)
-  const int n = (a > (F)0.25 * s) + (a >= (F)0.75 * s) + (a > (F)1.25 * s) + (a >= (F)1.75 * s) + (a > (F)2.5 * s) +
-                (a >= (F)3.5 * s) + (a > (F)5 * s);
-  return (s > (F)0 ? n : 0) + (y < (F)0 ? 8 : 0);
-}
-
 struct Row4 {
   uint32_t scale[2], code[2];   // of the lane's elements 8 l .. 8 l + 7 and 256 + 8 l ..
 };
-// A lane's 16 values and the neighbour's (a block is two lanes').
-template <typename F>
-__device__ __forceinline__ Row4 quantise_exact(const F* y) {
-  Row4 r;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    F top = 0;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const F x = fabs(y[8 * h + i]);
-      bad |= !(x < (F)INFINITY);
-      top = x > top ? x : top;
-    }
-    const F o = __shfl_xor_sync(~0u, top, 1);
-    top = o > top ? o : top;
-    bad = __shfl_xor_sync(~0u, (int)bad, 1) || bad;
-    r.scale[h] = bad ? 0x7f : exact_scale(top);
-    r.code[h] = 0;
-    const F s = bad ? (F)0 : (F)e4m3_value(r.scale[h]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.code[h] |= exact_code(y[8 * h + i], s) << (4 * i);
-  }
-  return r;
+// The scale nearest to top / 6, top exact (a border between two scales is 3 times
+// their sum, exact too; scales ascend with their bytes, a tie goes to the even
+// one): fp32's, or one of its neighbours.
+template <typename Above, typename Is>
+__device__ __forceinline__ uint32_t next_scale(uint32_t b, Above above, Is is, float* up, float* down) {
+  *up = 3.f * (e4m3_value(b) + e4m3_value(min(b + 1, 126u)));
+  *down = 3.f * (e4m3_value(max(b, 1u) - 1) + e4m3_value(b));
+  if (b < 126 && (above(*up) || (is(*up) && (b & 1)))) return b + 1;
+  if (b > 0 && !above(*down) && !(is(*down) && !(b & 1))) return b - 1;
+  return b;
 }
-// The same in fp32; *near: a border is too close for that.
-__device__ __forceinline__ Row4 quantise_fast(const float* y, bool* near) {
+// The code nearest to a / s: borders between codes, times the scale, are exact.
+template <typename Above, typename Is>
+__device__ __forceinline__ uint32_t code_of(float s, Above above, Is is) {
+  constexpr float borders[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.f};
+  uint32_t n = 0;
+#pragma unroll
+  for (int k = 0; k < 7; ++k) n += above(borders[k] * s) || ((k & 1) && is(borders[k] * s));   // ties to the even code
+  return s > 0.f ? n : 0;
+}
+
+// A lane's 16 values (a block is two lanes') in fp32; *near: some border is too
+// close for that, unless the values are EXACT.  A block with a value that is
+// not finite gets a scale that is not a number.
+template <bool EXACT>
+__device__ __forceinline__ Row4 quantise(const float* y, bool* near) {
   Row4 r;
   bool close = false;
 #pragma unroll
@@ -178,7 +158,21 @@ __device__ __forceinline__ Row4 quantise_fast(const float* y, bool* near) {
     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
     bad = __shfl_xor_sync(~0u, (int)bad, 1) || bad;
     const float want = top * (1.f / 6.f);
-    const uint32_t sc = to_e4m3(want);
+    uint32_t sc = to_e4m3(want);
+    if constexpr (EXACT) {
+      float up, down;
+      sc = next_scale(sc, [&](float b) { return top > b; }, [&](float b) { return top == b; }, &up, &down);
+      const float s = e4m3_value(sc);
+      r.scale[h] = bad ? 0x7f : sc;
+      r.code[h] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(v[i]);
+        const uint32_t n = code_of(s, [&](float b) { return a > b; }, [&](float b) { return a == b; });
+        r.code[h] |= (bad ? 0 : n + (v[i] < 0.f ? 8 : 0)) << (4 * i);
+      }
+      continue;
+    }
     close |= to_e4m3(want * (1.f + kNear)) != to_e4m3(want * (1.f - kNear));
     const float s = e4m3_value(sc), inv = s > 0.f && !bad ? 1.f / s : 0.f;
     r.scale[h] = bad ? 0x7f : sc;
@@ -197,22 +191,125 @@ __device__ __forceinline__ Row4 quantise_fast(const float* y, bool* near) {
   return r;
 }
 
-// x r w / 2^k (r = rstd, or x / 2^k) in codes; the whole warp calls this.
-// Rows whose sums, weights or values leave the middle of fp32's range take the
-// 64 bits too, where no finite row's do.
+// Sums and products of fp32 with their rounding errors (Knuth, Dekker): the
+// result is x.h + x.l.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two add(const Two& a, const Two& b) {
+  const Two s = two_sum(a.h, b.h);
+  return two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ bool above(const Two& a, float b) { return a.h > b || (a.h == b && a.l > 0.f); }
+__device__ __forceinline__ bool is(const Two& a, float b) { return a.h == b && a.l == 0.f; }
+
+// The whole row from its inputs, two blocks at a time: in pairs of fp32, which
+// are 2^-43 off and say so (false) where that does not decide, or (WIDE) in 64
+// bits.  (In 64 bits alone, whose operations take this GPU some 100 clk each,
+// 13,045 rows took 35 us instead of 25, 41 with the loop rolled.)
+template <typename T, bool NORM, bool WIDE>
+__device__ __noinline__ bool quantise_exact(const T* x, const T* w, double eps, float unit, uint8_t* dst) {
+  const int lane = threadIdx.x & 31;
+  Two r = {1.f, 0.f};
+  double wide = 1;
+  static_assert(NORM || WIDE, "without a norm fp32 holds the values");
+  if constexpr (!WIDE) {
+    Two s = {0.f, 0.f};
+#pragma unroll 4
+    for (int i = lane; i < 512; i += 32) {
+      const float v = Elt<T>::to_f(x[i]);
+      s = add(s, Two{__fmul_rn(v, v), 0.f});   // the square of 11 bits is exact
+    }
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) s = add(s, Two{__shfl_xor_sync(~0u, s.h, o), __shfl_xor_sync(~0u, s.l, o)});
+    const float e = (float)eps;
+    s = add(Two{s.h * (1.f / 512.f), s.l * (1.f / 512.f)}, Two{e, (float)(eps - (double)e)});
+    // one step of Newton's from fp32's root: what 1 - s r^2 leaves, halved
+    r.h = 1.0f / sqrtf(s.h);
+    const float p = __fmul_rn(r.h, r.h), pl = fmaf(r.h, r.h, -p), q = __fmul_rn(s.h, p), ql = fmaf(s.h, p, -q);
+    const float rest = __fsub_rn(__fsub_rn(1.f, q), __fadd_rn(ql, fmaf(s.h, pl, __fmul_rn(s.l, p))));
+    r.l = 0.5f * r.h * rest;
+  } else if constexpr (NORM) {
+    double s = 0;
+#pragma unroll 1
+    for (int i = lane; i < 512; i += 32) {
+      const double v = Elt<T>::to_f(x[i]);
+      s = fma(v, v, s);
+    }
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    wide = rsqrt(s * (1.0 / 512.0) + eps);
+  }
+  bool sure = true;
+#pragma unroll(WIDE ? 1 : 4)
+  for (int i = 0; i < 16; ++i) {
+    const int e = 32 * i + lane;
+    Two a;
+    bool negative;
+    if constexpr (WIDE) {
+      double y = (double)Elt<T>::to_f(x[e]) * (double)unit;
+      if (NORM) y = y * wide * (double)Elt<T>::to_f(w[e]);
+      negative = y < 0;
+      y = fmin(fabs(y), 1e38);   // far past the largest scale
+      y = Elt<T>::to_f(x[e]) - Elt<T>::to_f(x[e]) == 0.f && (!NORM || Elt<T>::to_f(w[e]) - Elt<T>::to_f(w[e]) == 0.f) &&
+                  wide - wide == 0
+              ? y
+              : (double)INFINITY;
+      a.h = (float)y;
+      a.l = a.h < INFINITY ? (float)(y - (double)a.h) : 0.f;
+    } else {
+      const float c = __fmul_rn(Elt<T>::to_f(x[e]), Elt<T>::to_f(w[e])) * unit;   // exact
+      negative = c < 0.f;
+      a.h = __fmul_rn(fabsf(c), r.h);
+      a.l = fmaf(fabsf(c), r.h, -a.h) + fabsf(c) * r.l;
+      if (a.h < INFINITY) a = two_sum(a.h, a.l);
+    }
+    const bool bad = !(a.h < INFINITY);
+    Two top = bad ? Two{0.f, 0.f} : a;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+      const Two u = {__shfl_xor_sync(~0u, top.h, o), __shfl_xor_sync(~0u, top.l, o)};
+      if (u.h > top.h || (u.h == top.h && u.l > top.l)) top = u;
+    }
+    const bool none = (__ballot_sync(~0u, bad) >> (lane & 16)) & 0xffff;
+    float up, down;
+    const uint32_t b = next_scale(to_e4m3(fminf(top.h, 2688.f) * (1.f / 6.f)), [&](float x) { return above(top, x); },
+                                  [&](float x) { return is(top, x); }, &up, &down);
+    auto unsure = [&](const Two& v, float border) {
+      return !WIDE && v.h == border && border != 0.f && fabsf(v.l) <= v.h * (1.f / (1ull << 42));
+    };
+    sure &= !unsure(top, up) && !unsure(top, down);
+    const float s = e4m3_value(b);
+    uint32_t n = code_of(
+        s, [&](float x) { return sure &= none || !unsure(a, x), above(a, x); }, [&](float x) { return is(a, x); });
+    n = none ? 0 : n + (negative ? 8 : 0);
+    const uint32_t high = __shfl_xor_sync(~0u, n, 1);
+    if (!(lane & 1)) dst[16 * i + (lane >> 1)] = (uint8_t)(n | high << 4);
+    if (!(lane & 15)) dst[kCodes + 2 * i + (lane >> 4)] = none ? 0x7f : (uint8_t)b;
+  }
+  return __all_sync(~0u, sure);
+}
+
+// y = x r w / 2^k (r = rstd, or x / 2^k) into a row; the whole warp calls this
+// with the row in its lanes.  Rows whose sums, weights or values leave the middle
+// of fp32's range take the 64 bits too, where no finite row's do.
 constexpr float kLarge = 1.2676506e30f, kSmall = 1.f / kLarge;   // 2^100
 template <typename T, bool NORM>
-__device__ __forceinline__ Row4 quantise(const AppendArgs& a, const float* x, const T* w) {
+__device__ __forceinline__ void store_row4(const AppendArgs& a, int t, const float* x, uint8_t* dst) {
   const int lane = threadIdx.x & 31;
   const float unit = __uint_as_float((uint32_t)(127 - a.scale_exp) << 23);   // 2^-k
   float v[16];
   bool far = false;
   if constexpr (NORM) {
-    float g[16], s = 0.f;
-    load_row512(w, lane, g);
+    float g[16], sum[4] = {0.f, 0.f, 0.f, 0.f};
+    load_row512((const T*)a.kw, lane, g);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s = fmaf(x[i], x[i], s);
-    s = warp_sum(s) * (1.0f / 512.0f) + (float)a.eps;
+    for (int i = 0; i < 16; ++i) sum[i & 3] = fmaf(x[i], x[i], sum[i & 3]);
+    const float s = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3])) * (1.0f / 512.0f) + (float)a.eps;
     far = !(s > kSmall && s < kLarge);
     const float r = 1.0f / sqrtf(s);
 #pragma unroll
@@ -228,29 +325,23 @@ __device__ __forceinline__ Row4 quantise(const AppendArgs& a, const float* x, co
       far |= !(fabsf(x[i]) < kLarge);
     }
   }
-  bool near;
-  const Row4 fast = quantise_fast(v, &near);
+  bool near = false;
+  const Row4 q = quantise<!NORM>(v, &near);
   far = __any_sync(~0u, far);
-  if (!far && !__any_sync(~0u, near)) return fast;
-  if (!NORM && !far) return quantise_exact(v);   // v is exact, and so is every comparison in fp32
-  // (of normal rows about one in a hundred)
-  double y[16];
-  if constexpr (NORM) {
-    float g[16];
-    load_row512(w, lane, g);
-    double s = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s = fma((double)x[i], (double)x[i], s);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    const double r = 1.0 / sqrt(s * (1.0 / 512.0) + a.eps);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = (double)x[i] * r * (double)g[i] * (double)unit;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = (double)x[i] * (double)unit;
+  if (far || __any_sync(~0u, near)) {
+    const T* row = (const T*)a.k + (size_t)t * 512;
+    bool done = false;
+    if constexpr (NORM) done = !far && quantise_exact<T, true, false>(row, (const T*)a.kw, a.eps, unit, dst);
+    if (!done) quantise_exact<T, NORM, true>(row, (const T*)a.kw, a.eps, unit, dst);
+    return;
   }
-  return quantise_exact(y);
+  uint32_t* codes = reinterpret_cast<uint32_t*>(dst);
+  codes[lane] = q.code[0];
+  codes[lane + 32] = q.code[1];
+  if (!(lane & 1)) {
+    dst[kCodes + (lane >> 1)] = (uint8_t)q.scale[0];
+    dst[kCodes + 16 + (lane >> 1)] = (uint8_t)q.scale[1];
+  }
 }
 
 template <typename T, bool INTER, bool SLOTS, bool PACKED>
@@ -274,14 +365,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendArgs a) {
     T* dst_rope;
     if constexpr (PACKED) {
       uint8_t* dst = (uint8_t*)a.cache + (size_t)s.row * (kRopeAt + (a.pg.row - 512) * 2);
-      const Row4 q = a.kw ? quantise<T, true>(a, v, (const T*)a.kw) : quantise<T, false>(a, v, nullptr);
-      uint32_t* codes = reinterpret_cast<uint32_t*>(dst);
-      codes[lane] = q.code[0];
-      codes[lane + 32] = q.code[1];
-      if (!(lane & 1)) {
-        dst[kCodes + (lane >> 1)] = (uint8_t)q.scale[0];
-        dst[kCodes + 16 + (lane >> 1)] = (uint8_t)q.scale[1];
-      }
+      if (a.kw)
+        store_row4<T, true>(a, t, v, dst);
+      else
+        store_row4<T, false>(a, t, v, dst);
       dst_rope = reinterpret_cast<T*>(dst + kRopeAt);
     } else {
       T* dst = (T*)a.cache + (size_t)s.row * a.pg.row;

@@ -1,41 +1,64 @@
 // Values of a 4-bit cache in 16 bits (sfa_cache4_unpack), and of the pages
 // that a call's block tables name.
 //
-// Bound by HBM: a thread takes four bytes of codes to one 16-byte piece of a
-// row (or copies a piece of its rotated part), neighbouring threads
-// neighbouring pieces.
+// Bound by HBM: a warp takes four rows at once, a lane two 4-byte words of codes
+// of each to two 16-byte pieces (and eight lanes a piece of the rotated part),
+// so that reads and writes are whole lines and twelve loads are in flight a lane.
 #include "kernels.h"
 #include "cache4.cuh"
 
 namespace sfa {
 namespace {
 
-// Piece p of a row: 8 elements of the latent part, or of the rotated one.
-template <typename T>
-__device__ __forceinline__ uint4 piece_of(const uint8_t* row, int p, const Dec4<T>& dec) {
-  if (p >= 64) return __ldg(reinterpret_cast<const uint4*>(row + kRopeAt) + (p - 64));
-  uint32_t s[2];
-  dec.scales(__ldg(row + kCodes + (p >> 1)), s);
-  return dec.eight(__ldg(reinterpret_cast<const uint32_t*>(row) + p), s[0]);
+constexpr int kWarps = 8, kRowsAtOnce = 4;
+
+// Rows first .. first + n - 1 (n <= kRowsAtOnce) of `src` to `dst`, by one warp.
+template <typename T, bool ROPE>
+__device__ __forceinline__ void unpack_rows(const uint8_t* src, uint4* dst, int n, const Dec4<T>& dec) {
+  constexpr int kPieces = ROPE ? 72 : 64, kBytes = kRopeAt + (ROPE ? 128 : 0);
+  const int lane = threadIdx.x & 31;
+  uint32_t code[kRowsAtOnce][2], scale[kRowsAtOnce][2];
+  uint4 rope[kRowsAtOnce];
+#pragma unroll
+  for (int r = 0; r < kRowsAtOnce; ++r) {
+    if (r >= n) break;
+    const uint8_t* row = src + r * kBytes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      code[r][h] = __ldg(reinterpret_cast<const uint32_t*>(row) + lane + 32 * h);
+      scale[r][h] = __ldg(row + kCodes + (lane >> 1) + 16 * h);
+    }
+    if (ROPE && lane < 8) rope[r] = __ldg(reinterpret_cast<const uint4*>(row + kRopeAt) + lane);
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsAtOnce; ++r) {
+    if (r >= n) break;
+    uint4* to = dst + r * kPieces;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t s[2];
+      dec.scales(scale[r][h], s);
+      to[lane + 32 * h] = dec.eight(code[r][h], s[0]);
+    }
+    if (ROPE && lane < 8) to[64 + lane] = rope[r];
+  }
 }
 
 template <typename T, bool ROPE>
-__global__ void __launch_bounds__(256) unpack_kernel(const UnpackArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) unpack_kernel(const UnpackArgs a) {
   constexpr int kPieces = ROPE ? 72 : 64, kBytes = kRopeAt + (ROPE ? 128 : 0);
   const Dec4<T> dec(a.scale_exp);
-  const long long n = a.rows * kPieces;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const long long row = i / kPieces;
-    reinterpret_cast<uint4*>(a.out)[i] =
-        piece_of<T>((const uint8_t*)a.cache + row * kBytes, (int)(i - row * kPieces), dec);
-  }
+  const long long step = (long long)gridDim.x * kWarps * kRowsAtOnce;
+  for (long long r = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRowsAtOnce; r < a.rows; r += step)
+    unpack_rows<T, ROPE>((const uint8_t*)a.cache + r * kBytes, reinterpret_cast<uint4*>(a.out) + r * kPieces,
+                         (int)min((long long)kRowsAtOnce, a.rows - r), dec);
 }
 
 // Block table entry by entry (a block each): its page's values, as far as the
 // sequence reaches, and the entry of the table over them.  Pages that are
 // none stay none.
 template <typename T, bool ROPE>
-__global__ void __launch_bounds__(256) unpack_tables_kernel(const UnpackArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) unpack_tables_kernel(const UnpackArgs a) {
   constexpr int kPieces = ROPE ? 72 : 64, kBytes = kRopeAt + (ROPE ? 128 : 0);
   const Dec4<T> dec(a.scale_exp);
   const Paged& g = a.pg;
@@ -52,10 +75,8 @@ __global__ void __launch_bounds__(256) unpack_tables_kernel(const UnpackArgs a) 
     if (!ok) continue;
     const uint8_t* src = (const uint8_t*)a.cache + (size_t)id * g.page_size * kBytes;
     uint4* dst = reinterpret_cast<uint4*>(a.out) + (size_t)to * g.page_size * kPieces;
-    for (int i = threadIdx.x; i < rows * kPieces; i += 256) {
-      const int row = i / kPieces;
-      dst[i] = piece_of<T>(src + (size_t)row * kBytes, i - row * kPieces, dec);
-    }
+    for (int r = (threadIdx.x >> 5) * kRowsAtOnce; r < rows; r += kWarps * kRowsAtOnce)
+      unpack_rows<T, ROPE>(src + (size_t)r * kBytes, dst + (size_t)r * kPieces, min(kRowsAtOnce, rows - r), dec);
   }
 }
 
@@ -63,17 +84,16 @@ __global__ void __launch_bounds__(256) unpack_tables_kernel(const UnpackArgs a) 
 
 template <typename T>
 cudaError_t launch_unpack(const UnpackArgs& a, int nsm, cudaStream_t st) {
-  const bool rope = a.width == 576;
-  const long long blocks = (a.rows * (rope ? 72 : 64) + 255) / 256, most = (long long)nsm * 32;
-  auto kern = rope ? unpack_kernel<T, true> : unpack_kernel<T, false>;
-  kern<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(a);
+  const long long per = kWarps * kRowsAtOnce, blocks = (a.rows + per - 1) / per, most = (long long)nsm * 32;
+  auto kern = a.width == 576 ? unpack_kernel<T, true> : unpack_kernel<T, false>;
+  kern<<<(unsigned)(blocks < most ? blocks : most), 32 * kWarps, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
 cudaError_t launch_unpack_tables(const UnpackArgs& a, int nsm, cudaStream_t st) {
   const long long blocks = (long long)a.pg.B * a.pg.max_pages, most = (long long)nsm * 32;
   auto kern = a.width == 576 ? unpack_tables_kernel<T, true> : unpack_tables_kernel<T, false>;
-  kern<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(a);
+  kern<<<(unsigned)(blocks < most ? blocks : most), 32 * kWarps, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -143,9 +143,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
 
 cudaError_t launch_plan(const PlanArgs& a, int nsm, cudaStream_t st) {
   const int bytes = 3 * a.B * (int)sizeof(int);
-  const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             3 * kPlanRequests * (int)sizeof(int));
-  if (e != cudaSuccess) return e;
+  if (bytes > 40 * 1024) {   // beyond what a launch has without asking
+    const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               3 * kPlanRequests * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+  }
   const int want = (a.tokens + kThreads - 1) / kThreads;
   plan_kernel<<<want < 1 ? 1 : want < nsm ? want : nsm, kThreads, bytes, st>>>(a);
   return cudaGetLastError();
