@@ -22,16 +22,19 @@ constexpr int kWarps = 4;
 constexpr int kPieces = 8;
 
 // Where a new token goes and what turns it.
+template <bool INTER>
 struct Spot {
   bool ok;         // else: left out
   long long row;   // of the cache
-  Places at;
+  int pos;         // by table: the position
+  PairsAt<INTER> at;   // by slot: the pairs'
 };
 // The row follows from the token's position and its sequence's block table;
 // page = false: only the position is wanted.
-__device__ __forceinline__ Spot by_table(const AppendArgs& a, int t, bool page) {
+template <bool INTER>
+__device__ __forceinline__ Spot<INTER> by_table(const AppendArgs& a, int t, bool page) {
   const SeqTok s = find_token(a.pg, t);
-  Spot r{};
+  Spot<INTER> r{};
   if (s.seq < 0) {
     if (s.bad && a.error) *a.error = kErrSeqLens;
     return r;
@@ -46,7 +49,7 @@ __device__ __forceinline__ Spot by_table(const AppendArgs& a, int t, bool page) 
     if (a.error) *a.error = kErrPosition;
     return r;
   }
-  r.at.p[0] = (int)pos;
+  r.pos = (int)pos;
   if (page) {
     const int ps = a.pg.page_size;
     const int id = __ldg(a.pg.table + (size_t)s.seq * a.pg.max_pages + (int)pos / ps);
@@ -60,16 +63,17 @@ __device__ __forceinline__ Spot by_table(const AppendArgs& a, int t, bool page) 
   return r;
 }
 // The row stands in the slot map; a negative slot is a token of no sequence.
-__device__ __forceinline__ Spot by_slot(const AppendArgs& a, int t) {
-  Spot r{};
+template <bool INTER>
+__device__ __forceinline__ Spot<INTER> by_slot(const AppendArgs& a, int t) {
+  Spot<INTER> r{};
   const int slot = __ldg(a.slots + t);
-  if (a.cs) r.at = load_places(a.pos, t, a.pg.T, a.axes);
+  if (a.cs) r.at.load(a.pos, t, a.pg.T, a.axes, a.axis_map, a.table_len);
   if (slot < 0) return r;
   if (slot >= (long long)a.pg.num_pages * a.pg.page_size) {
     if (a.error) *a.error = kErrPage;
     return r;
   }
-  if (a.cs && outside(r.at, a.table_len)) {
+  if (a.cs && r.at.pad) {
     if (a.error) *a.error = kErrPosition;
     return r;
   }
@@ -78,11 +82,11 @@ __device__ __forceinline__ Spot by_slot(const AppendArgs& a, int t) {
   return r;
 }
 template <bool INTER, bool SLOTS>
-__device__ __forceinline__ void spot_angles(const AppendArgs& a, const Spot& s, int piece, Angles* ang) {
+__device__ __forceinline__ void spot_angles(const AppendArgs& a, const Spot<INTER>& s, int piece, Angles* ang) {
   if constexpr (SLOTS)
-    load_angles<INTER>(a.cs, s.at, a.axis_map, piece, ang);
+    s.at.angles(a.cs, a.axis_map, piece, ang);
   else
-    load_angles<INTER>(a.cs + (size_t)s.at.p[0] * 64, piece, ang);
+    load_angles<INTER>(a.cs + (size_t)s.pos * 64, piece, ang);
 }
 
 // ------------------------------------------------------------------ rows of 4 bits
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendArgs a) {
       unpack8<T>(w, rope);
     }
     if (!PACKED && a.kw) load_row512((const T*)a.kw, lane, g);
-    const Spot s = SLOTS ? by_slot(a, t) : by_table(a, t, true);
+    const Spot<INTER> s = SLOTS ? by_slot<INTER>(a, t) : by_table<INTER>(a, t, true);
     if (!s.ok) return;
     T* dst_rope;
     if constexpr (PACKED) {
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendArgs a) {
     w[j] = make_uint4(0, 0, 0, 0);
     if (lane + 32 * j < n) w[j] = (reinterpret_cast<const uint4*>(a.qr) + base)[lane + 32 * j];
   }
-  const Spot s = SLOTS ? by_slot(a, t) : by_table(a, t, false);
+  const Spot<INTER> s = SLOTS ? by_slot<INTER>(a, t) : by_table<INTER>(a, t, false);
   if (!s.ok) return;
   Angles ang;
   spot_angles<INTER, SLOTS>(a, s, lane & 7, &ang);

@@ -136,7 +136,7 @@ struct RowsArgs {
   float *q_rstd, *k_rstd;
   const void *dq, *dk;
   float *dqw, *dkw, *part;
-  int T, G, interleaved;
+  int T, G, interleaved, backward;
   float eps;
   int blocks_k, blocks_q;   // set by the launchers
 };

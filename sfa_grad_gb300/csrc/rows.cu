@@ -54,13 +54,12 @@ __device__ void norm_rows(const RowsArgs& a, const T* x, const T* w, T* y, float
 template <typename T, bool INTER, bool AXES>
 __device__ void rotate_rows(const RowsArgs& a, const T* x, T* y, int heads, int t, int h0, float sgn) {
   const int lane = threadIdx.x & 31;
-  Places at;
+  PairsAt<INTER> at;
   int pos = 0;
   bool pad;
   if constexpr (AXES) {
-    at = load_places(a.pos, t, a.T, a.axes);
-    pad = outside(at, a.table_len);
-    if (pad) at = Places{{0, 0, 0, 0}};
+    at.load(a.pos, t, a.T, a.axes, a.axis_map, a.table_len);
+    pad = at.pad;
   } else {
     pos = __ldg(a.pos + t);
     pad = pos < 0 || pos >= a.table_len;
@@ -77,7 +76,7 @@ __device__ void rotate_rows(const RowsArgs& a, const T* x, T* y, int heads, int 
   }
   Angles ang;
   if constexpr (AXES)
-    load_angles<INTER>(a.cs, at, a.axis_map, lane & 7, &ang);
+    at.angles(a.cs, a.axis_map, lane & 7, &ang);
   else
     load_angles<INTER>(a.cs + (size_t)(pad ? 0 : pos) * 64, lane & 7, &ang);
 #pragma unroll
@@ -118,7 +117,8 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(RowsArgs a) {
     return;
   }
   b -= a.blocks_q;
-  rotate_item<T, INTER, AXES>(a, (const T*)a.qr, (T*)a.qro, (const T*)a.kr, (T*)a.kro, (long long)b * kWarps + warp, 1.f);
+  rotate_item<T, INTER, AXES>(a, (const T*)a.qr, (T*)a.qro, (const T*)a.kr, (T*)a.kro, (long long)b * kWarps + warp,
+                              a.backward ? -1.f : 1.f);
 }
 
 // Gradient of rows of 512: warps of `nblk` blocks take rows in strides, keep
@@ -276,6 +276,11 @@ cudaError_t launch_norm_rope(RowsArgs a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_norm_rope_grad(RowsArgs a, int nsm, cudaStream_t st) {
+  if (!a.dk && !a.dq) {   // rotations alone: the forward's kernel, which leaves room for more warps
+    a.k = a.q = nullptr;
+    a.backward = 1;
+    return launch_norm_rope<T>(a, st);
+  }
   a.blocks_k = a.dk ? norm_grad_blocks(a.T, nsm) : 0;
   a.blocks_q = a.dq ? norm_grad_blocks((long long)a.T * a.G, nsm) : 0;
   const long long n = a.blocks_k + (long long)a.blocks_q + rope_blocks(a);

@@ -76,7 +76,7 @@ __device__ __forceinline__ void load_angles(const float* cs_row, int piece, Angl
   }
 }
 // Positions of a token on up to four axes; pair i turns by the one that bits
-// 2i, 2i + 1 of `map` name.  Axes that are not there repeat the first.
+// 2i, 2i + 1 of a `map` name.  Axes that are not there repeat the first.
 struct Places {
   int p[4];
 };
@@ -92,22 +92,53 @@ __device__ __forceinline__ bool outside(const Places& r, long long table_len) {
   for (int i = 0; i < 4; ++i) bad |= r.p[i] < 0 || r.p[i] >= table_len;
   return bad;
 }
-// As above with a position for each pair.
+// Where a token's pairs are turned to, on several axes, and the angles of a
+// piece; by a whole warp.  Interleaved, a lane reads its piece's four pairs.
+// Else a piece has eight: a lane reads its own pair's angle, and the pieces take
+// theirs from the lanes.  (Each the other way: 4096 tokens x 128 heads
+// interleaved 28.5 instead of 24 us, 16381 x 64 not interleaved 53 instead of 51,
+// the append of 13,045 rows of 4 bits with 16 heads 29 instead of 25.)
 template <bool INTER>
-__device__ __forceinline__ void load_angles(const float* cs, const Places& r, unsigned long long map, int piece,
-                                            Angles* a) {
-  constexpr int kPairs = INTER ? 4 : 8;
-  const int first = INTER ? piece * 4 : (piece & 3) * 8;
-  const uint32_t m = (uint32_t)(map >> (2 * first));
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const uint32_t axis = m >> (2 * i) & 3;
-    const int at = axis == 0 ? r.p[0] : axis == 1 ? r.p[1] : axis == 2 ? r.p[2] : r.p[3];
-    const float* row = cs + (size_t)at * 64 + first + i;
-    a->c[i] = __ldg(row);
-    a->s[i] = __ldg(row + 32);
+struct PairsAt {
+  Places all;
+  int own;
+  bool pad;   // outside the table on some axis
+  __device__ __forceinline__ void load(const int* pos, int t, int tokens, int axes, unsigned long long map,
+                                       long long table_len) {
+    if constexpr (INTER) {
+      all = load_places(pos, t, tokens, axes);
+      pad = outside(all, table_len);
+      if (pad) all = Places{{0, 0, 0, 0}};
+    } else {
+      const int lane = threadIdx.x & 31;
+      const int p = lane < axes ? __ldg(pos + (size_t)lane * tokens + t) : 0;
+      pad = __any_sync(~0u, p < 0 || p >= table_len);
+      own = __shfl_sync(~0u, p, (int)(map >> (2 * lane)) & 3);
+      if (pad) own = 0;
+    }
   }
-}
+  __device__ __forceinline__ void angles(const float* cs, unsigned long long map, int piece, Angles* a) const {
+    if constexpr (INTER) {
+      const uint32_t m = (uint32_t)(map >> (8 * piece));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t axis = m >> (2 * i) & 3;
+        const int at = axis == 0 ? all.p[0] : axis == 1 ? all.p[1] : axis == 2 ? all.p[2] : all.p[3];
+        const float* row = cs + (size_t)at * 64 + piece * 4 + i;
+        a->c[i] = __ldg(row);
+        a->s[i] = __ldg(row + 32);
+      }
+    } else {
+      const float* row = cs + (size_t)own * 64 + (threadIdx.x & 31);
+      const float c = __ldg(row), s = __ldg(row + 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a->c[i] = __shfl_sync(~0u, c, (piece & 3) * 8 + i);
+        a->s[i] = __shfl_sync(~0u, s, (piece & 3) * 8 + i);
+      }
+    }
+  }
+};
 // Rotates the lane's piece (lane % 8 = piece) by +angle, or by -angle
 // (sgn = -1).  Not interleaved, a pair's halves sit four lanes apart: every
 // lane of the warp calls this.
