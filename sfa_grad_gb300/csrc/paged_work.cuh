@@ -194,21 +194,26 @@ struct Work {
     // (added up in a loop, unrolled over the warps, they took 4400 clk, most of
     // it for fetching the code: this runs once a launch)
     static_assert(kWarps <= 32, "a lane a warp");
-    long long total, toks_all, tiles_all;
-    auto sum = [&](int which, long long* all) {
-      long long x = lane < kWarps ? scan[which * kWarps + lane] : 0;
+    long long x[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) x[i] = lane < kWarps ? scan[i * kWarps + lane] : 0;
 #pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(~0u, x, o);
-        if (lane >= o) x += y;
-      }
-      *all = __shfl_sync(~0u, x, 31);
-      const long long before = __shfl_sync(~0u, x, (w + 31) & 31);
-      return w ? before : 0;
-    };
-    u += sum(0, &total);
-    t += sum(1, &toks_all);
-    g += (int)sum(2, &tiles_all);
+    for (int o = 1; o < 32; o <<= 1) {
+      long long y[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) y[i] = __shfl_up_sync(~0u, x[i], o);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (lane >= o) x[i] += y[i];
+    }
+    long long all[3], ahead[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      all[i] = __shfl_sync(~0u, x[i], 31);
+      ahead[i] = __shfl_sync(~0u, x[i], (w + 31) & 31);
+    }
+    if (w) u += ahead[0], t += ahead[1], g += (int)ahead[2];
+    const long long total = all[0], toks_all = all[1], tiles_all = all[2];
     const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)workers * (INT32_MAX / 2);
     const int np = total < 1 ? 1 : total < workers ? (int)total : workers;
     const int own = total > workers ? kOwn : 0;

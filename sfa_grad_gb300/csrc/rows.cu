@@ -13,6 +13,8 @@
 // 5.9 TB/s; their gradients 32.4 us, 4.6 TB/s, with the second launch that adds
 // up the weight's; 16381 tokens x 16 normed heads, fp16, gradients: 166 us, 5.6
 // TB/s.
+#include <type_traits>
+
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -101,7 +103,7 @@ __device__ void rotate_item(const RowsArgs& a, const T* qr, T* qro, const T* kr,
   }
 }
 
-template <typename T, bool INTER, bool AXES>
+template <typename T, bool INTER, bool AXES, bool BACK>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(RowsArgs a) {
   const int warp = threadIdx.x >> 5;
   int b = blockIdx.x;
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(RowsArgs a) {
   }
   b -= a.blocks_q;
   rotate_item<T, INTER, AXES>(a, (const T*)a.qr, (T*)a.qro, (const T*)a.kr, (T*)a.kro, (long long)b * kWarps + warp,
-                              a.backward ? -1.f : 1.f);
+                              BACK ? -1.f : 1.f);
 }
 
 // Gradient of rows of 512: warps of `nblk` blocks take rows in strides, keep
@@ -268,8 +270,13 @@ cudaError_t launch_norm_rope(RowsArgs a, cudaStream_t st) {
   a.blocks_q = a.q ? (int)(((long long)a.T * a.G + kWarps - 1) / kWarps) : 0;
   const long long n = a.blocks_k + (long long)a.blocks_q + rope_blocks(a);
   if (n == 0) return cudaSuccess;
-  auto kern = a.axes > 1 ? (a.interleaved ? norm_rope_kernel<T, true, true> : norm_rope_kernel<T, false, true>)
-                         : (a.interleaved ? norm_rope_kernel<T, true, false> : norm_rope_kernel<T, false, false>);
+  auto pick = [&](auto back) {
+    constexpr bool B = decltype(back)::value;
+    return a.axes > 1
+               ? (a.interleaved ? norm_rope_kernel<T, true, true, B> : norm_rope_kernel<T, false, true, B>)
+               : (a.interleaved ? norm_rope_kernel<T, true, false, B> : norm_rope_kernel<T, false, false, B>);
+  };
+  auto kern = a.backward ? pick(std::true_type{}) : pick(std::false_type{});
   kern<<<(unsigned)n, kWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
 }
