@@ -1,12 +1,17 @@
 // Append of new tokens' latent rows to the paged cache, with the norm of the
-// latent part and the position rotation on the way (sfa_cache_append).
+// latent part and the position rotation on the way (sfa_cache_append), in 16 or
+// in 4 bits (sfa_cache4_append), by block tables or by a slot map
+// (sfa_cache_append_slots).
 //
 // One warp a token writes its 1152-byte row straight to its page; further
 // warps rotate the tokens' query rows, 32 heads each, so that a decoding step
 // has one launch ahead of its attention.  Bound by the rows' bytes, and with
 // few tokens by the latency of the lengths, the block table and the row, read
 // one after the other.  Measured, bf16: 64 single tokens x 128 heads 6.2 us;
-// 8 chunks, 13,045 tokens x 64 heads, 47.3 us, 5.2 TB/s.
+// 8 chunks, 13,045 tokens x 64 heads, 47.3 us, 5.2 TB/s.  Into 4 bits,
+// from cold caches, 13,045 tokens by slots with 16 heads 24.6 us, keys alone 22.5 (16
+// bits 15.3): a row close to a border takes its warp some 6 us, and a launch of
+// four waves waits for the last.
 #include <type_traits>
 
 #include "kernels.h"
@@ -99,7 +104,7 @@ __device__ __forceinline__ void spot_angles(const AppendArgs& a, const Spot<INTE
 // the one of eps, halved by the square root; root, reciprocal, two products; the
 // division by 6 or by the scale, two more; 12 in all, and one to look aside.
 // What is within 16 of them (2^-20) of a border is near: a scale of one normal row in
-// 800, a code of one in 400.
+// 1400, a code of one in 480.
 constexpr float kNear = 1.0f / (1 << 20);
 
 __device__ __forceinline__ uint32_t to_e4m3(float x) {   // one byte, to nearest, at most 448

@@ -27,9 +27,24 @@
 // x 128 heads, one token each, 262,000 keys, 98 us: there bound by the bytes
 // into shared memory, which keys and values pass separately.
 //
+// Rows of 4 bits, up to 512 of q a sequence: codes and scales come by TMA in units
+// of 128 keys x 256 features, warps unpack them into the ring's slots, and the
+// products are as above.  Keys and values are unpacked separately, each CTA its
+// own half: the half of the keys that S needs and the half of the features that
+// O needs share only a quarter of a tile, and it would have to stay in shared
+// memory until P is ready.  Bound by shared memory, which a slot crosses with
+// 49 to 53 KB (384 to 415 clk at 128 bytes a clk, where its MMAs take 256), and in bf16
+// by the unpacking beside it: 640 clk a slot, fp16 480.  64 sequences x 128 heads of
+// 1024 .. 8192 keys, bf16, 102 us (16 bits: 98, bound by the bytes into shared
+// memory); one of 131071 keys 61 us.  On the way there, 64 x 128 heads: bytes read by
+// global loads 187; staged by TMA 116; rotated parts a tile ahead in a place of their
+// own and conversions that take a register's bytes 103.  (Fetching a unit before
+// the one in hand is unpacked: no gain.)
+//
 // Warps of a CTA: 0..3, 5, 7 and 16 the TMA loads of one ring slot each, 4 the
 // MMAs (only in the pair's first CTA), 6 the walk over the work with the page
-// table and the query rows, 8..15 softmax and epilogue.
+// table and the query rows, 8..15 softmax and epilogue.  Rows of 4 bits: 5 the
+// loads of units, 7 those of rotated parts, 0..3 and 16..27 the unpacking.
 #include "cache4.cuh"
 #include "paged_work.cuh"
 
@@ -944,11 +959,18 @@ static int few_rows(const Paged& p, int nsm) {
 }
 
 // Rows of 4 bits that are unpacked on the way to the MMAs cost every row tile
-// its unpacking; unpacked ahead of the call, once.
+// its unpacking; unpacked ahead of the call, once, and then they pass HBM in 16
+// bits.  16 sequences of 4096 keys with 128 heads: 512 rows 109 us and 107 (bf16), 100 and 107
+// (fp16), 768 rows 144 and 133, 132 and 133, 128 rows 50 and 66; one sequence of 16384
+// keys with 1024 rows 66 and 70.  Unpacking ahead also takes a workspace.
 static bool many_rows4(const Paged& p) {
   return (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G > 512;
 }
 
+// Single CTAs for few rows, as for 16 bits, but whatever the tables hold: 128
+// sequences of 2048 .. 16384 keys with 16 heads 231 us, in pairs 310; one of 1000 keys 26
+// and 27.  (With 64 rows a tile of theirs 187 us for 64 sequences x 128 heads, where
+// pairs take 105.)
 static int few_rows4(const Paged& p) {
   return (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G <= 32 ? 32 : 0;
 }

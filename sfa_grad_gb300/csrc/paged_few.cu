@@ -25,11 +25,22 @@
 // keys 158 us, 4.8 TB/s: with eight slots the loads wait
 // for the products, a tile takes 3900 clk.
 //
+// Rows of 4 bits (R = 32): groups of 16 rows come as they are, by bulk copies, and
+// eight warps unpack them into the ring's panels, which both products read as
+// above.  What bounds this is shared memory: a tile of 64 keys is written twice
+// and read three times, 2440 clk at 128 bytes a clk, and takes 3100.  128 sequences x
+// 16 heads of 2048 .. 16384 keys 225 us (16 bits: 230, bound by HBM), one of 1000
+// keys 17.3 us.  (Bytes read by the unpacking warps themselves, by global
+// loads of rows 416 bytes apart: 254 us.  Eight slots and four groups, which
+// fill shared memory, 234 where seven and eight took 250.  Sixteen unpacking
+// warps, or tiles of 16 rows with a slot more: 2 %.)
+//
 // Work is split and merged as in paged.cu.
 //
 // Warps: 0..7 softmax, rescaling, epilogue, 8 the scores' MMAs, 15 the values',
 // 9 the walk with the page table and the query rows, 10..13 the loads of a
-// tile's slots, one each, 14 those of its rope panel.
+// tile's slots, one each, 14 those of its rope panel.  Rows of 4 bits: 10 the
+// copies of groups, 11..14 and 16..19 the unpacking.
 #include "cache4.cuh"
 #include "paged_work.cuh"
 
@@ -57,7 +68,9 @@ struct Few {
   // The tensor core rounds every step of a sum towards zero, by the sum so far.
   static constexpr int kSums = Q4 ? 4 : 1;
   static constexpr int kSlots = R == 32 && !Q4 ? 10 : 8;
-  static constexpr int kRaw = 4;                        // groups of packed rows on their way: a place each, so that a warp meets every phase of its own
+  // Groups of packed rows on their way: a multiple of a tile's four, so that a
+  // place belongs to the warps of one group, which meet every phase of it.
+  static constexpr int kRaw = 4;
   static constexpr uint32_t kRowBytes = kRopeAt + (ROPE ? 128 : 0);
   static constexpr uint32_t kQPanel = R * 128;
   static constexpr uint32_t kOffP = 9 * kQPanel;       // P^T: 64 keys x 64 rows
