@@ -550,8 +550,8 @@ typedef struct sfa_plan_params {
  *   slots, positions (tokens,): of the new tokens, request after request; -1
  *       behind the last.
  * Both act_seq arrays, with the table, are what sfa_cache_append and
- * sfa_paged_fwd (TND) take; slots what sfa_cache_append_slots takes.  The
- * outputs overlap no input.
+ * sfa_paged_fwd (TND) take; slots what sfa_cache_append_slots takes.  Nothing
+ * that is written overlaps anything else (SFA_ERR_PARAM_INVALID).
  * A step that does not fit changes nothing and gives act_seq_q_out 0,
  * act_seq_kv_out and free_count_out as they were and slots -1: lengths that
  * are negative or exceed the table, or new tokens that exceed `tokens`

@@ -421,6 +421,18 @@ sfa_status sfa_page_plan(const sfa_plan_params* p, int32_t* block_table, const i
   if (!words_aligned(block_table, act_seq_kv, new_tokens, free_pages, free_count, act_seq_q_out, act_seq_kv_out,
                      free_count_out, slots, positions, error))
     return SFA_ERR_PARAM_INVALID;
+  // blocks read the inputs while others write the outputs
+  struct {
+    const int32_t* at;
+    size_t n;
+  } const part[] = {{act_seq_q_out, (size_t)p->B}, {act_seq_kv_out, (size_t)p->B}, {free_count_out, 1},
+                    {slots, (size_t)p->tokens}, {positions, (size_t)p->tokens}, {error, error ? 1u : 0u},
+                    {block_table, (size_t)(p->B * p->max_pages)}, {free_pages, (size_t)p->num_pages},
+                    {act_seq_kv, (size_t)p->B}, {new_tokens, (size_t)p->B}, {free_count, 1}};
+  for (int i = 0; i < 8; ++i)   // (the last three are only read)
+    for (int k = i + 1; k < 11; ++k)
+      if (part[i].n && part[k].n && part[i].at < part[k].at + part[k].n && part[k].at < part[i].at + part[i].n)
+        return SFA_ERR_PARAM_INVALID;
   PlanArgs a{block_table, act_seq_kv, new_tokens, free_pages, free_count, act_seq_q_out, act_seq_kv_out, free_count_out,
              slots, positions, error, (int)p->B, (int)p->max_pages, (int)p->num_pages, (int)p->page_size,
              (int)p->tokens};

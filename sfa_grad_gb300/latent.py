@@ -450,7 +450,7 @@ def page_plan(block_table, act_seq_kv, new_tokens, free_pages, free_count, *, pa
     Returns (act_seq_q, act_seq_kv, free_count, slots, positions): the new
     tokens and lengths of the step, what is left, and the row of the cache and
     position of each new token, `tokens` of them (-1 behind the last).
-    `outputs`: such a tuple to write into, overlapping no input.  `error`:
+    `outputs`: such a tuple to write into, none of them an input.  `error`:
     optional int32 (1,) that receives a SFA_DEVERR_* code; a step that does not
     fit changes nothing."""
     if block_table.dim() != 2 or free_pages.dim() != 1:

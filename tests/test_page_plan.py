@@ -178,21 +178,31 @@ def test_captured_step():
 
 def test_refusals():
     from sfa_grad_gb300.latent import PlanParams, _lib
-    L, f, odd = _lib(), ctypes.c_void_p(256), ctypes.c_void_p(258)
+    L, f = _lib(), ctypes.c_void_p(256)
     good = dict(B=3, max_pages=4, num_pages=12, page_size=16, tokens=5)
     for over in (dict(B=0), dict(B=8193), dict(max_pages=0), dict(max_pages=2 ** 30), dict(num_pages=0), dict(num_pages=2 ** 30),
                  dict(page_size=8), dict(page_size=24), dict(page_size=2048), dict(tokens=-1), dict(tokens=2 ** 31)):
         p = PlanParams(**{**good, **over})
         assert L.sfa_page_plan(ctypes.byref(p), *[f] * 11, None) == sfa.SFA_ERR_SHAPE, over
     p = ctypes.byref(PlanParams(**good))
+    v = lambda x: ctypes.c_void_p(x)  # noqa: E731
+    apart = [v(4096 * (k + 1)) for k in range(11)]
+    # table, kv, new, free, count; q, kv, count, slots, positions, error: what is written overlaps nothing
+    for i, k in ((5, 1), (6, 1), (7, 4), (8, 9), (5, 6), (10, 7), (9, 3), (8, 0), (0, 3), (6, 2), (10, 4), (0, 1), (3, 4)):
+        a = list(apart)
+        a[i] = v(a[k].value)
+        assert L.sfa_page_plan(p, *a, None) == sfa.SFA_ERR_PARAM_INVALID, (i, k)
+    a = list(apart)
+    a[6] = v(a[1].value + 8)         # the last of three lengths
+    assert L.sfa_page_plan(p, *a, None) == sfa.SFA_ERR_PARAM_INVALID
     assert L.sfa_page_plan(None, *[f] * 11, None) == sfa.SFA_ERR_NULLPTR
     for i in range(10):
-        a = [f] * 11
+        a = list(apart)
         a[i] = None
         assert L.sfa_page_plan(p, *a, None) == sfa.SFA_ERR_NULLPTR, i
     for i in range(11):
-        a = [f] * 11
-        a[i] = odd
+        a = list(apart)
+        a[i] = v(a[i].value + 2)
         assert L.sfa_page_plan(p, *a, None) == sfa.SFA_ERR_PARAM_INVALID, i
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     with pytest.raises(ValueError, match="act_seq_kv"):
