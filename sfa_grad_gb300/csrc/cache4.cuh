@@ -37,20 +37,23 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   memcpy(&a, &x, 4);
   return a;
 }
-// A pair of fp16 in T.
+// Products of two pairs of fp16, in T.
 template <typename T>
-__device__ __forceinline__ uint32_t to_pair(uint32_t h) {
-  if constexpr (Elt<T>::is_f16) return h;
-  __half2 x;
-  memcpy(&x, &h, 4);
-  const float2 f = __half22float2(x);
-  return Elt<T>::pack(f.x, f.y);
+__device__ __forceinline__ uint32_t product(uint32_t a, uint32_t b) {
+  if constexpr (Elt<T>::is_f16) return mul2(a, b);
+  float x, y;
+  asm("{\n.reg .b16 a0, a1, b0, b1;\nmov.b32 {a0, a1}, %2;\nmov.b32 {b0, b1}, %3;\n"
+      "fma.rn.f32.f16 %0, a0, b0, 0f80000000;\nfma.rn.f32.f16 %1, a1, b1, 0f80000000;\n}"
+      : "=f"(x), "=f"(y)
+      : "r"(a), "r"(b));
+  return Elt<T>::pack(x, y);
 }
 
-// Values are formed in fp16, where every product of the unit's range is exact;
-// bf16 takes them from there, exactly too.  (8 warps, 32 elements a lane: 104
-// clk in fp16, 216 in bf16; 293 with exponents moved by shifts and masks, 268
-// with codes shifted into place, 354 looked up by byte permutations.)
+// Codes and scales have conversions to fp16 alone, and every product of the unit's
+// range is exact there; for bf16 the products are formed in fp32 and packed,
+// exactly too.  (8 warps, 32 elements a lane: 104 clk in fp16, 203 in bf16; 216
+// from products in fp16, 293 with exponents moved by shifts and masks, 268 with
+// codes shifted into place, 354 looked up by byte permutations.)
 template <typename T>
 struct Dec4 {
   uint32_t unit;   // 2^k, twice (normal: k >= -14)
@@ -65,8 +68,7 @@ struct Dec4 {
   __device__ __forceinline__ uint4 eight(uint32_t w, uint32_t s) const {
     uint32_t h[4];
     e2m1_f16(w, h);
-    return make_uint4(to_pair<T>(mul2(h[0], s)), to_pair<T>(mul2(h[1], s)), to_pair<T>(mul2(h[2], s)),
-                      to_pair<T>(mul2(h[3], s)));
+    return make_uint4(product<T>(h[0], s), product<T>(h[1], s), product<T>(h[2], s), product<T>(h[3], s));
   }
 };
 

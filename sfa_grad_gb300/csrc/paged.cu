@@ -34,8 +34,8 @@
 // O needs share only a quarter of a tile, and it would have to stay in shared
 // memory until P is ready.  Bound by shared memory, which a slot crosses with
 // 49 to 53 KB (384 to 415 clk at 128 bytes a clk, where its MMAs take 256), and in bf16
-// by the unpacking beside it: 640 clk a slot, fp16 480.  64 sequences x 128 heads of
-// 1024 .. 8192 keys, bf16, 102 us (16 bits: 98, bound by the bytes into shared
+// by the unpacking beside it: 630 clk a slot, fp16 480.  64 sequences x 128 heads of
+// 1024 .. 8192 keys, bf16, 100 us (16 bits: 98, bound by the bytes into shared
 // memory); one of 131071 keys 61 us.  On the way there, 64 x 128 heads: bytes read by
 // global loads 187; staged by TMA 116; rotated parts a tile ahead in a place of their
 // own and conversions that take a register's bytes 103.  (Fetching a unit before

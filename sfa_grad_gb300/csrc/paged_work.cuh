@@ -190,30 +190,41 @@ struct Work {
     }
     if (lane == 31) scan[w] = u, scan[kWarps + w] = t, scan[2 * kWarps + w] = g;
     const bool any = __syncthreads_or(bad);
-    // the warps' sums, one a lane: what lies before this warp, and all of them
-    // (added up in a loop, unrolled over the warps, they took 4400 clk, most of
-    // it for fetching the code: this runs once a launch)
-    static_assert(kWarps <= 32, "a lane a warp");
-    long long x[3];
+    long long total = 0, toks_all = 0, tiles_all = 0;
+    if constexpr (kWarps <= 17) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) x[i] = lane < kWarps ? scan[i * kWarps + lane] : 0;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < w) u += scan[i], t += scan[kWarps + i], g += (int)scan[2 * kWarps + i];
+        total += scan[i];
+        toks_all += scan[kWarps + i];
+        tiles_all += scan[2 * kWarps + i];
+      }
+    } else {
+      // More warps (rows of 4 bits): their sums one a lane.  As above the 20 warps of
+      // single CTAs took 4400 clk, most of it for fetching the code, which runs
+      // once a launch (one sequence of 1000 keys 25 us instead of 21); the 16
+      // and 17 of the 16-bit kernels lose nothing by it.
+      static_assert(kWarps <= 32, "a lane a warp");
+      long long x[3], all[3], ahead[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) x[i] = lane < kWarps ? scan[i * kWarps + lane] : 0;
 #pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      long long y[3];
+      for (int o = 1; o < 32; o <<= 1) {
+        long long y[3];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) y[i] = __shfl_up_sync(~0u, x[i], o);
+        for (int i = 0; i < 3; ++i) y[i] = __shfl_up_sync(~0u, x[i], o);
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (lane >= o) x[i] += y[i];
+        for (int i = 0; i < 3; ++i)
+          if (lane >= o) x[i] += y[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        all[i] = __shfl_sync(~0u, x[i], 31);
+        ahead[i] = __shfl_sync(~0u, x[i], (w + 31) & 31);
+      }
+      if (w) u += ahead[0], t += ahead[1], g += (int)ahead[2];
+      total = all[0], toks_all = all[1], tiles_all = all[2];
     }
-    long long all[3], ahead[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      all[i] = __shfl_sync(~0u, x[i], 31);
-      ahead[i] = __shfl_sync(~0u, x[i], (w + 31) & 31);
-    }
-    if (w) u += ahead[0], t += ahead[1], g += (int)ahead[2];
-    const long long total = all[0], toks_all = all[1], tiles_all = all[2];
     const bool wrong = any || (p.tnd && toks_all > p.T) || total > (long long)workers * (INT32_MAX / 2);
     const int np = total < 1 ? 1 : total < workers ? (int)total : workers;
     const int own = total > workers ? kOwn : 0;
@@ -229,7 +240,7 @@ struct Work {
       c->ntiles = 0;
       if (last == cost) c->end_seq[1] = -1, c->end_units[1] = total;
     }
-#pragma unroll 1
+#pragma unroll(kWarps <= 17 ? 2 : 1)
     for (int e = 0; e < 2; ++e) {
       const long long at = e ? last : first;
       if (!mine || at < from || at >= to) continue;
