@@ -23,6 +23,11 @@ __device__ __forceinline__ void e2m1_f16(uint32_t w, uint32_t* h) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
 // Two scales as fp16.
 __device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
   uint32_t r;

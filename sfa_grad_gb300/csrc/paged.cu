@@ -144,11 +144,6 @@ __device__ __forceinline__ int load_from(uint32_t cluster_addr) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
 // ------------------------------------------------------------------ tensor cores, both SMs of the pair
 // The MMA warp runs as a whole and one elected lane issues: descriptors then
 // stay in uniform registers.  Four MMAs of N = 256 from a single-lane branch
@@ -455,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<Q4>, 1)
     auto fetch = [&](int n) {
       const int m = (n >> 1) - 1, end = 2 * (ntiles - 1);
       const bool values = m >= 0 && ((m & 1) || m == end);
-      const int t = m == end ? ntiles - 1 : m >> 1;   // of values
+      const int t = max(m >> 1, 0);   // of values
       const uint32_t src = units + (n % kUnits) * kUnit;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

@@ -54,7 +54,9 @@ constexpr int kSegs = 4;                    // work descriptors in flight
 constexpr int kTiles = 8;                   // tiles whose cache rows are known in advance
 constexpr int kMaxSlots = 10;
 constexpr int kGroup = 16;                  // rows of 4 bits that arrive together: never of two pages
-constexpr int kMaxRaw = 8;
+// Groups on their way: a multiple of a tile's four, so that a place belongs to
+// the warps of one group, which meet every phase of it.
+constexpr int kRaw = 4;
 constexpr uint32_t kPanel = 8192;           // 64 rows of 128 bytes
 constexpr uint32_t kSlot = 2 * kPanel;
 constexpr uint32_t kColS = 256;             // tensor memory: O^T, 64 columns a block of 128 features, then two S^T
@@ -68,9 +70,6 @@ struct Few {
   // The tensor core rounds every step of a sum towards zero, by the sum so far.
   static constexpr int kSums = Q4 ? 4 : 1;
   static constexpr int kSlots = R == 32 && !Q4 ? 10 : 8;
-  // Groups of packed rows on their way: a multiple of a tile's four, so that a
-  // place belongs to the warps of one group, which meet every phase of it.
-  static constexpr int kRaw = 4;
   static constexpr uint32_t kRowBytes = kRopeAt + (ROPE ? 128 : 0);
   static constexpr uint32_t kQPanel = R * 128;
   static constexpr uint32_t kOffP = 9 * kQPanel;       // P^T: 64 keys x 64 rows
@@ -85,7 +84,7 @@ struct Ctl {
   uint64_t full[kMaxSlots], empty[kMaxSlots], rfull[2], rempty[2];
   uint64_t qfull, qempty, sfull[2], sfree[2], pready, pfree, ofree;
   uint64_t xch, fch, settle[2];
-  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t tile_full[kTiles], tile_empty[kTiles];
   uint64_t flags[2];                        // a byte a softmax warp: some row's max rises
@@ -95,7 +94,7 @@ struct Ctl {
   Seg seg[kSegs];
   int y[kTiles][4];                         // cache row of each box of a tile
   int loads[kMaxSlots], rloads[2];          // uses of a slot (4 bits: of a group's place) that have been issued
-  int none[kMaxRaw];                        // a group without a page: zeros
+  int none[kRaw];                        // a group without a page: zeros
   alignas(16) float rbuf[64];               // a row's reference, times log2
   float fbuf[64];                           // ... and its factor for O
 };
@@ -181,11 +180,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
 
 template <typename T, bool ROPE, int R, bool Q4>
 __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
@@ -237,7 +231,7 @@ __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
       mbar_init(&c->empty[lane], 1);
     }
     if (lane < kMaxSlots) c->loads[lane] = 0;
-    if (Q4 && lane < F::kRaw) mbar_init(&c->raw_full[lane], 1), mbar_init(&c->raw_empty[lane], kDecode / 4);
+    if (Q4 && lane < kRaw) mbar_init(&c->raw_full[lane], 1), mbar_init(&c->raw_empty[lane], kDecode / 4);
     mbar_fence_init();
   } else if (warp == 2 && lane < (Q4 ? 2 : 4)) {
     const CUtensorMap* m = lane == 0 ? &maps.q : lane == 1 ? &maps.qr : lane == 2 ? &maps.c2 : &maps.c1;
@@ -338,7 +332,7 @@ __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
       if (lane == 0) mbar_arrive(&c->tile_empty[i]);
       bool ok = true;
       for (int g = 0; g < 4 && ok; ++g) {
-        const int u = 4 * t + g, s = u % F::kRaw, use = u / F::kRaw;
+        const int u = 4 * t + g, s = u % kRaw, use = u / kRaw;
         if (use > 0 && !(ok = warp_wait(&c->raw_empty[s], (use - 1) & 1, w))) break;
         if (lane == g) {
           c->none[s] = y == none;
@@ -369,8 +363,8 @@ __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
     int s = 0, ph = 1;   // ring slot, and the phase of its release (the first use waits for none)
     bool ok = true;
     for (int t = 0; t < ntiles && ok; ++t) {
-      const int u = 4 * t + g, rs = u % F::kRaw;
-      if (!(ok = warp_wait(&c->raw_full[rs], (u / F::kRaw) & 1, w))) break;
+      const int u = 4 * t + g, rs = u % kRaw;
+      if (!(ok = warp_wait(&c->raw_full[rs], (u / kRaw) & 1, w))) break;
       const uint32_t src = smem_u32(sm) + F::kOffRaw + (rs * kGroup + key) * F::kRowBytes;
       uint4 code[4], rope4[2];
       uint32_t two[4];
@@ -765,7 +759,7 @@ __global__ void __launch_bounds__((Few<R, Q4, ROPE>::kThreads), 1)
   __syncthreads();
   tc_fence_after();
   if (Q4) {
-    if (c->abort && tid < F::kRaw && c->loads[tid] > 0) mbar_settle(&c->raw_full[tid], (c->loads[tid] - 1) & 1, status);
+    if (c->abort && tid < kRaw && c->loads[tid] > 0) mbar_settle(&c->raw_full[tid], (c->loads[tid] - 1) & 1, status);
   } else if (c->abort && tid < kSlots + 2) {   // copies on their way, where some warp gave up
     const int s = tid < kSlots ? tid : tid - kSlots, n = tid < kSlots ? c->loads[s] : c->rloads[s];
     if (n > 0) mbar_settle(tid < kSlots ? &c->full[s] : &c->rfull[s], (n - 1) & 1, status);
