@@ -98,7 +98,7 @@ __device__ __forceinline__ void spot_angles(const AppendArgs& a, const Spot<INTE
 // y / 2^k in blocks of 16: the scale is max|y| / 6 in e4m3, a code the value
 // nearest to y / scale, ties to even, both of the exact y: a value that fp32's
 // roundings could carry over a border between two codes or two scales is
-// found, and its row is quantised again from y in 64 bits.
+// found, and its row is quantised again from its inputs, in more bits.
 //
 // Roundings of fp32 on the way, 2^-24 each: 4 + 2 + 5 additions of squares and
 // the one of eps, halved by the square root; root, reciprocal, two products; the
@@ -305,8 +305,11 @@ __device__ __noinline__ bool quantise_exact(const T* x, const T* w, double eps, 
 
 // y = x r w / 2^k (r = rstd, or x / 2^k) into a row; the whole warp calls this
 // with the row in its lanes.  Rows whose sums, weights or values leave the middle
-// of fp32's range take the 64 bits too, where no finite row's do.
+// of fp32's range take the 64 bits too, where no finite row's do.  (A square root
+// of 512 sums below 2^100 times a weight below 2^60 leaves products with weights,
+// which come before the factor r, below 2^119.)
 constexpr float kLarge = 1.2676506e30f, kSmall = 1.f / kLarge;   // 2^100
+constexpr float kLargeWeight = 1.1529215e18f;                    // 2^60
 template <typename T, bool NORM>
 __device__ __forceinline__ void store_row4(const AppendArgs& a, int t, const float* x, uint8_t* dst) {
   const int lane = threadIdx.x & 31;
@@ -324,7 +327,7 @@ __device__ __forceinline__ void store_row4(const AppendArgs& a, int t, const flo
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float h = g[i] * unit;
-      far |= !(fabsf(h) < kLarge);
+      far |= !(fabsf(h) < kLargeWeight);
       v[i] = x[i] * r * h;
     }
   } else {

@@ -217,6 +217,25 @@ def test_append_norm_at_the_ends_of_the_range(eps):
 
 
 @pytest.mark.gpu
+def test_append_with_weights_of_any_size():
+    """Large weights beside ordinary ones, rows of large values: whichever way a row is rounded, its large
+    elements are cut off at the largest value."""
+    t, n = torch.bfloat16, 12000
+    g = torch.Generator().manual_seed(21)
+    k = (torch.randn(n, 1, 512, generator=g) * torch.exp2(torch.randint(-40, 45, (n, 1, 1), generator=g).float())).to(t)
+    w = 1 + 0.2 * torch.randn(512, generator=g)
+    w[::32] *= torch.exp2(torch.randint(-90, 95, (16,), generator=g).float())
+    w[256] = 2.0 ** 58
+    w = w.to(t)
+    cache = torch.zeros(n // 16, 16, 288, dtype=torch.uint8, device="cuda")
+    sfa.cache_append_slots(cache, torch.arange(n, dtype=torch.int32, device="cuda"), None, k.cuda(), k_weight=w.cuda(), eps=EPS)
+    _same(cache.flatten(0, 1), _exact_rows(k[:, 0], w, 1.0))
+    w = w.clamp(-2.0 ** 59, 2.0 ** 59)
+    sfa.cache_append_slots(cache, torch.arange(n, dtype=torch.int32, device="cuda"), None, k.cuda(), k_weight=w.cuda(), eps=EPS)
+    _same(cache.flatten(0, 1), _exact_rows(k[:, 0], w, 1.0))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("packed", [True, False])
 @pytest.mark.parametrize("interleaved", [True, False])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
