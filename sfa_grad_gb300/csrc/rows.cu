@@ -32,18 +32,19 @@ constexpr int kGradBlocks = 3;
 // of 4096 x 128 heads took 41 us with two, 37 with four, 32 with eight.
 constexpr int kPieces = 8;
 
+template <bool AXES>
 __device__ __forceinline__ bool padded(const RowsArgs& a, int t) {
   if (!a.pos) return false;
-  if (a.axes > 1) return outside(load_places(a.pos, t, a.T, a.axes), a.table_len);
+  if constexpr (AXES) return outside(load_places(a.pos, t, a.T, a.axes), a.table_len);
   const int p = __ldg(a.pos + t);
   return p < 0 || p >= a.table_len;
 }
 
 // Rows of 512: x -> x r w, one warp a row.
-template <typename T>
+template <typename T, bool AXES>
 __device__ void norm_rows(const RowsArgs& a, const T* x, const T* w, T* y, float* rstd, int heads, long long row) {
   const int lane = threadIdx.x & 31;
-  const bool pad = padded(a, (int)(row / heads));
+  const bool pad = padded<AXES>(a, (int)(row / heads));
   float v[16], g[16];
   load_row512(x + row * 512, lane, v);
   load_row512(w, lane, g);
@@ -111,13 +112,13 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(RowsArgs a) {
   int b = blockIdx.x;
   if (b < a.blocks_k) {
     const long long row = (long long)b * kWarps + warp;
-    if (row < a.T) norm_rows<T>(a, (const T*)a.k, (const T*)a.kw, (T*)a.ko, a.k_rstd, 1, row);
+    if (row < a.T) norm_rows<T, AXES>(a, (const T*)a.k, (const T*)a.kw, (T*)a.ko, a.k_rstd, 1, row);
     return;
   }
   b -= a.blocks_k;
   if (b < a.blocks_q) {
     const long long row = (long long)b * kWarps + warp;
-    if (row < (long long)a.T * a.G) norm_rows<T>(a, (const T*)a.q, (const T*)a.qw, (T*)a.qo, a.q_rstd, a.G, row);
+    if (row < (long long)a.T * a.G) norm_rows<T, AXES>(a, (const T*)a.q, (const T*)a.qw, (T*)a.qo, a.q_rstd, a.G, row);
     return;
   }
   b -= a.blocks_q;
