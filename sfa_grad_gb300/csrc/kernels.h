@@ -170,16 +170,17 @@ struct AppendArgs {
 template <typename T>
 cudaError_t launch_append(AppendArgs a, cudaStream_t st);
 
-// Values of a 4-bit cache (cache4.cu): all of it, rows in order, or (b not 0)
-// the pages that the block tables of pg name, with tables of their own.
+// Values of a 4-bit cache (cache4.cu): all of it, rows in order
+// (launch_unpack), or the pages that the block tables of pg name
+// (launch_unpack_tables).
 struct UnpackArgs {
   const void* cache;
   void* out;
   long long rows;        // all of it: num_pages * page_size
   int width, scale_exp;  // elements of a row: 512 or 576
   Paged pg;              // the tables' form
-  int* table;            // tables of `out`
-  int by_page;           // out's pages are the cache's
+  int by_page;           // out's pages lie as the cache's do; else one for each entry of the tables
+  int* table;            // by page: rows taken of each page (num_pages); else the tables of `out`
 };
 template <typename T>
 cudaError_t launch_unpack(const UnpackArgs& a, int nsm, cudaStream_t st);

@@ -970,8 +970,10 @@ static int few_rows4(const Paged& p) {
   return (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G <= 32 ? 32 : 0;
 }
 
-// Where a packed cache's values go: tables, then pages.  Pages shared by
-// sequences are unpacked once where the cache has fewer than the tables name.
+// Where a packed cache's values go: tables, then pages.  Where the cache has no
+// more pages than the tables have entries, a page as it lies in the cache (pages
+// shared by sequences then are unpacked once, and the tables' place counts
+// their rows); else a page for each entry.
 static bool by_page(const Paged& p) { return p.num_pages <= (long long)p.B * p.max_pages; }
 static size_t table_bytes(const Paged& p) { return up256((size_t)p.B * p.max_pages * sizeof(int)); }
 
@@ -996,8 +998,10 @@ static cudaError_t launch_unpacked(PagedArgs a, int nsm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.packed = 0;
   a.cache = u.out;
-  a.pg.table = u.table;
-  if (!u.by_page) a.pg.num_pages = a.pg.B * a.pg.max_pages;
+  if (!u.by_page) {
+    a.pg.table = u.table;
+    a.pg.num_pages = a.pg.B * a.pg.max_pages;
+  }
   return launch_paged<T>(a, nsm, st);
 }
 
