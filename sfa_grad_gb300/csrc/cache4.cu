@@ -56,13 +56,14 @@ __global__ void __launch_bounds__(32 * kWarps) unpack_kernel(const UnpackArgs a)
 }
 
 // Block table entry by entry (a block each): its page's values, as far as the
-// sequence reaches.  By page, they go where the page lies in the cache, so that
-// the caller's table serves, and a page that several entries name is unpacked
-// once: an entry takes the rows beyond those that others have taken (64 sequences
-// of one token x 128 heads over one history of 16384 rows: 337 us, 64 times the
-// same rows; so 223, where the call over 16-bit rows takes 192).  Else every
-// entry has a page of its own and an entry in a table over them, where pages
-// that are none stay none.
+// sequence reaches; none of a sequence without query rows, which nobody reads.
+// By page, they go where the page lies in the cache, so that the caller's table
+// serves, and a page that several entries name is unpacked once: an entry takes
+// the rows beyond those that others have taken (64 sequences of one token x 128
+// heads over one history of 16384 rows: 337 us, 64 times the same rows; so 223,
+// where the call over 16-bit rows takes 192).  Else every entry has a page of
+// its own and an entry in a table over them, where pages that are none stay
+// none.
 template <typename T, bool ROPE>
 __global__ void __launch_bounds__(32 * kWarps) unpack_tables_kernel(const UnpackArgs a) {
   constexpr int kPieces = ROPE ? 72 : 64, kBytes = kRopeAt + (ROPE ? 128 : 0);
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(32 * kWarps) unpack_tables_kernel(const Unpack
     const int b = (int)(e / g.max_pages), j = (int)(e - (long long)b * g.max_pages);
     const long long kv = min((long long)__ldg(g.act_kv + b), (long long)g.max_pages * g.page_size);
     const int rows = (int)max(0LL, min((long long)g.page_size, kv - (long long)j * g.page_size));
-    if (!rows) continue;
+    if (!rows || (g.act_q && __ldg(g.act_q + b) <= 0)) continue;
     const int id = __ldg(g.table + e);
     const bool ok = id >= 0 && id < g.num_pages;
     if (!a.by_page && threadIdx.x == 0) a.table[e] = ok ? (int)e : -1;

@@ -29,6 +29,25 @@ def _both(x, dtype, heads, layout="TND", **kw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["TND", "BSND"])
+@pytest.mark.parametrize("spare", [2, 600])
+def test_sequences_without_query_rows_stay_packed(spare, layout):
+    """One sequence of eight has new tokens: the others' rows are read by nobody, and not unpacked (with 600
+    spare pages by table, else by page)."""
+    qlens, kvlens, heads = [0] * 8, [3000] * 8, 8
+    qlens[5], kvlens[5] = 600, 700
+    x = packed_inputs(qlens, kvlens, heads, "bf16", layout=layout, s1=600, spare=spare, seed=4)
+    got, want, left = _both(x, "bf16", heads, layout)
+    rows = (slice(None),) if layout == "TND" else (5,)
+    assert torch.equal(got[0][rows], want[0][rows])
+    assert torch.equal(got[1], want[1]) or layout == "BSND"
+    # 11 pages of 64 rows of 1152 bytes, and an entry of 4 bytes for each page of tables and cache; a page
+    # more for what else may lie there
+    entries = x["block_table"].numel() + x["cache"].shape[0]
+    assert int((left != FILL).sum()) <= 12 * 64 * 1152 + 4 * entries
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,rope", [("bf16", True), ("fp16", False)])
 @pytest.mark.parametrize("page", [16, 48, 256])
 def test_shared_pages_of_different_lengths(page, dtype, rope):
