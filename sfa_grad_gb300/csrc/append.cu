@@ -98,7 +98,9 @@ __device__ __forceinline__ void spot_angles(const AppendArgs& a, const Spot<INTE
 // y / 2^k in blocks of 16: the scale is max|y| / 6 in e4m3, a code the value
 // nearest to y / scale, ties to even, both of the exact y: a value that fp32's
 // roundings could carry over a border between two codes or two scales is
-// found, and its row is quantised again from its inputs, in more bits.
+// found, and its row is quantised again from its inputs, in more bits.  A code
+// takes y's sign, zeros' too (as the conversion does it), so that a row's bytes
+// do not depend on the way it took.
 //
 // Roundings of fp32 on the way, 2^-24 each: 4 + 2 + 5 additions of squares and
 // the one of eps, halved by the square root; root, reciprocal, two products; the
@@ -178,7 +180,7 @@ __device__ __forceinline__ Row4 quantise(const float* y, bool* near) {
       for (int i = 0; i < 8; ++i) {
         const float a = fabsf(v[i]);
         const uint32_t n = code_of(s, [&](float b) { return a > b; }, [&](float b) { return a == b; });
-        r.code[h] |= (bad ? 0 : n + (v[i] < 0.f ? 8 : 0)) << (4 * i);
+        r.code[h] |= (bad ? 0 : n + (signbit(v[i]) ? 8 : 0)) << (4 * i);
       }
       continue;
     }
@@ -262,7 +264,7 @@ __device__ __noinline__ bool quantise_exact(const T* x, const T* w, double eps, 
     if constexpr (WIDE) {
       double y = (double)Elt<T>::to_f(x[e]) * (double)unit;
       if (NORM) y = y * wide * (double)Elt<T>::to_f(w[e]);
-      negative = y < 0;
+      negative = signbit(y);
       y = fmin(fabs(y), 1e38);   // far past the largest scale
       y = Elt<T>::to_f(x[e]) - Elt<T>::to_f(x[e]) == 0.f && (!NORM || Elt<T>::to_f(w[e]) - Elt<T>::to_f(w[e]) == 0.f) &&
                   wide - wide == 0
@@ -272,7 +274,7 @@ __device__ __noinline__ bool quantise_exact(const T* x, const T* w, double eps, 
       a.l = a.h < INFINITY ? (float)(y - (double)a.h) : 0.f;
     } else {
       const float c = __fmul_rn(Elt<T>::to_f(x[e]), Elt<T>::to_f(w[e])) * unit;   // exact
-      negative = c < 0.f;
+      negative = signbit(c);
       a.h = __fmul_rn(fabsf(c), r.h);
       a.l = fmaf(fabsf(c), r.h, -a.h) + fabsf(c) * r.l;
       if (a.h < INFINITY) a = two_sum(a.h, a.l);
