@@ -283,35 +283,37 @@ def make_paged_params(cache, block_table, act_seq_kv, *, tokens, heads, layout="
 
 
 def _cache(cache, dtype, cache_scale):
-    """dtype of the rows, width of their rotated part, and the scale of a cache
-    of 4 bits (None: 16 bits)."""
-    if cache.dtype is torch.uint8:
-        if cache.dim() != 3 or cache.shape[2] not in (CODES4, CODES4 + 128):
-            raise ValueError("cache of 4 bits: expected (num_pages, page_size, 416) or (num_pages, page_size, 288)")
-        if dtype not in DTYPES:
-            raise ValueError("rows must be bfloat16 or float16")
-        return dtype, (cache.shape[2] - CODES4) // 2, 1.0 if cache_scale is None else cache_scale
-    if cache.dtype not in DTYPES:
+    """dtype of the rows, width of their rotated part, the scale of a cache of
+    4 bits (None: 16 bits), and the cache's shape."""
+    held, shape = cache.dtype, cache.shape
+    if held in DTYPES:
+        if len(shape) != 3 or shape[2] not in (512, 576):
+            raise ValueError("cache: expected (num_pages, page_size, 576) or (num_pages, page_size, 512)")
+        if cache_scale is not None:
+            raise ValueError("cache_scale given for a cache of 16 bits")
+        return held, shape[2] - 512, None, shape
+    if held is not torch.uint8:
         raise ValueError("cache must be bfloat16 or float16, or uint8 (rows of 4 bits)")
-    if cache.dim() != 3 or cache.shape[2] not in (512, 576):
-        raise ValueError("cache: expected (num_pages, page_size, 576) or (num_pages, page_size, 512)")
-    if cache_scale is not None:
-        raise ValueError("cache_scale given for a cache of 16 bits")
-    return cache.dtype, cache.shape[2] - 512, None
+    if len(shape) != 3 or shape[2] not in (CODES4, CODES4 + 128):
+        raise ValueError("cache of 4 bits: expected (num_pages, page_size, 416) or (num_pages, page_size, 288)")
+    if dtype not in DTYPES:
+        raise ValueError("rows must be bfloat16 or float16")
+    return dtype, (shape[2] - CODES4) // 2, 1.0 if cache_scale is None else cache_scale, shape
 
 
 def _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale, sparse_mode, interleaved,
            wait_limit_us, dtype=None, cache_scale=None):
     """The fields of PagedParams, the addresses of cache, block_table,
-    act_seq_q and act_seq_kv, and of a cache of 4 bits its scale."""
-    dt, dr, unit = _cache(cache, dtype, cache_scale)
+    act_seq_q and act_seq_kv, of a cache of 4 bits its scale, and the rows'
+    dtype and device."""
+    dt, dr, unit, shape = _cache(cache, dtype, cache_scale)
     if block_table.dim() != 2:
         raise ValueError("block_table: expected (B, max_pages)")
     dev = cache.get_device()
-    pages, page, _ = cache.shape
-    b, per = block_table.shape
-    at = (_need("cache", cache, cache.shape, cache.dtype, dev),
-          _need("block_table", block_table, block_table.shape, torch.int32, dev))
+    pages, page, _ = shape
+    b, per = entries = block_table.shape
+    at = (_need("cache", cache, shape, dt if unit is None else torch.uint8, dev),
+          _need("block_table", block_table, entries, torch.int32, dev))
     kva = _need("act_seq_kv", act_seq_kv, (b,), torch.int32, dev)
     lay = LAYOUTS[layout.upper()]
     qla = None
@@ -320,7 +322,7 @@ def _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q
     if lay == 0 and tokens != b * seq:
         raise ValueError(f"BSND rows of {tokens} tokens do not match {b} sequences of {seq}")
     return (lay, DTYPES[dt], b, 0 if lay else seq, tokens if lay else 0, heads, 512, dr, pages, page, per, scale,
-            sparse_mode, 1 if interleaved else 0, wait_limit_us), at + (qla, kva), unit
+            sparse_mode, 1 if interleaved else 0, wait_limit_us), at + (qla, kva), unit, dt, dev
 
 
 def _leading(name, t, layout):
@@ -348,22 +350,21 @@ def cache_append(cache, block_table, act_seq_kv, k, k_rope=None, cos_sin=None, *
     SFA_DEVERR_* code.  Returns (cache, q_rope_out)."""
     lead, tokens, seq = _leading("k", k, layout)
     heads = 1 if q_rope is None else q_rope.shape[-2]
-    p, (ca, bta, aq, akv), unit = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, 1.0, 3,
-                                         interleaved, 0, k.dtype, cache_scale)
+    p, (ca, bta, aq, akv), unit, dt, dev = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q,
+                                                  1.0, 3, interleaved, 0, k.dtype, cache_scale)
     (ka, kra, kw, cs, qra, qroa), table_len, err, q_rope_out = _new_rows(
-        cache, p[7], lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error)
+        dt, dev, p[7], lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error)
     args = (ca, bta, aq, akv, ka, kra, kw, eps, cs, table_len, qra, qroa, err)
     if unit is None:
-        _call(cache.get_device(), stream, _lib().sfa_cache_append, "sfa_cache_append", _pack_paged(*p), *args)
+        _call(dev, stream, _lib().sfa_cache_append, "sfa_cache_append", _pack_paged(*p), *args)
     else:
-        _call(cache.get_device(), stream, _lib().sfa_cache4_append, "sfa_cache4_append", _pack_paged(*p), unit, *args)
+        _call(dev, stream, _lib().sfa_cache4_append, "sfa_cache4_append", _pack_paged(*p), unit, *args)
     return cache, q_rope_out
 
 
-def _new_rows(cache, dr, lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error):
+def _new_rows(dt, dev, dr, lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error):
     """Addresses of an append's rows, its table's length and error word, and
     q_rope_out."""
-    dt, dev = k.dtype if cache.dtype is torch.uint8 else cache.dtype, cache.get_device()
     ka = _need("k", k, lead + (1, 512), dt, dev)
     kw = None if k_weight is None else _need("k_weight", k_weight, (512,), dt, dev)
     kra = cs = qra = qroa = None
@@ -395,16 +396,16 @@ def cache_append_slots(cache, slots, positions, k, k_rope=None, cos_sin=None, *,
     axis of each rotated pair), (axes, tokens).  k is (tokens, 1, 512).
     Positions are not needed for a cache without rotated rows.  Returns (cache,
     q_rope_out)."""
-    dt, dr, unit = _cache(cache, k.dtype, cache_scale)
+    dt, dr, unit, shape = _cache(cache, k.dtype, cache_scale)
     dev = cache.get_device()
     if k.dim() != 3:
         raise ValueError("k: expected (tokens, 1, 512)")
     lead, tokens = k.shape[:1], k.shape[0]
     heads = 1 if q_rope is None else q_rope.shape[-2]
-    ca = _need("cache", cache, cache.shape, cache.dtype, dev)
+    ca = _need("cache", cache, shape, cache.dtype, dev)
     sa = _need("slots", slots, (tokens,), torch.int32, dev)
     (ka, kra, kw, cs, qra, qroa), table_len, err, q_rope_out = _new_rows(
-        cache, dr, lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error)
+        dt, dev, dr, lead, heads, k, k_rope, k_weight, cos_sin, q_rope, q_rope_out, error)
     n, at, pos = 1, None, None
     if dr:
         if positions is None:
@@ -414,7 +415,7 @@ def cache_append_slots(cache, slots, positions, k, k_rope=None, cos_sin=None, *,
         pos = _need("positions", positions, (tokens,) if axes is None else (n, tokens), torch.int32, dev)
     elif axes is not None:
         raise ValueError("axes given for a cache without rope rows")
-    pages, page, _ = cache.shape
+    pages, page, _ = shape
     _call(dev, stream, _lib().sfa_cache_append_slots, "sfa_cache_append_slots",
           _pack_cache(DTYPES[dt], 16 if unit is None else 4, pages, page, dr, 0.0 if unit is None else unit),
           _pack_rows(DTYPES[dt], 1 if interleaved else 0, tokens, heads, table_len, eps), ca, sa, n, at, pos, ka, kra,
@@ -428,14 +429,14 @@ def cache_unpack(cache, dtype, *, cache_scale=None, out=None, stream=None):
     576 or 512) in dtype, which is the one its rows were appended in."""
     if cache.dtype is not torch.uint8:
         raise ValueError("cache must be uint8 (rows of 4 bits)")
-    dt, dr, unit = _cache(cache, dtype, cache_scale)
+    dt, dr, unit, held = _cache(cache, dtype, cache_scale)
     dev = cache.get_device()
-    shape = cache.shape[:2] + (512 + dr,)
+    shape = held[:2] + (512 + dr,)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=cache.device)
     _call(dev, stream, _lib().sfa_cache4_unpack, "sfa_cache4_unpack",
           _pack_cache(DTYPES[dt], 4, shape[0], shape[1], dr, unit),
-          _need("cache", cache, cache.shape, torch.uint8, dev), _need("out", out, shape, dt, dev))
+          _need("cache", cache, held, torch.uint8, dev), _need("out", out, shape, dt, dev))
     return out
 
 
@@ -504,9 +505,8 @@ def paged_fwd(q, cache, block_table, act_seq_kv, scale, *, q_rope=None, layout="
     read_device_error reads a passed workspace's error word."""
     lead, tokens, seq = _leading("q", q, layout)
     heads = q.shape[-2]
-    p, (ca, bta, aq, akv), unit = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q, scale,
-                                         sparse_mode, True, wait_limit_us, q.dtype, cache_scale)
-    dt, dev = q.dtype if unit is not None else cache.dtype, cache.get_device()
+    p, (ca, bta, aq, akv), unit, dt, dev = _paged(cache, block_table, act_seq_kv, tokens, heads, layout, seq, act_seq_q,
+                                                  scale, sparse_mode, True, wait_limit_us, q.dtype, cache_scale)
     qa = _need("q", q, lead + (heads, 512), dt, dev)
     qra = None
     if p[7]:
