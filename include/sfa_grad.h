@@ -481,8 +481,8 @@ sfa_status sfa_paged_fwd(const sfa_paged_params* p, const void* q, const void* q
  * it without a rounding to dtype before: a block's scale is max |y| / (6
  * cache_scale) and a code y / (scale * cache_scale), each rounded to the
  * nearest, ties to even, as exact arithmetic on k does it (a row close to a
- * border is rounded again from 64-bit values).  A block with a value that is
- * not finite reads back as not a number.
+ * border is rounded again in more bits, up to 64); a code has y's sign, zeros
+ * too.  A block with a value that is not finite reads back as not a number.
  * Further errors: SFA_ERR_SHAPE (cache_scale).
  */
 sfa_status sfa_cache4_append(const sfa_paged_params* p, double cache_scale, void* cache, const int32_t* block_table,
@@ -491,7 +491,13 @@ sfa_status sfa_cache4_append(const sfa_paged_params* p, double cache_scale, void
                              const void* q_rope, void* q_rope_out, int32_t* error, void* stream);
 
 /*
- * sfa_paged_fwd over such a cache, by the values that its rows stand for.
+ * sfa_paged_fwd over such a cache, by the values that its rows stand for.  With
+ * more than 512 rows of q a sequence on the mean (S1 * N1; TND: T1 * N1 / B, room
+ * that no sequence uses counted in) the workspace also holds values in 16 bits:
+ * those of the whole cache, or of a page for each entry of the block table if
+ * these are fewer.  That can be several times the cache; a call for the
+ * sequences of single tokens, apart from the one for chunks of a prompt, goes
+ * without.
  */
 sfa_status sfa_paged4_workspace_size(const sfa_paged_params* p, size_t* bytes);
 sfa_status sfa_paged4_fwd(const sfa_paged_params* p, double cache_scale, const void* q, const void* q_rope,
@@ -556,8 +562,16 @@ typedef struct sfa_plan_params {
  * act_seq_kv_out and free_count_out as they were and slots -1: lengths that
  * are negative or exceed the table, or new tokens that exceed `tokens`
  * (SFA_DEVERR_SEQLENS); more pages needed than there are, or more free and
- * returned ones than num_pages (SFA_DEVERR_POOL).  A page outside the cache
- * is handed on like any other; a token in it gets slot -1 (SFA_DEVERR_PAGE).
+ * returned ones than num_pages (SFA_DEVERR_POOL).
+ * What a request holds follows from act_seq_kv alone: the pages of its first
+ * tokens, in order.  So a length is lowered between steps (tokens of a draft
+ * taken back) within its last page only, or after the pages behind the new
+ * length have been put behind the free ones and counted in *free_count: the
+ * request would not give them back, and takes new ones in their place.  And a
+ * page that several requests name comes back from each of them when they end:
+ * the caller leaves all but one out of the free pages before the next step.
+ * A page outside the cache is handed on like any other; a token in it gets slot
+ * -1 (SFA_DEVERR_PAGE).
  * `error` (optional, device int32) receives the code and is not written
  * otherwise.  Asynchronous on `stream`; no workspace; the same call gives the
  * same result.

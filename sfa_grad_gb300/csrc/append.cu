@@ -8,10 +8,11 @@
 // has one launch ahead of its attention.  Bound by the rows' bytes, and with
 // few tokens by the latency of the lengths, the block table and the row, read
 // one after the other.  Measured, bf16: 64 single tokens x 128 heads 6.2 us;
-// 8 chunks, 13,045 tokens x 64 heads, 47.3 us, 5.2 TB/s.  Into 4 bits,
-// from cold caches, 13,045 tokens by slots with 16 heads 24.6 us, keys alone 22.5 (16
-// bits 15.3): a row close to a border takes its warp some 6 us, and a launch of
-// four waves waits for the last.
+// 8 chunks, 13,045 tokens x 64 heads, 47.3 us, 5.2 TB/s.  By slots, fp16, 13,045 tokens
+// with 16 heads from cold caches: into 4 bits 26.0 us, into 16 bits 24.1; keys alone
+// 23.3 and 15.1; from warm caches 20.6 and 17.3, keys alone 17.4 and 8.6.  Into 4 bits
+// a row close to a border takes its warp some 6 us, and a launch of four waves
+// waits for the last.
 #include <type_traits>
 
 #include "kernels.h"

@@ -20,6 +20,12 @@
 // (m, l, O) in fp32 and a second kernel merges them in order: few rows over a
 // long cache spread over all SMs, and the result does not depend on timing.
 //
+// P is rounded to the call's type, for the MMAs take both operands in one, the
+// values' (its sum l is of the fp32 weights).  The roundings are independent from key
+// to key, so the output's error in the mean square grows little by them: 0.0018
+// to 0.0019 of its size in bf16, where its own rounding gives 0.0017, in fp16
+// 0.00023 and 0.00021.
+//
 // Measured, bf16, pages of 64: 512 tokens x 128 heads over 16384 keys 1380 us
 // (1667 TFLOP/s; back to back the power limit makes it 1500 to 1525; the tensor
 // pipe is busy 74 % of the cycles, the rest is switches between the two
@@ -955,9 +961,16 @@ static int few_rows(const Paged& p, int nsm) {
 
 // Rows of 4 bits that are unpacked on the way to the MMAs cost every row tile
 // its unpacking; unpacked ahead of the call, once, and then they pass HBM in 16
-// bits.  16 sequences of 4096 keys with 128 heads: 512 rows 109 us and 107 (bf16), 100 and 107
-// (fp16), 768 rows 144 and 133, 132 and 133, 128 rows 50 and 66; one sequence of 16384
-// keys with 1024 rows 66 and 70.  Unpacking ahead also takes a workspace.
+// bits.  16 sequences of 4096 keys with 128 heads, on the way and ahead: 128 rows 40 us
+// and 55 (bf16), 39 and 58 (fp16), 512 rows 98 and 95, 91 and 100, 768 rows 132 and
+// 120, 121 and 125; one sequence of 16384 keys with 1024 rows 59 and 52, 55 and 53, with
+// 65,536 rows 2167 and 1384, 1954 and 1400.  Unpacking ahead also takes a workspace.
+//
+// The mean counts the room of the tensors (T, S1), for the lengths are the
+// device's, and one choice serves all sequences.  So a chunk of 512 tokens x 128
+// heads beside 63 single tokens of 1024 .. 8192 keys has all of them unpacked: 868 us in
+// one call, 711 and 110 in two.  The single tokens alone in tensors with that
+// much room to spare take 176 us instead of 110.
 static bool many_rows4(const Paged& p) {
   return (long long)(p.tnd ? (p.T + p.B - 1) / p.B : p.S1) * p.G > 512;
 }

@@ -13,7 +13,7 @@
 // 6.8 TB/s): 4096 tokens, keys normed, 128 query heads rotated, bf16: 24.6 us,
 // 5.9 TB/s; their gradients 32.4 us, 4.6 TB/s, with the second launch that adds
 // up the weight's; 16381 tokens x 16 normed heads, fp16, gradients: 166 us, 5.6
-// TB/s.  On three axes 4096 tokens x 128 heads, rotations alone, 22.6 us, 6.0 TB/s;
+// TB/s; forward, with their rotations, 114 us, 5.3 TB/s.  On three axes 4096 tokens x 128 heads, rotations alone, 22.7 us, 6.0 TB/s;
 // 16381 x 64, fp16, not interleaved, gradients 49.3 us, 5.6 TB/s.
 #include <type_traits>
 
@@ -32,6 +32,9 @@ constexpr int kGradBlocks = 3;
 // of 4096 x 128 heads took 41 us with two, 37 with four, 32 with eight.
 constexpr int kPieces = 8;
 
+// (By the kernel's type: where one kernel asked at run time, the normed rows of one
+// axis paid for four positions, 16381 x 16 heads 132 us instead of 115 in fp16, 227
+// instead of 192 in bf16 with halves.)
 template <bool AXES>
 __device__ __forceinline__ bool padded(const RowsArgs& a, int t) {
   if (!a.pos) return false;

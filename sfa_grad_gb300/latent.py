@@ -453,7 +453,10 @@ def page_plan(block_table, act_seq_kv, new_tokens, free_pages, free_count, *, pa
     position of each new token, `tokens` of them (-1 behind the last).
     `outputs`: such a tuple to write into, none of them an input.  `error`:
     optional int32 (1,) that receives a SFA_DEVERR_* code; a step that does not
-    fit changes nothing."""
+    fit changes nothing.  A request holds the pages of its act_seq_kv tokens: a
+    length that is lowered between steps stays within its last page, or the
+    caller returns the pages behind it; pages that requests share come back
+    from each of them."""
     if block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("expected block_table (B, max_pages) and free_pages (num_pages,)")
     b, per = block_table.shape

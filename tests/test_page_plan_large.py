@@ -89,3 +89,27 @@ def test_many_blocks_change_nothing(what):
     assert all(torch.equal(t[k], before[k]) for k in t)
     assert not bool(q.any()) and torch.equal(kv, t["act_seq_kv"]) and torch.equal(count, t["free_count"])
     assert bool((slots == -1).all()) and bool((pos == -1).all())
+
+
+@pytest.mark.gpu
+def test_a_length_lowered_between_steps():
+    """Tokens of a draft taken back: within the last page nothing else changes; past its border the caller
+    returns the pages behind, and no page is lost or held twice."""
+    page, batch = 16, 3
+    pool = Pool(batch, 8, 12, page, seed=1)
+    t = pool.tensors()
+    for new, taken in (([20, 30, 5], [0, 0, 0]), ([6, 5, 9], [3, 2, 0]), ([7, 1, 9], [6, 0, 4]), ([40, -1, 1], [38, 0, 0]),
+                       ([1, 60, 3], [0, 59, 3]), ([-1, -1, -1], [0, 0, 0])):
+        tokens = sum(max(n, 0) for n in new)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = _plan(t, new, page, tokens, error=err)
+        _same(t, got, pool.step(new), pool, tokens)
+        assert err.item() == 0
+        for b, n in enumerate(taken):
+            left = pool.kv[b] - n
+            pool.free += pool.table[b][pool.held(left):pool.held(pool.kv[b])]
+            pool.kv[b] = left
+        held = [p for b in range(batch) for p in pool.table[b][:pool.held(pool.kv[b])]]
+        assert sorted(held + pool.free) == list(range(12))
+        t = pool.tensors()
+    assert pool.kv == [0, 0, 0] and len(pool.free) == 12
