@@ -13,8 +13,9 @@
 // 6.8 TB/s): 4096 tokens, keys normed, 128 query heads rotated, bf16: 24.6 us,
 // 5.9 TB/s; their gradients 32.4 us, 4.6 TB/s, with the second launch that adds
 // up the weight's; 16381 tokens x 16 normed heads, fp16, gradients: 166 us, 5.6
-// TB/s; forward, with their rotations, 114 us, 5.3 TB/s.  On three axes 4096 tokens x 128 heads, rotations alone, 22.7 us, 6.0 TB/s;
-// 16381 x 64, fp16, not interleaved, gradients 49.3 us, 5.6 TB/s.
+// TB/s; forward, with their rotations, 114 us, 5.6 TB/s.  On three axes 4096
+// tokens x 128 heads, rotations alone, 22.7 us, 6.0 TB/s; 16381 x 64, fp16, not
+// interleaved, gradients 49.0 us, 5.6 TB/s.
 #include <type_traits>
 
 #include "kernels.h"
