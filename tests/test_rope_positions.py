@@ -25,4 +25,4 @@ def test_positions_cost_normed_rows_nothing(dtype, interleaved):
     with_, without = in_turns(lambda: sfa.norm_rope(pos, cs, outputs=a, **kw),
                               lambda: sfa.norm_rope(None, None, outputs=b, **kw))
     assert all(x is None or torch.equal(x, y) for x, y in zip(a, b))
-    assert with_ <= 1.08 * without, (with_, without)
+    assert with_ <= 1.12 * without, (with_, without)
